@@ -1,0 +1,159 @@
+// gmm_softmax.h - device helpers shared by the softmax-over-codes kernels:
+// unaligned wide loads, bf16 conversion, online softmax statistics and sorted
+// top-m lists.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+namespace gmm {
+
+constexpr int TOP_MAX = 16;  // GMM_TOP_MAX: alternatives kept per row
+// exp(d) for d <= 0 on the hardware's base-2 exponential; results below 2^-126
+// come out as 0, which no sum here can tell from themselves.
+__device__ __forceinline__ float exp_neg(float d) {
+    return __builtin_amdgcn_exp2f(d * 1.44269504088896341f);
+}
+
+// 16 bytes of a row at any element alignment (the hardware's global accesses
+// need no alignment, so rows of any stride take the same path).
+struct __attribute__((packed, aligned(2))) Raw16 {
+    uint32_t w[4];
+};
+
+__device__ __forceinline__ float bf16_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
+// round to nearest even; NaN stays a quiet NaN
+__device__ __forceinline__ uint32_t f32_to_bf16(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if (f != f) return (u >> 16) | 0x40u;
+    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+}
+
+// T = float or uint16_t (bf16 bits): VE values per 16 bytes.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int VE = 4;
+    static __device__ __forceinline__ float get(const Raw16& r, int k) {
+        return __uint_as_float(r.w[k]);
+    }
+    static __device__ __forceinline__ float one(const float* p) { return *p; }
+    static __device__ __forceinline__ void set(Raw16& r, int k, float v) {
+        r.w[k] = __float_as_uint(v);
+    }
+    static __device__ __forceinline__ float store(float v) { return v; }
+};
+template <>
+struct Vec<uint16_t> {
+    static constexpr int VE = 8;
+    static __device__ __forceinline__ float get(const Raw16& r, int k) {
+        return __uint_as_float((k & 1) ? (r.w[k >> 1] & 0xffff0000u) : (r.w[k >> 1] << 16));
+    }
+    static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(*p); }
+    static __device__ __forceinline__ void set(Raw16& r, int k, float v) {
+        const uint32_t b = f32_to_bf16(v);
+        r.w[k >> 1] = (k & 1) ? ((r.w[k >> 1] & 0xffffu) | (b << 16)) : b;
+    }
+    static __device__ __forceinline__ uint16_t store(float v) { return (uint16_t)f32_to_bf16(v); }
+};
+
+// The VE values of p[i .. i+VE), those at or past `end` as -inf.
+template <typename T>
+__device__ __forceinline__ Raw16 load_vec(const T* p, int64_t i, int64_t end) {
+    constexpr int VE = Vec<T>::VE;
+    if (i + VE <= end) return *reinterpret_cast<const Raw16*>(p + i);
+    Raw16 r = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+    for (int k = 0; k < VE; ++k)
+        Vec<T>::set(r, k, i + k < end ? Vec<T>::one(p + i + k) : -INFINITY);
+    return r;
+}
+
+// Online softmax statistics of a set of scaled logits l: m = max l (or
+// -FLT_MAX where none is above it), s = sum exp(l - m), a = sum exp(l - m)
+// (l - m). An empty set, or one of -inf only, has s = 0. A NaN or +inf leaves
+// s = NaN. m starts at the lowest finite value instead of -inf so that l - m
+// is never inf - inf for a masked l; differences are cut at -1000, where exp
+// is 0 in fp32 already, so that 0 * (l - m) stays 0.
+struct Stats {
+    float m, s, a;
+    __device__ __forceinline__ void clear() {
+        m = -3.402823466e38f;
+        s = 0.f;
+        a = 0.f;
+    }
+    // restates s and a for the larger maximum mn
+    __device__ __forceinline__ void raise(float mn) {
+        const float d = fmaxf(m - mn, -1000.f);
+        const float e = exp_neg(d);
+        a = e * fmaf(s, d, a);
+        s *= e;
+        m = mn;
+    }
+    // adds one value: d = l - m
+    __device__ __forceinline__ void add(float d) {
+        const float e = exp_neg(d);
+        s += e;
+        a = fmaf(e, fmaxf(d, -1000.f), a);
+    }
+    __device__ __forceinline__ void join(float m2, float s2, float a2) {
+        const float mn = fmaxf(m, m2);
+        Stats o{m2, s2, a2};
+        raise(mn);
+        o.raise(mn);
+        s += o.s;
+        a += o.a;
+    }
+    // over the wave's 64 lanes, in a fixed order, the same in every lane
+    __device__ __forceinline__ void wave_join() {
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            join(__shfl_xor(m, off), __shfl_xor(s, off), __shfl_xor(a, off));
+    }
+    __device__ __forceinline__ bool empty() const { return s == 0.f; }
+};
+
+// (v, i) before (v2, i2): larger value first, ties to the smaller index.
+__device__ __forceinline__ bool top_before(float v, int i, float v2, int i2) {
+    return v > v2 || (v == v2 && i < i2);
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) v = fmaxf(v, __shfl_xor(v, off));
+    return v;
+}
+
+__device__ __forceinline__ float lane_get(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// A wave's sorted list of its m best (value, index) pairs: entry j in lane j,
+// the empty entry is (-inf, INT_MAX). -inf and NaN never enter.
+struct TopList {
+    float v;
+    int i;
+    __device__ __forceinline__ void clear() {
+        v = -INFINITY;
+        i = 0x7fffffff;
+    }
+    __device__ __forceinline__ float least(int m) const { return lane_get(v, m - 1); }
+    // wave-uniform nv, ni
+    __device__ __forceinline__ void insert(float nv, int ni, int m, int lane) {
+        const uint64_t before = __builtin_amdgcn_ballot_w64(top_before(v, i, nv, ni));
+        const int pos = __popcll(before & ((uint64_t(1) << m) - 1));
+        if (pos >= m) return;
+        const float uv = __shfl_up(v, 1);
+        const int ui = __shfl_up(i, 1);
+        if (lane == pos) {
+            v = nv;
+            i = ni;
+        } else if (lane > pos) {
+            v = uv;
+            i = ui;
+        }
+    }
+};
+
+}  // namespace gmm

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -34,6 +35,12 @@ lib.gmm_kmeans_fit.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i32, _i32, _f6
 lib.gmm_ivf_workspace_bytes.argtypes = [_i64, _i32, _i32]
 lib.gmm_ivf_workspace_bytes.restype = _sz
 lib.gmm_ivf_build.argtypes = [_vp, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _sz, _vp]
+lib.gmm_logits_score_workspace_bytes.argtypes = [_i64, _i32, _i32]
+lib.gmm_logits_score_workspace_bytes.restype = _sz
+lib.gmm_logits_score.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i32, _f32, _vp, _vp, _vp, _vp,
+                                 _vp, _vp, _sz, _vp]
+lib.gmm_logits_score_backward.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
+                                          _f32, _vp, _i64, _vp]
 lib.gmm_device_status.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.restype = ctypes.c_int
@@ -44,8 +51,8 @@ lib.gmm_profile_begin.argtypes = [_i32]
 lib.gmm_profile_end.argtypes = [ctypes.POINTER(_f64), ctypes.POINTER(_i32), ctypes.POINTER(_f64),
                                 ctypes.POINTER(_i32)]
 for _f in (lib.gmm_em_step, lib.gmm_fit, lib.gmm_loglik, lib.gmm_assign_topm, lib.gmm_kmeans_step,
-           lib.gmm_kmeans_fit, lib.gmm_ivf_build, lib.gmm_device_status, lib.gmm_profile_begin,
-           lib.gmm_profile_end):
+           lib.gmm_kmeans_fit, lib.gmm_ivf_build, lib.gmm_logits_score, lib.gmm_logits_score_backward,
+           lib.gmm_device_status, lib.gmm_profile_begin, lib.gmm_profile_end):
     _f.restype = ctypes.c_int
 
 (GMM_OK, GMM_E_INVALID, GMM_E_DTYPE, GMM_E_WORKSPACE, GMM_E_PARAMS, GMM_E_HIP,
@@ -228,6 +235,114 @@ def ivf_build(idx, resp, k: int, min_resp: float = 0.0, values: bool = True):
                              _ptr(vals), _ptr(ws), nb, _stream(dev)))
     total = int(offsets[k].item())
     return offsets, rows[:total], (vals[:total] if values else None)
+
+
+TOP_MAX = 16  # GMM_TOP_MAX
+
+
+class Scores(NamedTuple):
+    """What :func:`logits_score` and :func:`head_score` return."""
+
+    logprob: Optional[torch.Tensor]  # (N,) float32, None without targets
+    entropy: torch.Tensor            # (N,) float32
+    norm: torch.Tensor               # (N, 2) float32: max l and log sum exp(l - max l)
+    top_idx: Optional[torch.Tensor]  # (N, m) int32, None when m == 0
+    top_logprob: Optional[torch.Tensor]  # (N, m) float32
+
+
+def _rows2(t, name):
+    """(dtype code, leading dimension) of a 2-D row-major device tensor."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit stride along columns")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    if t.dtype == torch.float32:
+        dt = GMM_F32
+    elif t.dtype == torch.bfloat16:
+        dt = GMM_BF16
+    else:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return dt, max(t.stride(0), t.shape[1])
+
+
+def _row(t, n, name, dtype, device):
+    """Address of a contiguous per-row vector, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous ({n},) tensor of {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the device of the rows")
+    return t.data_ptr()
+
+
+def _scratch(need, ws, device):
+    """(tensor, bytes) of a workspace: the caller's, or a new one."""
+    if need == 0:
+        raise GmmError(GMM_E_INVALID)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not ws.is_cuda or ws.device != device:
+        raise ValueError("ws must be on the device of the rows")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _score_outputs(n, m, targets, device):
+    new = torch.empty
+    f32 = torch.float32
+    return Scores(None if targets is None else new(n, dtype=f32, device=device),
+                  new(n, dtype=f32, device=device), new((n, 2), dtype=f32, device=device),
+                  new((n, m), dtype=torch.int32, device=device) if m > 0 else None,
+                  new((n, m), dtype=f32, device=device) if m > 0 else None)
+
+
+def logits_score(logits, targets=None, m: int = 0, scale: float = 1.0, ws=None) -> Scores:
+    """Log-probabilities of given codes, entropy and top-m alternatives from logits (N, V).
+
+    logits: float32 or bfloat16 with unit column stride; targets: int32 (N,),
+    negative where there is none. See gmm_logits_score in ``include/gmm_em.h``.
+    """
+    dt, ldl = _rows2(logits, "logits")
+    n, v = logits.shape
+    dev = logits.device
+    t = _row(targets, n, "targets", torch.int32, dev)
+    ws, nb = _scratch(lib.gmm_logits_score_workspace_bytes(n, v, m), ws, dev)
+    out = _score_outputs(n, m, targets, dev)
+    with torch.cuda.device(dev):
+        _check(lib.gmm_logits_score(logits.data_ptr(), n, v, ldl, dt, t, m, scale, _ptr(out[0]),
+                                    _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(out[4]),
+                                    ws.data_ptr(), nb, _stream(dev)))
+    return out
+
+
+def logits_score_backward(logits, targets, norm, entropy=None, g_logprob=None, g_entropy=None,
+                          scale: float = 1.0, out=None):
+    """Gradient of :func:`logits_score` with respect to the logits, in their type.
+
+    norm and entropy are what the forward call returned; g_logprob and
+    g_entropy float32 (N,), each None for 0. out may be the logits themselves.
+    """
+    dt, ldl = _rows2(logits, "logits")
+    n, v = logits.shape
+    dev = logits.device
+    if norm.dtype != torch.float32 or tuple(norm.shape) != (n, 2) or not norm.is_contiguous() \
+            or norm.device != dev:
+        raise ValueError("norm must be the (N, 2) float32 tensor of the forward call")
+    if out is None:
+        out = torch.empty((n, v), dtype=logits.dtype, device=dev)
+    dt2, ldo = _rows2(out, "out")
+    if dt2 != dt or out.shape != logits.shape or out.device != dev:
+        raise ValueError("out must have the shape, type and device of logits")
+    f32 = torch.float32
+    t, h, gl, gh = (_row(a, n, nm, ty, dev) for a, nm, ty in (
+        (targets, "targets", torch.int32), (entropy, "entropy", f32),
+        (g_logprob, "g_logprob", f32), (g_entropy, "g_entropy", f32)))
+    with torch.cuda.device(dev):
+        _check(lib.gmm_logits_score_backward(logits.data_ptr(), n, v, ldl, dt, t, norm.data_ptr(), h,
+                                             gl, gh, scale, out.data_ptr(), ldo, _stream(dev)))
+    return out
 
 
 def device_status(ws, device="cuda") -> int:

@@ -227,6 +227,52 @@ int gmm_kmeans_fit(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t x_d
                    double* inertia_hist_dev, int32_t* iters_done, void* workspace,
                    size_t workspace_bytes, void* stream);
 
+/* Scores of given codes under a softmax over v codes, from its logits.
+ * The log-likelihood of a learned softmax over components in place of a
+ * mixture's: with l = scale * x for row x of the logits,
+ *   norm[2r], norm[2r+1] = max l, log sum exp(l - max l)
+ *   logprob[r]  = l[t] - norm[2r] - norm[2r+1]        for t = targets[r]
+ *   entropy[r]  = -sum p log p                         with p = softmax(l)
+ *   top_idx[r][j], top_logprob[r][j], j < m: the m most probable codes, most
+ *     probable first (ties: smaller index first), and their log p.
+ * logits (device): n rows of v values with leading dimension ldl >= v (in
+ * elements; any alignment of an element), fp32 or bf16; offsets are 64-bit.
+ * targets (device, n int32, may be NULL: then logprob is not used): a
+ * negative target gives no code, its logprob is 0; one of v or more gives
+ * NaN. scale (an inverse temperature) must be finite and > 0. entropy (n floats)
+ * and norm (2n floats) may be NULL. 0 <= m <= min(v, GMM_TOP_MAX); top_idx and
+ * top_logprob (n*m, row-major) are unused when m = 0, and top_idx with the
+ * exponentials of top_logprob is what gmm_ivf_build reads.
+ * Masks: a logit of -inf (or one whose l is) has probability 0 and is never an
+ * alternative: places left over hold -1 and -inf. A row with nothing left has
+ * norm (-inf, 0), entropy 0 and logprob -inf. A row with a NaN or +inf has NaN
+ * in logprob, entropy and norm; NaN is never an alternative. Rows whose
+ * largest logit is the type's lowest finite value are ordinary rows.
+ * Sums are fp32 in a fixed order (bitwise reproducible). n may be 0; n <= 2^40,
+ * v <= 2^30. The workspace (device, 256-byte aligned) has
+ * gmm_logits_score_workspace_bytes(n, v, m) bytes (0: invalid sizes). */
+#define GMM_TOP_MAX 16
+size_t gmm_logits_score_workspace_bytes(int64_t n, int32_t v, int32_t m);
+int gmm_logits_score(const void* logits, int64_t n, int32_t v, int64_t ldl, int32_t dtype,
+                     const int32_t* targets, int32_t m, float scale, float* logprob,
+                     float* entropy, float* norm, int32_t* top_idx, float* top_logprob,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of gmm_logits_score's logprob and entropy with respect to the
+ * logits: for the gradients g_logprob and g_entropy (device, n floats each; each
+ * may be NULL: 0) that arrive at them,
+ *   dlogits[r][v] = scale * (g_logprob ([v = t] - p) - g_entropy p (log p + entropy))
+ * norm and entropy are what gmm_logits_score wrote for the same logits, targets
+ * and scale; targets may be NULL without g_logprob, entropy without g_entropy.
+ * dlogits (device, type of the logits, leading dimension lddl >= v) may be the
+ * logits themselves with the same leading dimension. Rows with nothing left get
+ * 0, rows without a target 0 from g_logprob, rows with a target of v or more or
+ * a NaN get NaN. Needs no workspace. */
+int gmm_logits_score_backward(const void* logits, int64_t n, int32_t v, int64_t ldl, int32_t dtype,
+                              const int32_t* targets, const float* norm, const float* entropy,
+                              const float* g_logprob, const float* g_entropy, float scale,
+                              void* dlogits, int64_t lddl, void* stream);
+
 /* Synchronises the stream and returns GMM_E_PARAMS if the last call that used
  * this workspace found invalid parameter values, GMM_OK otherwise, or
  * GMM_E_HIP if the synchronisation failed. */
