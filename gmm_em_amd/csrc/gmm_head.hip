@@ -1,0 +1,862 @@
+// gmm_head.hip - the scores of a head (logits x = h W^T of rows h under a code
+// matrix W) and their gradients, without the n x v matrix of logits
+// (gmm_head_score, gmm_head_score_backward, declared in include/gmm_em.h).
+//
+// Scores without alternatives: each tile of logits stays in the accumulators
+// of the product (gmm_gemm.h); its epilogue turns it into one (max, sum exp,
+// sum exp (l - max)) per row and tile, and the row's parts are joined by a
+// second kernel. With alternatives (m > 0), chunks of rows are written as
+// fp32 logits into the workspace and scored from there.
+// Gradient: the logits' tiles are computed again, and the epilogue turns them
+// into dx = scale (g_lp ([v = t] - p) - g_H p (log p + H)), written for a chunk of
+// rows in both orders (n x v and v x n), from which two more products make
+// dh = dx W and dW = dx^T h. For bf16 data dx is rounded to bf16, the type of
+// the matrix units' operands; for fp32 data it is kept in three planes like
+// the operands.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "gmm_em.h"
+#include "gmm_gemm.h"
+#include "gmm_nn.h"
+#include "gmm_softmax.h"
+
+namespace gmm {
+
+constexpr int32_t HEAD_MAX_DIM = 1 << 20;
+constexpr int32_t HEAD_MAX_CODES = 1 << 22;  // row strides of dx: 32-bit tile offsets
+constexpr int64_t HEAD_MAX_LD = (int64_t)1 << 22;
+constexpr size_t HEAD_LOGIT_BYTES = (size_t)256 << 20;  // fp32 logits of one chunk of rows
+constexpr size_t HEAD_PART_BYTES = (size_t)256 << 20;   // tile statistics of one chunk
+constexpr size_t HEAD_DX_BYTES = (size_t)1 << 30;       // dx of one chunk, both orders
+
+// ---- operand planes
+
+// Cuts a finite fp32 value into three bf16 values that add up to it exactly;
+// infinities and NaN go whole into the first.
+__device__ __forceinline__ void cut3(float x, uint16_t* p) {
+    const uint32_t u = __float_as_uint(x);
+    p[0] = (uint16_t)(u >> 16);
+    p[1] = p[2] = 0;
+    if ((u & 0x7f800000u) == 0x7f800000u) {
+        if (u & 0x007fffffu) p[0] |= 0x40;  // NaN whose payload was cut off
+        return;
+    }
+    const float r = x - __uint_as_float(u & 0xffff0000u);
+    p[1] = (uint16_t)(__float_as_uint(r) >> 16);
+    const float r2 = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+    p[2] = (uint16_t)(__float_as_uint(r2) >> 16);
+}
+
+template <typename T>
+struct Planes;
+template <>
+struct Planes<float> {
+    static constexpr int P = 3;
+    static __device__ __forceinline__ void cut(float x, uint16_t* p) { cut3(x, p); }
+};
+template <>
+struct Planes<uint16_t> {
+    static constexpr int P = 1;
+    static __device__ __forceinline__ void cut(float x, uint16_t* p) {
+        p[0] = (uint16_t)f32_to_bf16(x);
+    }
+};
+
+// out[plane][r][c] for c < kp, 0 past the d-th value; 8 values per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_planes(const T* x, int64_t rows, int d, int64_t ld, int kp,
+                                                uint16_t* out, int64_t plane) {
+    constexpr int P = Planes<T>::P;
+    const int per = kp / 8;
+    const int64_t total = rows * per;
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total;
+         j += (int64_t)gridDim.x * 256) {
+        const int64_t r = j / per;
+        const int c = (int)(j - r * per) * 8;
+        union {
+            uint16_t v[8];
+            uint4 q;
+        } o[P];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint16_t p[P];
+            Planes<T>::cut(c + k < d ? Vec<T>::one(x + r * ld + c + k) : 0.f, p);
+#pragma unroll
+            for (int q = 0; q < P; ++q) o[q].v[k] = p[q];
+        }
+#pragma unroll
+        for (int q = 0; q < P; ++q) *(uint4*)(out + q * plane + r * kp + c) = o[q].q;
+    }
+}
+
+// ---- fp16's powers of two
+
+constexpr int RANGE_BLOCKS = 256;
+
+// The exponent e for which a value with these magnitude bits, times 2^e, lies in
+// [2^14, 2^15); 0 for zero and for what is not finite.
+__device__ __forceinline__ int range_of(uint32_t bits) {
+    if (bits == 0 || bits >= 0x7f800000u) return 0;
+    int e;
+    (void)frexpf(__uint_as_float(bits), &e);  // in [2^(e-1), 2^e)
+    return 15 - e;
+}
+
+// The exponent of the largest of the blocks' magnitudes (every lane of a wave).
+__device__ __forceinline__ int range_exp(const uint32_t* part) {
+    const int lane = threadIdx.x & 63;
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < RANGE_BLOCKS / 64; ++k) {
+        const uint32_t o = part[k * 64 + lane];
+        m = m > o ? m : o;
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)m, off);
+        m = m > o ? m : o;
+    }
+    return range_of(m);
+}
+
+// Largest finite magnitude of each block's rows of bf16 values, by magnitude bits.
+__device__ __forceinline__ uint32_t rows_range(const uint16_t* x, int64_t rows, int d, int64_t ld) {
+    uint32_t m = 0;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < rows; r += RANGE_BLOCKS * 4)
+        for (int c = lane * 8; c < d; c += 512) {
+            const Raw16 v = load_vec(x + r * ld, c, (int64_t)d);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t b = __float_as_uint(Vec<uint16_t>::get(v, k)) & 0x7fffffffu;
+                if (b < 0x7f800000u && b > m) m = b;
+            }
+        }
+    return m;
+}
+
+struct RangeArgs {
+    const uint16_t *h, *w;
+    int64_t n, ldh, ldw;
+    int32_t d, v;
+    ScoreGradArgs g;
+    uint32_t* part;    // [3][RANGE_BLOCKS]: W, h, dx
+    int32_t* row_exp;  // [n]: dx's power of two for each row
+};
+
+// What dx's row can reach: |g_lp| + |g_H| max p |log p + H|, with p |log p| < 0.37.
+__device__ __forceinline__ float grad_bound(const GradRow& g) {
+    const float b = g.scale * (fabsf(g.glp) + fabsf(g.gh) * (0.375f + fabsf(g.h)));
+    return b < 3.0e38f ? b : 0.f;  // not finite: no power of two helps
+}
+
+__global__ __launch_bounds__(256) void k_head_range(RangeArgs p) {
+    __shared__ uint32_t sh[4][3];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t m[3];
+    m[0] = rows_range(p.w, p.v, p.d, p.ldw);
+    m[1] = rows_range(p.h, p.n, p.d, p.ldh);
+    m[2] = 0;
+    for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < p.n; r += RANGE_BLOCKS * 256) {
+        const uint32_t b = __float_as_uint(grad_bound(grad_row(p.g, r)));
+        p.row_exp[r] = range_of(b);
+        m[2] = m[2] > b ? m[2] : b;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t o = (uint32_t)__shfl_xor((int)m[k], off);
+            m[k] = m[k] > o ? m[k] : o;
+        }
+        if (lane == 0) sh[wave][k] = m[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        uint32_t o = 0;
+        for (int w = 0; w < 4; ++w) o = o > sh[w][threadIdx.x] ? o : sh[w][threadIdx.x];
+        p.part[threadIdx.x * RANGE_BLOCKS + blockIdx.x] = o;
+    }
+}
+
+__device__ __forceinline__ uint16_t f32_to_f16(float f) {
+    return __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+
+// ---- transposed operands
+
+// out[plane][c][r] for c < d and r < rp, 0 past the last row: 64 x 64 tiles
+// turned through LDS. bf16 values become fp16 times the power of two of `range`.
+template <typename T>
+__global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int d, int64_t ld, int rp,
+                                                  const uint32_t* range, uint16_t* out,
+                                                  int64_t plane) {
+    constexpr int P = Planes<T>::P;
+    constexpr bool F16 = std::is_same<T, uint16_t>::value;
+    __shared__ uint16_t tile[P][64][66];
+    const int ct = (d + 63) / 64;
+    const int64_t total = (int64_t)ct * (rp / 64);
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const float up = F16 ? ldexpf(1.f, range_exp(range)) : 1.f;
+    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+        const int64_t r0 = b / ct * 64;
+        const int c0 = (int)(b % ct) * 64;
+        for (int r = ty; r < 64; r += 4) {
+            uint16_t p[P];
+            const bool in = r0 + r < rows && c0 + tx < d;
+            const float y = in ? Vec<T>::one(x + (r0 + r) * ld + c0 + tx) : 0.f;
+            if (F16)
+                p[0] = f32_to_f16(y * up);
+            else
+                Planes<T>::cut(y, p);
+#pragma unroll
+            for (int q = 0; q < P; ++q) tile[q][tx][r] = p[q];
+        }
+        __syncthreads();
+        for (int c = ty; c < 64; c += 4)
+            if (c0 + c < d)
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+                    out[q * plane + (int64_t)(c0 + c) * rp + r0 + tx] = tile[q][c][tx];
+        __syncthreads();
+    }
+}
+
+// ---- epilogues
+
+// reduction over the 16 lanes that share a row of the accumulators
+template <int N>
+__device__ __forceinline__ float ror16(float v) {
+    return __uint_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x120 + N, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float max16(float v) {
+    v = fmaxf(v, ror16<8>(v));
+    v = fmaxf(v, ror16<4>(v));
+    v = fmaxf(v, ror16<2>(v));
+    return fmaxf(v, ror16<1>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+    v += ror16<8>(v);
+    v += ror16<4>(v);
+    v += ror16<2>(v);
+    return v + ror16<1>(v);
+}
+
+struct HeadArgs {
+    GemmIn in;
+    int32_t mt, nt;      // tiles
+    ScoreArgs s;         // rows of this chunk (s.n = in.m, s.v = in.n)
+    float* x;            // logits or target logits of the chunk
+    ScorePart* part;     // [rows][nt]
+    const float *norm, *entropy, *g_logprob, *g_entropy;
+    uint16_t *dx, *dxt;  // planes [rows][vp], [v][np]
+    int64_t plane_dx, plane_dxt;
+    int32_t vp, np;
+    const uint32_t* range;   // of dx over all rows
+    const int32_t* row_exp;  // of dx's rows
+};
+
+__host__ __device__ __forceinline__ ScoreGradArgs grad_args(const HeadArgs& p) {
+    ScoreGradArgs a{};
+    a.v = p.s.v;
+    a.scale = p.s.scale;
+    a.targets = p.s.targets;
+    a.norm = p.norm;
+    a.entropy = p.entropy;
+    a.g_logprob = p.g_logprob;
+    a.g_entropy = p.g_entropy;
+    return a;
+}
+
+// Statistics of each row over the tile's columns, and the targets' logits.
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
+    using G = Gemm<BM, BN, WM, WN>;
+    __shared__ __align__(16) unsigned char lds[G::LDS];
+    int tm, tn;
+    if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    G g;
+    g.template run<bf16x8>(p.in, m0, n0, lds);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave / WN, wn = wave % WN, h = lane >> 4, i = lane & 15;
+    float* sh = (float*)lds;              // [WN][BM][3]
+    int* tg = (int*)(sh + WN * BM * 3);   // [BM] targets of the rows
+    if (tid < BM) tg[tid] = p.s.targets && m0 + tid < p.in.m ? p.s.targets[m0 + tid] : -1;
+    __syncthreads();
+    const int col0 = n0 + wn * G::TN * 16 + i;
+#pragma unroll
+    for (int x = 0; x < G::TM; ++x) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = (wm * G::TM + x) * 16 + 4 * h + q;
+            const int t = tg[r];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < G::TN; ++y) {
+                const int col = col0 + y * 16;
+                if (col == t && col < p.in.n) p.x[m0 + r] = g.acc[x][y][q];
+                mx = fmaxf(mx, col < p.in.n ? g.acc[x][y][q] : -INFINITY);
+            }
+            Stats st;
+            st.clear();
+            st.m = fmaxf(st.m, max16(mx) * p.s.scale);
+#pragma unroll
+            for (int y = 0; y < G::TN; ++y)
+                if (col0 + y * 16 < p.in.n) st.add(fmaf(g.acc[x][y][q], p.s.scale, -st.m));
+            st.s = sum16(st.s);
+            st.a = sum16(st.a);
+            if (i == 0) {
+                float* o = sh + (wn * BM + r) * 3;
+                o[0] = st.m;
+                o[1] = st.s;
+                o[2] = st.a;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < BM && m0 + tid < p.in.m) {
+        Stats st{sh[tid * 3], sh[tid * 3 + 1], sh[tid * 3 + 2]};
+#pragma unroll
+        for (int w = 1; w < WN; ++w) {
+            const float* o = sh + (w * BM + tid) * 3;
+            st.join(o[0], o[1], o[2]);
+        }
+        p.part[(int64_t)(m0 + tid) * p.nt + tn] = ScorePart{st.m, st.s, st.a};
+    }
+}
+
+// One wave per row joins its tiles' statistics.
+__global__ __launch_bounds__(256) void k_head_join(HeadArgs p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= p.in.m) return;
+    Stats st;
+    st.clear();
+    for (int t = lane; t < p.nt; t += 64) {
+        const ScorePart q = p.part[row * p.nt + t];
+        st.join(q.m, q.s, q.a);
+    }
+    st.wave_join();
+    score_out(p.s, row, st, p.x[row], -INFINITY, -1, lane);
+}
+
+// fp32 logits of a chunk of rows, row stride v.
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_head_logits(HeadArgs p) {
+    using G = Gemm<BM, BN, WM, WN>;
+    __shared__ __align__(16) unsigned char lds[G::LDS];
+    int tm, tn;
+    if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    G g;
+    g.template run<bf16x8>(p.in, m0, n0, lds);
+    g.each([&](int r, int c, f32x4 v) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (m0 + r + q < p.in.m && n0 + c < p.in.n)
+                p.x[(int64_t)(m0 + r + q) * p.in.n + n0 + c] = v[q];
+    });
+}
+
+// dx of a chunk of rows, in both orders; 0 in the padding.
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
+    using G = Gemm<BM, BN, WM, WN>;
+    constexpr int P = Planes<T>::P;
+    __shared__ __align__(16) unsigned char lds[G::LDS];
+    int tm, tn;
+    if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    G g;
+    g.template run<bf16x8>(p.in, m0, n0, lds);
+    constexpr bool F16 = std::is_same<T, uint16_t>::value;
+    GradRow* rows = (GradRow*)lds;
+    float* up = (float*)(rows + BM);  // [BM] the rows' powers of two
+    const int tid = threadIdx.x;
+    const float up_all = F16 ? ldexpf(1.f, range_exp(p.range)) : 1.f;
+    if (tid < BM && m0 + tid < p.in.m) {
+        rows[tid] = grad_row(grad_args(p), m0 + tid);
+        if (F16) up[tid] = ldexpf(1.f, p.row_exp[m0 + tid]);
+    }
+    __syncthreads();
+    g.each([&](int r, int c, f32x4 v) {
+        const int col = n0 + c;
+        if (col >= p.vp) return;
+        uint16_t o[P][4], ot[P][4];  // dx, and dx for the other order
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool in = m0 + r + q < p.in.m && col < p.in.n;
+            const float y = in ? rows[r + q].at(v[q], col) : 0.f;
+            if (F16) {
+                o[0][q] = in ? f32_to_f16(y * up[r + q]) : 0;
+                ot[0][q] = f32_to_f16(y * up_all);
+            } else {
+                uint16_t cut[P];
+                Planes<T>::cut(y, cut);
+#pragma unroll
+                for (int k = 0; k < P; ++k) o[k][q] = ot[k][q] = cut[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (m0 + r + q < p.in.m)
+                    p.dx[k * p.plane_dx + (int64_t)(m0 + r + q) * p.vp + col] = o[k][q];
+            if (col < p.in.n && m0 + r < p.np)  // np is a multiple of 64: whole fours
+                *(uint2*)(p.dxt + k * p.plane_dxt + (int64_t)col * p.np + m0 + r) =
+                    uint2{(uint32_t)ot[k][0] | ((uint32_t)ot[k][1] << 16),
+                          (uint32_t)ot[k][2] | ((uint32_t)ot[k][3] << 16)};
+        }
+    });
+}
+
+struct GradOut {
+    GemmIn in;
+    int32_t mt, nt;
+    const float* add;  // sum of the earlier chunks, m x n, or null
+    float* sum;        // where the sum so far goes, or null: the result goes to out
+    void* out;
+    int64_t ldo;
+    // fp16 operands: the powers of two that they were multiplied by, a's for
+    // each row where row_exp is given
+    const uint32_t *range_a, *range_b;
+    const int32_t* row_exp;
+};
+
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
+    using G = Gemm<BM, BN, WM, WN>;
+    __shared__ __align__(16) unsigned char lds[G::LDS];
+    int tm, tn;
+    if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    constexpr bool F16 = std::is_same<T, uint16_t>::value;
+    G g;
+    g.template run<std::conditional_t<F16, f16x8, bf16x8>>(p.in, m0, n0, lds);
+    int back = 0;
+    if (F16) back = -range_exp(p.range_b) - (p.row_exp ? 0 : range_exp(p.range_a));
+    g.each([&](int r, int c, f32x4 v) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int64_t row = m0 + r + q;
+            const int col = n0 + c;
+            if (row >= p.in.m || col >= p.in.n) continue;
+            float y = v[q];
+            if (F16) y = ldexpf(y, p.row_exp ? back - p.row_exp[row] : back);
+            if (p.add) y += p.add[row * p.in.n + col];
+            if (p.sum)
+                p.sum[row * p.in.n + col] = y;
+            else
+                ((T*)p.out)[row * p.ldo + col] = Vec<T>::store(y);
+        }
+    });
+}
+
+// ---- host side
+
+static size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+static int pad(int64_t k) { return (int)((k + GK - 1) / GK * GK); }
+
+// Workgroups' tile: 256 x 256 where at least 200 of them fill the chip's 256
+// CUs, else 128 x 128.
+template <typename F>
+static void with_tile(int64_t m, int64_t n, F f) {
+    const int64_t big = ((m + 255) / 256) * ((n + 255) / 256);
+    if (big >= 200)
+        f(std::integral_constant<int, 256>());
+    else
+        f(std::integral_constant<int, 128>());
+}
+
+template <int B>
+struct Tile;
+template <>
+struct Tile<256> {
+    static constexpr int BM = 256, BN = 256, WM = 2, WN = 4;
+};
+template <>
+struct Tile<128> {
+    static constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
+};
+
+// Workspace of a head call: operands that need laying out, then the chunk's
+// scratch. Offsets in bytes; a part that is not needed takes none.
+struct HeadPlan {
+    int planes, pairs, dp, vp, np;
+    int64_t chunk;      // rows per chunk, a multiple of 256
+    bool pack_h, pack_w;
+    size_t o_w, o_h, o_x, o_part, o_wt, o_ht, o_dx, o_dxt, o_sum, o_score, o_range, o_exp, bytes;
+};
+
+static bool direct(const void* p, int32_t d, int64_t ld, int dtype) {
+    return dtype == GMM_BF16 && d % GK == 0 && ld % 8 == 0 && ld <= HEAD_MAX_LD &&
+           (uintptr_t)p % 16 == 0;
+}
+
+// pack_h, pack_w: whether hidden and weight have to be laid out (the sizing
+// entry point assumes both, so its result serves every alignment).
+static HeadPlan head_plan(int64_t n, int32_t d, int32_t v, int dtype, int32_t m, bool grad,
+                          bool pack_h, bool pack_w) {
+    HeadPlan q{};
+    q.planes = dtype == GMM_F32 ? 3 : 1;
+    q.pairs = dtype == GMM_F32 ? 6 : 1;
+    q.dp = pad(d);
+    q.vp = pad(v);
+    q.pack_h = pack_h;
+    q.pack_w = pack_w;
+    const int64_t tiles = (v + 127) / 128;
+    size_t row, most;
+    if (grad) {
+        row = (size_t)q.planes * q.vp * 4;
+        most = HEAD_DX_BYTES;
+    } else if (m > 0) {
+        row = (size_t)v * 4;
+        most = HEAD_LOGIT_BYTES;
+    } else {
+        row = (size_t)tiles * sizeof(ScorePart);
+        most = HEAD_PART_BYTES;
+    }
+    int64_t chunk = (int64_t)(most / row) / 256 * 256;
+    if (chunk < 256) chunk = 256;
+    if (chunk > ((int64_t)1 << 20)) chunk = (int64_t)1 << 20;
+    const int64_t all = (n + 255) / 256 * 256;
+    q.chunk = chunk < all ? chunk : (all > 0 ? all : 256);
+    q.np = (int)q.chunk;
+    size_t off = 0;
+    auto take = [&](size_t b) {
+        const size_t o = off;
+        off += up256(b);
+        return o;
+    };
+    const size_t c = (size_t)q.chunk, ps = (size_t)q.planes * 2;
+    q.o_w = take(pack_w ? ps * v * q.dp : 0);
+    q.o_h = take(pack_h ? ps * c * q.dp : 0);
+    q.o_x = take(grad ? 0 : (m > 0 ? c * v * 4 : c * 4));
+    q.o_part = take(!grad && m == 0 ? c * tiles * sizeof(ScorePart) : 0);
+    q.o_score = take(!grad && m > 0 ? score_plan(q.chunk, v, m).bytes + score_plan(1, v, m).bytes * 256 : 0);
+    q.o_wt = take(grad ? ps * d * q.vp : 0);
+    q.o_ht = take(grad ? ps * d * q.np : 0);
+    q.o_dx = take(grad ? ps * c * q.vp : 0);
+    q.o_dxt = take(grad ? ps * v * q.np : 0);
+    q.o_sum = take(grad && q.chunk < n ? (size_t)v * d * 4 : 0);
+    const bool f16 = grad && dtype == GMM_BF16;
+    q.o_range = take(f16 ? 3 * RANGE_BLOCKS * sizeof(uint32_t) : 0);
+    q.o_exp = take(f16 ? (size_t)n * sizeof(int32_t) : 0);
+    q.bytes = off < 256 ? 256 : off;
+    return q;
+}
+
+static bool head_shape_ok(int64_t n, int32_t d, int32_t v) {
+    return n >= 0 && n <= SC_MAX_ROWS && d >= 1 && v >= 1;
+}
+static bool head_supported(int32_t d, int32_t v) { return d <= HEAD_MAX_DIM && v <= HEAD_MAX_CODES; }
+
+template <typename T>
+static void planes(const void* x, int64_t rows, int d, int64_t ld, int kp, void* out, int64_t plane,
+                   hipStream_t st) {
+    const int64_t work = (rows * (kp / 8) + 255) / 256;
+    const unsigned grid = (unsigned)(work < 65536 ? work : 65536);
+    if (grid)
+        hipLaunchKernelGGL((k_planes<T>), dim3(grid), dim3(256), 0, st, (const T*)x, rows, d, ld, kp,
+                           (uint16_t*)out, plane);
+}
+template <typename T>
+static void planes_t(const void* x, int64_t rows, int d, int64_t ld, int rp, const uint32_t* range,
+                     void* out, int64_t plane, hipStream_t st) {
+    const int64_t work = (int64_t)((d + 63) / 64) * (rp / 64);
+    const unsigned grid = (unsigned)(work < 65536 ? work : 65536);
+    hipLaunchKernelGGL((k_planes_t<T>), dim3(grid), dim3(256), 0, st, (const T*)x, rows, d, ld, rp,
+                       range, (uint16_t*)out, plane);
+}
+
+static unsigned tile_grid(int mt, int nt) {
+    return (unsigned)(((int64_t)mt * nt + 7) / 8 * 8);
+}
+
+template <int B, typename K, typename A>
+static void launch_tiles(K kernel, A& a, hipStream_t st) {
+    using C = Tile<B>;
+    a.mt = (a.in.m + C::BM - 1) / C::BM;
+    a.nt = (a.in.n + C::BN - 1) / C::BN;
+    hipLaunchKernelGGL(kernel, dim3(tile_grid(a.mt, a.nt)), dim3(64 * C::WM * C::WN), 0, st, a);
+}
+
+struct HeadIn {
+    const void *h, *w;
+    int64_t n, ldh, ldw;
+    int32_t d, v, dtype;
+};
+
+// Lays out W once, then per chunk of rows fills a.in for the logits' product.
+template <typename T>
+static void head_weight(const HeadIn& x, const HeadPlan& q, char* ws, GemmIn* g, hipStream_t st) {
+    g->pairs = q.pairs;
+    g->kp = q.dp;
+    g->n = x.v;
+    if (q.pack_w) {
+        g->b = (const uint16_t*)(ws + q.o_w);
+        g->ldb = q.dp;
+        g->plane_b = (int64_t)x.v * q.dp;
+        planes<T>(x.w, x.v, x.d, x.ldw, q.dp, ws + q.o_w, g->plane_b, st);
+    } else {
+        g->b = (const uint16_t*)x.w;
+        g->ldb = x.ldw;
+    }
+}
+template <typename T>
+static void head_rows(const HeadIn& x, const HeadPlan& q, char* ws, int64_t r0, int64_t rows, GemmIn* g,
+                      hipStream_t st) {
+    const T* h = (const T*)x.h + r0 * x.ldh;
+    g->m = (int32_t)rows;
+    if (q.pack_h) {
+        g->a = (const uint16_t*)(ws + q.o_h);
+        g->lda = q.dp;
+        g->plane_a = q.chunk * q.dp;
+        planes<T>(h, rows, x.d, x.ldh, q.dp, ws + q.o_h, g->plane_a, st);
+    } else {
+        g->a = (const uint16_t*)h;
+        g->lda = x.ldh;
+    }
+}
+
+template <typename T>
+static hipError_t head_score(const HeadIn& x, const HeadPlan& q, ScoreArgs s, char* ws,
+                             hipStream_t st) {
+    HeadArgs a{};
+    head_weight<T>(x, q, ws, &a.in, st);
+    a.x = (float*)(ws + q.o_x);
+    a.part = (ScorePart*)(ws + q.o_part);
+    for (int64_t r0 = 0; r0 < x.n; r0 += q.chunk) {
+        const int64_t rows = x.n - r0 < q.chunk ? x.n - r0 : q.chunk;
+        head_rows<T>(x, q, ws, r0, rows, &a.in, st);
+        a.s = s;
+        a.s.n = rows;
+        if (s.targets) {
+            a.s.targets = s.targets + r0;
+            a.s.logprob = s.logprob + r0;
+        }
+        if (s.entropy) a.s.entropy = s.entropy + r0;
+        if (s.norm) a.s.norm = s.norm + 2 * r0;
+        if (s.m > 0) {
+            a.s.top_idx = s.top_idx + r0 * s.m;
+            a.s.top_logprob = s.top_logprob + r0 * s.m;
+        }
+        with_tile(rows, x.v, [&](auto b) {
+            constexpr int B = decltype(b)::value;
+            using C = Tile<B>;
+            if (s.m > 0)
+                launch_tiles<B>(k_head_logits<C::BM, C::BN, C::WM, C::WN>, a, st);
+            else
+                launch_tiles<B>(k_head_stats<C::BM, C::BN, C::WM, C::WN>, a, st);
+        });
+        if (s.m > 0) {
+            ScoreArgs l = a.s;
+            l.x = a.x;
+            l.ldl = x.v;
+            const hipError_t e = launch_score(l, GMM_F32, ws + q.o_score, st);
+            if (e != hipSuccess) return e;
+        } else {
+            hipLaunchKernelGGL(k_head_join, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
+        }
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void* dh, int64_t lddh,
+                            void* dw, int64_t lddw, char* ws, hipStream_t st) {
+    head_weight<T>(x, q, ws, &a.in, st);
+    const int64_t plane_wt = (int64_t)x.d * q.vp, plane_ht = (int64_t)x.d * q.np;
+    uint16_t* wt = (uint16_t*)(ws + q.o_wt);
+    uint16_t* ht = (uint16_t*)(ws + q.o_ht);
+    uint32_t* range = (uint32_t*)(ws + q.o_range);  // W, h, dx
+    int32_t* row_exp = (int32_t*)(ws + q.o_exp);
+    if (std::is_same<T, uint16_t>::value) {
+        RangeArgs r{};
+        r.h = (const uint16_t*)x.h;
+        r.w = (const uint16_t*)x.w;
+        r.n = x.n;
+        r.ldh = x.ldh;
+        r.ldw = x.ldw;
+        r.d = x.d;
+        r.v = x.v;
+        r.g = grad_args(a);
+        r.part = range;
+        r.row_exp = row_exp;
+        hipLaunchKernelGGL(k_head_range, dim3(RANGE_BLOCKS), dim3(256), 0, st, r);
+    }
+    if (dh) planes_t<T>(x.w, x.v, x.d, x.ldw, q.vp, range, wt, plane_wt, st);
+    a.range = range + 2 * RANGE_BLOCKS;
+    a.dx = (uint16_t*)(ws + q.o_dx);
+    a.dxt = (uint16_t*)(ws + q.o_dxt);
+    a.plane_dx = q.chunk * q.vp;
+    a.vp = q.vp;
+    const HeadArgs all = a;
+    for (int64_t r0 = 0; r0 < x.n; r0 += q.chunk) {
+        const int64_t rows = x.n - r0 < q.chunk ? x.n - r0 : q.chunk;
+        head_rows<T>(x, q, ws, r0, rows, &a.in, st);
+        a.np = pad(rows);
+        a.row_exp = row_exp + r0;
+        a.plane_dxt = (int64_t)x.v * a.np;
+        a.s.targets = all.s.targets ? all.s.targets + r0 : nullptr;
+        a.norm = all.norm + 2 * r0;
+        a.entropy = all.entropy ? all.entropy + r0 : nullptr;
+        a.g_logprob = all.g_logprob ? all.g_logprob + r0 : nullptr;
+        a.g_entropy = all.g_entropy ? all.g_entropy + r0 : nullptr;
+        with_tile(rows, x.v, [&](auto b) {
+            constexpr int B = decltype(b)::value;
+            using C = Tile<B>;
+            launch_tiles<B>(k_head_dx<T, C::BM, C::BN, C::WM, C::WN>, a, st);
+        });
+        if (dh) {
+            GradOut o{};
+            o.in = GemmIn{a.dx, wt, q.vp, q.vp, a.plane_dx, plane_wt, (int32_t)rows, x.d, q.vp,
+                          q.pairs};
+            o.out = (T*)dh + r0 * lddh;
+            o.ldo = lddh;
+            o.range_b = range;
+            o.row_exp = row_exp + r0;
+            with_tile(rows, x.d, [&](auto b) {
+                constexpr int B = decltype(b)::value;
+                using C = Tile<B>;
+                launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, st);
+            });
+        }
+        if (dw) {
+            planes_t<T>((const T*)x.h + r0 * x.ldh, rows, x.d, x.ldh, a.np,
+                        range + RANGE_BLOCKS, ht, plane_ht, st);
+            GradOut o{};
+            o.in = GemmIn{a.dxt, ht, a.np, a.np, a.plane_dxt, plane_ht, x.v, x.d, a.np, q.pairs};
+            float* sum = (float*)(ws + q.o_sum);
+            o.add = r0 > 0 ? sum : nullptr;
+            o.sum = r0 + q.chunk < x.n ? sum : nullptr;
+            o.out = dw;
+            o.ldo = lddw;
+            o.range_a = range + 2 * RANGE_BLOCKS;
+            o.range_b = range + RANGE_BLOCKS;
+            with_tile(x.v, x.d, [&](auto b) {
+                constexpr int B = decltype(b)::value;
+                using C = Tile<B>;
+                launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, st);
+            });
+        }
+    }
+    return hipGetLastError();
+}
+
+// dw of no rows is 0
+template <typename T>
+__global__ __launch_bounds__(256) void k_head_zero(T* out, int64_t rows, int d, int64_t ld) {
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < rows * d;
+         j += (int64_t)gridDim.x * 256)
+        out[j / d * ld + j % d] = 0;
+}
+
+}  // namespace gmm
+
+using namespace gmm;
+
+extern "C" {
+
+size_t gmm_head_score_workspace_bytes(int64_t n, int32_t d, int32_t v, int32_t dtype, int32_t m) {
+    if (!head_shape_ok(n, d, v) || !head_supported(d, v) || m < 0 || m > TOP_MAX || m > v) return 0;
+    if (dtype != GMM_F32 && dtype != GMM_BF16) return 0;
+    return head_plan(n, d, v, dtype, m, false, true, true).bytes;
+}
+
+size_t gmm_head_score_backward_workspace_bytes(int64_t n, int32_t d, int32_t v, int32_t dtype) {
+    if (!head_shape_ok(n, d, v) || !head_supported(d, v)) return 0;
+    if (dtype != GMM_F32 && dtype != GMM_BF16) return 0;
+    return head_plan(n, d, v, dtype, 0, true, true, true).bytes;
+}
+
+int gmm_head_score(const void* hidden, int64_t n, int32_t d, int64_t ldh, const void* weight,
+                   int32_t v, int64_t ldw, int32_t dtype, const int32_t* targets, int32_t m,
+                   float scale, float* logprob, float* entropy, float* norm, int32_t* top_idx,
+                   float* top_logprob, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dtype != GMM_F32 && dtype != GMM_BF16) return GMM_E_DTYPE;
+    if (!head_shape_ok(n, d, v) || ldh < d || ldw < d || m < 0 || m > TOP_MAX || m > v ||
+        !scale_ok(scale))
+        return GMM_E_INVALID;
+    if (!head_supported(d, v)) return GMM_E_UNSUPPORTED;
+    if (n > 0 && (!hidden || !weight || (targets && !logprob) ||
+                  (m > 0 && (!top_idx || !top_logprob))))
+        return GMM_E_INVALID;
+    const bool ph = !direct(hidden, d, ldh, dtype), pw = !direct(weight, d, ldw, dtype);
+    const HeadPlan q = head_plan(n, d, v, dtype, m, false, ph, pw);
+    if (!workspace || workspace_bytes < q.bytes || (uintptr_t)workspace % 256 != 0)
+        return GMM_E_WORKSPACE;
+    if (n == 0) return GMM_OK;
+    const HeadIn x{hidden, weight, n, ldh, ldw, d, v, dtype};
+    ScoreArgs s{};
+    s.v = v;
+    s.m = m;
+    s.scale = scale;
+    s.targets = targets;
+    s.logprob = logprob;
+    s.entropy = entropy;
+    s.norm = norm;
+    s.top_idx = top_idx;
+    s.top_logprob = top_logprob;
+    const hipError_t e =
+        dtype == GMM_F32 ? head_score<float>(x, q, s, (char*)workspace, (hipStream_t)stream)
+                         : head_score<uint16_t>(x, q, s, (char*)workspace, (hipStream_t)stream);
+    return e == hipSuccess ? GMM_OK : GMM_E_HIP;
+}
+
+int gmm_head_score_backward(const void* hidden, int64_t n, int32_t d, int64_t ldh,
+                            const void* weight, int32_t v, int64_t ldw, int32_t dtype,
+                            const int32_t* targets, const float* norm, const float* entropy,
+                            const float* g_logprob, const float* g_entropy, float scale,
+                            void* d_hidden, int64_t lddh, void* d_weight, int64_t lddw,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    if (dtype != GMM_F32 && dtype != GMM_BF16) return GMM_E_DTYPE;
+    if (!head_shape_ok(n, d, v) || ldh < d || ldw < d || !scale_ok(scale)) return GMM_E_INVALID;
+    if ((d_hidden && lddh < d) || (d_weight && lddw < d) || (!d_hidden && !d_weight))
+        return GMM_E_INVALID;
+    if (!head_supported(d, v)) return GMM_E_UNSUPPORTED;
+    if (n > 0 && (!hidden || !weight || !norm || (g_logprob && !targets) || (g_entropy && !entropy)))
+        return GMM_E_INVALID;
+    const bool ph = !direct(hidden, d, ldh, dtype), pw = !direct(weight, d, ldw, dtype);
+    const HeadPlan q = head_plan(n, d, v, dtype, 0, true, ph, pw);
+    if (!workspace || workspace_bytes < q.bytes || (uintptr_t)workspace % 256 != 0)
+        return GMM_E_WORKSPACE;
+    hipStream_t st = (hipStream_t)stream;
+    if (n == 0) {
+        if (d_weight) {
+            const int64_t work = ((int64_t)v * d + 255) / 256;
+            const dim3 grid((unsigned)(work < 4096 ? work : 4096));
+            if (dtype == GMM_F32)
+                hipLaunchKernelGGL((k_head_zero<float>), grid, dim3(256), 0, st, (float*)d_weight,
+                                   (int64_t)v, d, lddw);
+            else
+                hipLaunchKernelGGL((k_head_zero<uint16_t>), grid, dim3(256), 0, st,
+                                   (uint16_t*)d_weight, (int64_t)v, d, lddw);
+        }
+        return hipGetLastError() == hipSuccess ? GMM_OK : GMM_E_HIP;
+    }
+    const HeadIn x{hidden, weight, n, ldh, ldw, d, v, dtype};
+    HeadArgs a{};
+    a.s.targets = targets;
+    a.s.scale = scale;
+    a.s.v = v;
+    a.norm = norm;
+    a.entropy = entropy;
+    a.g_logprob = g_logprob;
+    a.g_entropy = g_entropy;
+    const hipError_t e = dtype == GMM_F32
+                             ? head_grad<float>(x, q, a, d_hidden, lddh, d_weight, lddw,
+                                                (char*)workspace, st)
+                             : head_grad<uint16_t>(x, q, a, d_hidden, lddh, d_weight, lddw,
+                                                   (char*)workspace, st);
+    return e == hipSuccess ? GMM_OK : GMM_E_HIP;
+}
+
+}  // extern "C"

@@ -18,7 +18,10 @@ inline bool score_shape_ok(int64_t n, int32_t v) {
     return n >= 0 && n <= SC_MAX_ROWS && v >= 1 && v <= SC_MAX_CODES;
 }
 
-struct ScorePart;
+// Softmax statistics of a part of a row, handed from one kernel to the next.
+struct ScorePart {
+    float m, s, a;
+};
 
 struct ScoreArgs {
     const void* x;
@@ -33,6 +36,35 @@ struct ScoreArgs {
     float* part_v;
     int32_t* part_i;
 };
+
+// Writes a row's results from its statistics and its target's logit xt
+// (thread 0) and its sorted alternatives (thread j < m holds entry j).
+__device__ __forceinline__ void score_out(const ScoreArgs& p, int64_t row, const Stats& st, float xt,
+                                          float tv, int ti, int tid) {
+    const bool none = st.empty();
+    const float logs = none ? 0.f : logf(st.s);
+    if (tid == 0) {
+        if (p.norm) {
+            p.norm[2 * row] = none ? -INFINITY : (st.s == st.s ? st.m : NAN);
+            p.norm[2 * row + 1] = logs;
+        }
+        if (p.entropy) p.entropy[row] = none ? 0.f : logs - st.a / st.s;
+        if (p.targets) {
+            const int t = p.targets[row];
+            float lp = 0.f;  // no code given
+            if (t >= p.v)
+                lp = NAN;
+            else if (t >= 0)
+                lp = none ? -INFINITY : fmaf(xt, p.scale, -st.m) - logs;
+            p.logprob[row] = lp;
+        }
+    }
+    if (tid < p.m) {
+        const bool there = tv > -INFINITY;
+        p.top_idx[row * p.m + tid] = there ? ti : -1;
+        p.top_logprob[row * p.m + tid] = there ? (tv - st.m) - logs : -INFINITY;
+    }
+}
 
 struct ScorePlan {
     int32_t parts, part_len;

@@ -29,41 +29,12 @@ namespace gmm {
 // Threads per row; vectors of 16 bytes in flight per thread.
 constexpr int SC_U = 4;
 
-// A row's part as it is handed from k_score to k_score_join.
-struct ScorePart {
-    float m, s, a;
-};
-
-// Writes a row's results from its statistics (thread 0) and its sorted
-// alternatives (thread j < m holds entry j).
+// The logit of the row's target (thread 0; where there is none, unused).
 template <typename T>
-__device__ __forceinline__ void score_out(const ScoreArgs& p, int64_t row, const Stats& st, float tv,
-                                          int ti, int tid) {
-    const bool none = st.empty();
-    const float logs = none ? 0.f : logf(st.s);
-    if (tid == 0) {
-        if (p.norm) {
-            p.norm[2 * row] = none ? -INFINITY : (st.s == st.s ? st.m : NAN);
-            p.norm[2 * row + 1] = logs;
-        }
-        if (p.entropy) p.entropy[row] = none ? 0.f : logs - st.a / st.s;
-        if (p.targets) {
-            const int t = p.targets[row];
-            float lp = 0.f;  // no code given
-            if (t >= p.v) {
-                lp = NAN;
-            } else if (t >= 0) {
-                const float x = Vec<T>::one((const T*)p.x + row * p.ldl + t);
-                lp = none ? -INFINITY : fmaf(x, p.scale, -st.m) - logs;
-            }
-            p.logprob[row] = lp;
-        }
-    }
-    if (tid < p.m) {
-        const bool there = tv > -INFINITY;
-        p.top_idx[row * p.m + tid] = there ? ti : -1;
-        p.top_logprob[row * p.m + tid] = there ? (tv - st.m) - logs : -INFINITY;
-    }
+__device__ __forceinline__ float target_logit(const ScoreArgs& p, int64_t row, int tid) {
+    if (tid != 0 || !p.targets) return 0.f;
+    const int t = p.targets[row];
+    return t >= 0 && t < p.v ? Vec<T>::one((const T*)p.x + row * p.ldl + t) : 0.f;
 }
 
 // cnt sorted-or-not candidates (cv, ci) in LDS; the thread holding candidate c
@@ -178,7 +149,7 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
             }
         }
         if (p.parts == 1) {
-            score_out<T>(p, row, st, top.v, top.i, tid);
+            score_out(p, row, st, target_logit<T>(p, row, tid), top.v, top.i, tid);
         } else {
             if (tid == 0) p.part[item] = ScorePart{st.m, st.s, st.a};
             if (TOP && tid < p.m) {
@@ -216,7 +187,8 @@ __global__ __launch_bounds__(64) void k_score_join(ScoreArgs p) {
         __syncthreads();
         top_rank(sv, si, cnt, p.m, ov, oi, lane, 64);
         __syncthreads();
-        score_out<T>(p, row, st, ov[lane & (TOP_MAX - 1)], oi[lane & (TOP_MAX - 1)], lane);
+        score_out(p, row, st, target_logit<T>(p, row, lane), ov[lane & (TOP_MAX - 1)],
+                  oi[lane & (TOP_MAX - 1)], lane);
         __syncthreads();
     }
 }

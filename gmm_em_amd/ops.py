@@ -41,6 +41,14 @@ lib.gmm_logits_score.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i32, _f32, _
                                  _vp, _vp, _sz, _vp]
 lib.gmm_logits_score_backward.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
                                           _f32, _vp, _i64, _vp]
+lib.gmm_head_score_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32]
+lib.gmm_head_score_workspace_bytes.restype = _sz
+lib.gmm_head_score.argtypes = [_vp, _i64, _i32, _i64, _vp, _i32, _i64, _i32, _vp, _i32, _f32, _vp,
+                               _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+lib.gmm_head_score_backward_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32]
+lib.gmm_head_score_backward_workspace_bytes.restype = _sz
+lib.gmm_head_score_backward.argtypes = [_vp, _i64, _i32, _i64, _vp, _i32, _i64, _i32, _vp, _vp, _vp,
+                                        _vp, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
 lib.gmm_device_status.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.restype = ctypes.c_int
@@ -52,7 +60,7 @@ lib.gmm_profile_end.argtypes = [ctypes.POINTER(_f64), ctypes.POINTER(_i32), ctyp
                                 ctypes.POINTER(_i32)]
 for _f in (lib.gmm_em_step, lib.gmm_fit, lib.gmm_loglik, lib.gmm_assign_topm, lib.gmm_kmeans_step,
            lib.gmm_kmeans_fit, lib.gmm_ivf_build, lib.gmm_logits_score, lib.gmm_logits_score_backward,
-           lib.gmm_device_status, lib.gmm_profile_begin, lib.gmm_profile_end):
+           lib.gmm_head_score, lib.gmm_head_score_backward, lib.gmm_device_status, lib.gmm_profile_begin, lib.gmm_profile_end):
     _f.restype = ctypes.c_int
 
 (GMM_OK, GMM_E_INVALID, GMM_E_DTYPE, GMM_E_WORKSPACE, GMM_E_PARAMS, GMM_E_HIP,
@@ -278,6 +286,12 @@ def _row(t, n, name, dtype, device):
     return t.data_ptr()
 
 
+def _norm(norm, n, device):
+    if norm.dtype != torch.float32 or tuple(norm.shape) != (n, 2) or not norm.is_contiguous() \
+            or norm.device != device:
+        raise ValueError("norm must be the (N, 2) float32 tensor of the forward call")
+
+
 def _scratch(need, ws, device):
     """(tensor, bytes) of a workspace: the caller's, or a new one."""
     if need == 0:
@@ -327,9 +341,7 @@ def logits_score_backward(logits, targets, norm, entropy=None, g_logprob=None, g
     dt, ldl = _rows2(logits, "logits")
     n, v = logits.shape
     dev = logits.device
-    if norm.dtype != torch.float32 or tuple(norm.shape) != (n, 2) or not norm.is_contiguous() \
-            or norm.device != dev:
-        raise ValueError("norm must be the (N, 2) float32 tensor of the forward call")
+    _norm(norm, n, dev)
     if out is None:
         out = torch.empty((n, v), dtype=logits.dtype, device=dev)
     dt2, ldo = _rows2(out, "out")
@@ -343,6 +355,54 @@ def logits_score_backward(logits, targets, norm, entropy=None, g_logprob=None, g
         _check(lib.gmm_logits_score_backward(logits.data_ptr(), n, v, ldl, dt, t, norm.data_ptr(), h,
                                              gl, gh, scale, out.data_ptr(), ldo, _stream(dev)))
     return out
+
+
+def _head(hidden, weight):
+    dt, ldh = _rows2(hidden, "hidden")
+    dt2, ldw = _rows2(weight, "weight")
+    if dt != dt2 or hidden.shape[1] != weight.shape[1] or hidden.device != weight.device:
+        raise ValueError("hidden (N, D) and weight (V, D) must agree in D, type and device")
+    return dt, ldh, ldw, hidden.shape[0], hidden.shape[1], weight.shape[0], hidden.device
+
+
+def head_score(hidden, weight, targets=None, m: int = 0, scale: float = 1.0, ws=None) -> Scores:
+    """:func:`logits_score` of hidden (N, D) @ weight (V, D).T, without the (N, V) logits.
+
+    float32 or bfloat16, both the same, rows of any stride. See gmm_head_score
+    in ``include/gmm_em.h``.
+    """
+    dt, ldh, ldw, n, d, v, dev = _head(hidden, weight)
+    t = _row(targets, n, "targets", torch.int32, dev)
+    ws, nb = _scratch(lib.gmm_head_score_workspace_bytes(n, d, v, dt, m), ws, dev)
+    out = _score_outputs(n, m, targets, dev)
+    with torch.cuda.device(dev):
+        _check(lib.gmm_head_score(hidden.data_ptr(), n, d, ldh, weight.data_ptr(), v, ldw, dt, t, m,
+                                  scale, _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]),
+                                  _ptr(out[4]), ws.data_ptr(), nb, _stream(dev)))
+    return out
+
+
+def head_score_backward(hidden, weight, targets, norm, entropy=None, g_logprob=None, g_entropy=None,
+                        scale: float = 1.0, ws=None):
+    """Gradients (d_hidden, d_weight) of :func:`head_score`, in the operands' type.
+
+    norm and entropy are what the forward call returned; g_logprob and
+    g_entropy float32 (N,), each None for 0.
+    """
+    dt, ldh, ldw, n, d, v, dev = _head(hidden, weight)
+    _norm(norm, n, dev)
+    f32 = torch.float32
+    t, h, gl, gh = (_row(a, n, nm, ty, dev) for a, nm, ty in (
+        (targets, "targets", torch.int32), (entropy, "entropy", f32),
+        (g_logprob, "g_logprob", f32), (g_entropy, "g_entropy", f32)))
+    ws, nb = _scratch(lib.gmm_head_score_backward_workspace_bytes(n, d, v, dt), ws, dev)
+    dh = torch.empty((n, d), dtype=hidden.dtype, device=dev)
+    dw = torch.empty((v, d), dtype=weight.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.gmm_head_score_backward(hidden.data_ptr(), n, d, ldh, weight.data_ptr(), v, ldw, dt,
+                                           t, norm.data_ptr(), h, gl, gh, scale, dh.data_ptr(), d,
+                                           dw.data_ptr(), d, ws.data_ptr(), nb, _stream(dev)))
+    return dh, dw
 
 
 def device_status(ws, device="cuda") -> int:

@@ -273,6 +273,41 @@ int gmm_logits_score_backward(const void* logits, int64_t n, int32_t v, int64_t 
                               const float* g_logprob, const float* g_entropy, float scale,
                               void* dlogits, int64_t lddl, void* stream);
 
+/* gmm_logits_score fused with the product that makes the logits: x = h W^T for
+ * n rows h of d values (hidden, leading dimension ldh >= d) and the codes' v rows
+ * of d values (weight, ldw >= d), both fp32 or both bf16 (device, any alignment
+ * of an element). targets, m, scale and the outputs are gmm_logits_score's; the
+ * n x v matrix of logits is not formed when m = 0, and a chunk of rows at a
+ * time lies in the workspace as fp32 when m > 0. bf16 products are exact and
+ * added in fp32; fp32 operands are cut into three bf16 planes and multiplied to
+ * 2^-24 of each product, so both types give fp32 logits. A row of h or W with an
+ * infinity or NaN gives NaN to what depends on it. 1 <= d <= 2^20,
+ * v <= 2^22 (GMM_E_UNSUPPORTED beyond). The workspace (device, 256-byte aligned)
+ * has gmm_head_score_workspace_bytes bytes (0: invalid or unsupported sizes); it
+ * is bounded in n. Rows of bf16 that are 16-byte aligned with d a multiple of 64
+ * are read in place, others are laid out in the workspace first. */
+size_t gmm_head_score_workspace_bytes(int64_t n, int32_t d, int32_t v, int32_t dtype, int32_t m);
+int gmm_head_score(const void* hidden, int64_t n, int32_t d, int64_t ldh, const void* weight,
+                   int32_t v, int64_t ldw, int32_t dtype, const int32_t* targets, int32_t m,
+                   float scale, float* logprob, float* entropy, float* norm, int32_t* top_idx,
+                   float* top_logprob, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of gmm_head_score's logprob and entropy with respect to hidden and
+ * weight: with dx of gmm_logits_score_backward for the same arguments,
+ *   d_hidden = dx W (n x d),   d_weight = dx^T h (v x d),
+ * in the operands' type, rounded once from fp32 sums (leading dimensions lddh,
+ * lddw >= d). Either may be NULL (not computed), not both. They must not overlap
+ * hidden or weight. dx is computed a chunk of rows at a time into the
+ * workspace: in bf16 for bf16 operands, exactly for fp32. n = 0 sets d_weight to
+ * 0. Sizes as for gmm_head_score. */
+size_t gmm_head_score_backward_workspace_bytes(int64_t n, int32_t d, int32_t v, int32_t dtype);
+int gmm_head_score_backward(const void* hidden, int64_t n, int32_t d, int64_t ldh,
+                            const void* weight, int32_t v, int64_t ldw, int32_t dtype,
+                            const int32_t* targets, const float* norm, const float* entropy,
+                            const float* g_logprob, const float* g_entropy, float scale,
+                            void* d_hidden, int64_t lddh, void* d_weight, int64_t lddw,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises the stream and returns GMM_E_PARAMS if the last call that used
  * this workspace found invalid parameter values, GMM_OK otherwise, or
  * GMM_E_HIP if the synchronisation failed. */
