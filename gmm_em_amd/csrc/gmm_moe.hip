@@ -1,0 +1,455 @@
+// gmm_moe.hip - a mixture-of-experts layer for a few rows (gmm_moe_layer,
+// declared in include/gmm_em.h):
+//   z = x G^T; the m experts of largest z (ties: smaller index) with their
+//   softmax shares r_j;  y = sum_j r_j W_out[e_j] (silu(a_j) * b_j),
+//   [a_j; b_j] = W_in[e_j] x.
+//
+// With few rows the layer is the reading of the weights of the experts that
+// some row picked: every weight is read once per 64 rows that need it, straight
+// into registers in the operand order of the matrix units (16 weight rows by
+// 16 rows of x), which then cost nothing beside the reads, also for one row.
+//   k_moe_route: a workgroup per row: z, the choice, the shares.
+//   k_moe_in:    (expert, 16 features of a and of b): the contracted axis is
+//                split over the waves and joined in LDS; silu(a) b goes to the
+//                workspace, as two bf16 parts for bf16 data (16 bits of it).
+//   k_moe_out:   (expert, 16 features of y): as before; r_j times it goes to
+//                the workspace.
+//   k_moe_join:  y = the sum over j in order, rounded once.
+// Every sum is fp32 in a fixed order.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "gmm_em.h"
+#include "gmm_gemm.h"
+#include "gmm_nn.h"
+#include "gmm_softmax.h"
+
+namespace gmm {
+
+constexpr int MOE_MAX_EXPERTS = 4096;    // gate logits of a row in LDS
+constexpr int64_t MOE_MAX_PAIRS = 1 << 20;  // (row, pick) pairs per call
+constexpr int32_t MOE_MAX_DIM = 1 << 20;
+constexpr int MOE_WIN = 2048;            // pairs looked through at a time
+constexpr int MOE_W = 4;                 // waves per workgroup, over the contracted axis
+
+struct MoeArgs {
+    const void *x, *gate, *w_in, *w_out;
+    int64_t ldx, ldy;
+    int32_t n, d, f, e, m, pairs;
+    int32_t slots;     // workgroups' second index: an expert, or a pair where those are fewer
+    int32_t by_pair;
+    int32_t all;       // shares over all experts instead of the picked ones
+    int32_t fp;        // row stride of act: f padded
+    int32_t* idx;
+    float* resp;
+    void* act;         // [parts][pairs][fp]
+    int64_t act_plane;
+    float* part;       // [pairs][d]
+    void* y;
+};
+
+// 16 bytes of a row, 0 at or past `end`.
+template <typename T>
+__device__ __forceinline__ Raw16 load_zero(const T* p, int64_t i, int64_t end) {
+    constexpr int VE = Vec<T>::VE;
+    if (i + VE <= end) return *reinterpret_cast<const Raw16*>(p + i);
+    Raw16 r = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+    for (int k = 0; k < VE; ++k)
+        if (i + k < end) Vec<T>::set(r, k, Vec<T>::one(p + i + k));
+    return r;
+}
+
+// c += the 16 x 16 product of 4 VE contracted values: lane 16 h + i holds
+// values VE h .. VE h + VE of row i of both operands.
+__device__ __forceinline__ f32x4 mfma_raw(const Raw16& a, const Raw16& b, f32x4 c, uint16_t) {
+    return mfma32(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c);
+}
+__device__ __forceinline__ f32x4 mfma_raw(const Raw16& a, const Raw16& b, f32x4 c, float) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.w[k]), __uint_as_float(b.w[k]), c,
+                                                 0, 0, 0);
+    return c;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
+    return v;
+}
+
+// ---- the choice of experts
+
+constexpr int RT_NT = 1024;
+template <typename T>
+__global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
+    constexpr int VE = Vec<T>::VE;
+    __shared__ float z[MOE_MAX_EXPERTS], key[MOE_MAX_EXPERTS];
+    __shared__ int id[MOE_MAX_EXPERTS];
+    __shared__ float ov[TOP_MAX], part[RT_NT / 64];
+    __shared__ int oi[TOP_MAX];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t row = blockIdx.x;
+    const T* x = (const T*)p.x + row * p.ldx;
+    for (int e = wave; e < p.e; e += RT_NT / 64) {
+        const T* g = (const T*)p.gate + (int64_t)e * p.d;
+        float s = 0.f;
+        for (int k = lane * VE; k < p.d; k += 64 * VE) {
+            const Raw16 a = load_zero(x, k, (int64_t)p.d), b = load_zero(g, k, (int64_t)p.d);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) s = fmaf(Vec<T>::get(a, u), Vec<T>::get(b, u), s);
+        }
+        s = wave_sum(s);
+        if (lane == 0) {
+            z[e] = s;
+            key[e] = s > -3.402823466e38f ? s : -3.402823466e38f;  // NaN ranks last
+            id[e] = e;
+        }
+    }
+    __syncthreads();
+    top_rank(key, id, p.e, p.m, ov, oi, tid, RT_NT);
+    __syncthreads();
+    const float top = ov[0];
+    float sum = 0.f;
+    if (p.all) {
+        for (int e = tid; e < p.e; e += RT_NT) sum += exp_neg(z[e] - top);
+        sum = wave_sum(sum);
+        if (lane == 0) part[wave] = sum;
+        __syncthreads();
+        sum = 0.f;
+        for (int w = 0; w < RT_NT / 64; ++w) sum += part[w];
+    } else {
+        for (int j = 0; j < p.m; ++j) sum += exp_neg(z[oi[j]] - top);
+    }
+    if (tid < p.m) {
+        p.idx[row * p.m + tid] = oi[tid];
+        p.resp[row * p.m + tid] = exp_neg(z[oi[tid]] - top) / sum;
+    }
+}
+
+// The pairs of window [w0, w0 + MOE_WIN) that picked expert e, in order.
+// Returns their count; all threads call it.
+__device__ __forceinline__ int moe_list(const MoeArgs& p, int e, int w0, int* list, int* cnt) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int base = 0;
+    for (int b = 0; b < MOE_WIN && w0 + b < p.pairs; b += 64 * MOE_W) {
+        const int i = w0 + b + tid;
+        const bool in = i < p.pairs && p.idx[i] == e;
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
+        if (lane == 0) cnt[wave] = __popcll(mask);
+        __syncthreads();
+        int at = base;
+        for (int w = 0; w < MOE_W; ++w) {
+            if (w < wave) at += cnt[w];
+            base += cnt[w];
+        }
+        if (in) list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = i;
+        __syncthreads();
+    }
+    return base;
+}
+
+// The expert of this workgroup, or -1: by pair, the first pair that picked an
+// expert does its work. All threads call it.
+__device__ __forceinline__ int moe_expert(const MoeArgs& p) {
+    if (!p.by_pair) return blockIdx.y;
+    const int e = p.idx[blockIdx.y];
+    int before = 0;
+    for (int i = threadIdx.x; i < (int)blockIdx.y; i += 64 * MOE_W) before |= p.idx[i] == e;
+    before = __syncthreads_or(before);
+    return before || e < 0 || e >= p.e ? -1 : e;
+}
+
+// ---- products
+
+// One group of U steps of the contracted axis, MOE_W apart, from step s.
+// FULL: the steps lie within k_end.
+template <typename T, int R, int TT, int PB, int U, bool FULL>
+__device__ __forceinline__ void moe_steps(const T* const* rows, const T* const* col, int64_t plane,
+                                          int s, int k_end, f32x4 (*acc)[TT]) {
+    constexpr int VE = Vec<T>::VE, STEP = 4 * VE;
+    const int h = (threadIdx.x & 63) >> 4;
+    Raw16 a[R][U], b[TT][PB][U];
+    auto get = [&](const T* q, int k) {
+        if constexpr (FULL)
+            return *reinterpret_cast<const Raw16*>(q + k);
+        else
+            return load_zero(q, k, (int64_t)k_end);
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int k = (s + u * MOE_W) * STEP + h * VE;
+#pragma unroll
+        for (int r = 0; r < R; ++r) a[r][u] = get(rows[r], k);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int q = 0; q < PB; ++q) b[t][q][u] = get(col[t] + q * plane, k);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int q = PB - 1; q >= 0; --q)
+                    acc[r][t] = mfma_raw(a[r][u], b[t][q][u], acc[r][t], T());
+}
+
+// acc[r][t] += W_r B_t over this wave's steps of the contracted axis (step s
+// belongs to wave s % MOE_W): R sets of 16 weight rows, of which rows[r] is
+// this lane's, TT sets of 16 columns (col[t]), each in PB planes. Groups of
+// 8 steps in flight, then 4, 2 and 1.
+template <typename T, int R, int TT, int PB>
+__device__ __forceinline__ void moe_dot(const T* const* rows, const T* const* col, int64_t plane,
+                                        int k_end, f32x4 (*acc)[TT]) {
+    constexpr int STEP = 4 * Vec<T>::VE;
+    const int full = k_end / STEP;
+    int s = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (TT == 1)
+        for (; s + 7 * MOE_W < full; s += 8 * MOE_W)
+            moe_steps<T, R, TT, PB, 8, true>(rows, col, plane, s, k_end, acc);
+    for (; s + 3 * MOE_W < full; s += 4 * MOE_W)
+        moe_steps<T, R, TT, PB, 4, true>(rows, col, plane, s, k_end, acc);
+    for (; s + MOE_W < full; s += 2 * MOE_W)
+        moe_steps<T, R, TT, PB, 2, true>(rows, col, plane, s, k_end, acc);
+    for (; s < full; s += MOE_W)
+        moe_steps<T, R, TT, PB, 1, true>(rows, col, plane, s, k_end, acc);
+    if (s * STEP < k_end) moe_steps<T, R, TT, PB, 1, false>(rows, col, plane, s, k_end, acc);
+}
+
+// Sums the waves' blocks: afterwards sh[b][lane][q] of wave 0's place holds the sum.
+template <int NB>
+__device__ __forceinline__ void moe_join_waves(const f32x4* acc, f32x4* sh) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) sh[(wave * NB + b) * 64 + lane] = acc[b];
+    __syncthreads();
+    for (int j = tid; j < NB * 64; j += 64 * MOE_W) {
+        f32x4 s = sh[j];
+#pragma unroll
+        for (int w = 1; w < MOE_W; ++w) s += sh[w * NB * 64 + j];
+        sh[j] = s;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void store_act(const MoeArgs& p, int64_t at, float v, float) {
+    ((float*)p.act)[at] = v;
+}
+// two bf16 parts: together 16 bits of v
+__device__ __forceinline__ void store_act(const MoeArgs& p, int64_t at, float v, uint16_t) {
+    uint16_t* a = (uint16_t*)p.act;
+    const uint32_t hi = f32_to_bf16(v);
+    const float rest = v - bf16_to_f32(hi);
+    a[at] = (uint16_t)hi;
+    a[p.act_plane + at] = rest == rest ? (uint16_t)f32_to_bf16(rest) : (uint16_t)0;
+}
+
+template <typename T, int TT>
+__device__ __forceinline__ void moe_in_tile(const MoeArgs& p, int e, int f0, const int* list, int cnt,
+                                            f32x4* sh) {
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15;
+    const int row = f0 + i < p.f ? f0 + i : p.f - 1;
+    const T* w = (const T*)p.w_in + (int64_t)e * 2 * p.f * p.d;
+    const T* rows[2] = {w + (int64_t)row * p.d, w + ((int64_t)p.f + row) * p.d};
+    const T* col[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int c = t * 16 + i < cnt ? t * 16 + i : cnt - 1;
+        col[t] = (const T*)p.x + (int64_t)(list[c] / p.m) * p.ldx;
+    }
+    f32x4 acc[2][TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    moe_dot<T, 2, TT, 1>(rows, col, 0, p.d, acc);
+    moe_join_waves<2 * TT>(&acc[0][0], sh);
+    // block t: gate part, block TT + t: the other; C[4 h + q][i] at lane 16 h + i
+    for (int j = tid; j < TT * 64; j += 64 * MOE_W) {
+        const int t = j >> 6, c = t * 16 + (j & 15), fq = f0 + 4 * ((j >> 4) & 3);
+        if (c >= cnt) continue;
+        const f32x4 a = sh[j], b = sh[TT * 64 + j];
+        const int64_t at = (int64_t)list[c] * p.fp;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (fq + q < p.f) store_act(p, at + fq + q, a[q] / (1.f + __expf(-a[q])) * b[q], T());
+    }
+    __syncthreads();
+}
+
+template <typename T>
+__global__ __launch_bounds__(64 * MOE_W) void k_moe_in(MoeArgs p) {
+    __shared__ f32x4 sh[MOE_W * 8 * 64];
+    __shared__ int list[MOE_WIN], cnt[MOE_W];
+    const int e = moe_expert(p);
+    if (e < 0) return;
+    const int f0 = blockIdx.x * 16;
+    for (int w0 = 0; w0 < p.pairs; w0 += MOE_WIN) {
+        const int c = moe_list(p, e, w0, list, cnt);
+        int at = 0;
+        for (; c - at > 16; at += 64) moe_in_tile<T, 4>(p, e, f0, list + at, c - at < 64 ? c - at : 64, sh);
+        if (at < c) moe_in_tile<T, 1>(p, e, f0, list + at, c - at, sh);
+        __syncthreads();
+    }
+}
+
+template <typename T, int TT>
+__device__ __forceinline__ void moe_out_tile(const MoeArgs& p, int e, int d0, const int* list, int cnt,
+                                             f32x4* sh) {
+    constexpr int PB = std::is_same<T, uint16_t>::value ? 2 : 1;
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15;
+    const int row = d0 + i < p.d ? d0 + i : p.d - 1;
+    const T* rows[1] = {(const T*)p.w_out + ((int64_t)e * p.d + row) * p.f};
+    const T* col[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int c = t * 16 + i < cnt ? t * 16 + i : cnt - 1;
+        col[t] = (const T*)p.act + (int64_t)list[c] * p.fp;
+    }
+    f32x4 acc[1][TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    moe_dot<T, 1, TT, PB>(rows, col, p.act_plane, p.f, acc);
+    moe_join_waves<TT>(&acc[0][0], sh);
+    for (int j = tid; j < TT * 64; j += 64 * MOE_W) {
+        const int t = j >> 6, c = t * 16 + (j & 15), dq = d0 + 4 * ((j >> 4) & 3);
+        if (c >= cnt) continue;
+        const f32x4 a = sh[j];
+        const int pair = list[c];
+        const float r = p.resp[pair];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (dq + q < p.d) p.part[(int64_t)pair * p.d + dq + q] = r * a[q];
+    }
+    __syncthreads();
+}
+
+template <typename T>
+__global__ __launch_bounds__(64 * MOE_W) void k_moe_out(MoeArgs p) {
+    __shared__ f32x4 sh[MOE_W * 4 * 64];
+    __shared__ int list[MOE_WIN], cnt[MOE_W];
+    const int e = moe_expert(p);
+    if (e < 0) return;
+    const int d0 = blockIdx.x * 16;
+    for (int w0 = 0; w0 < p.pairs; w0 += MOE_WIN) {
+        const int c = moe_list(p, e, w0, list, cnt);
+        int at = 0;
+        for (; c - at > 16; at += 64) moe_out_tile<T, 4>(p, e, d0, list + at, c - at < 64 ? c - at : 64, sh);
+        if (at < c) moe_out_tile<T, 1>(p, e, d0, list + at, c - at, sh);
+        __syncthreads();
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_moe_join(MoeArgs p) {
+    const int64_t total = (int64_t)p.n * p.d;
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total;
+         j += (int64_t)gridDim.x * 256) {
+        const int64_t row = j / p.d;
+        const int c = (int)(j - row * p.d);
+        float y = 0.f;
+        for (int k = 0; k < p.m; ++k) {
+            const int64_t pair = row * p.m + k;
+            const int e = p.idx[pair];
+            if (e >= 0 && e < p.e) y += p.part[pair * p.d + c];
+        }
+        ((T*)p.y)[row * p.ldy + c] = Vec<T>::store(y);
+    }
+}
+
+struct MoePlan {
+    int fp;
+    size_t o_act, o_part, bytes;
+};
+
+static bool moe_plan(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype, int32_t m, MoePlan* q) {
+    auto align = [](size_t b) { return (b + 255) & ~(size_t)255; };
+    const size_t pairs = (size_t)n * m;
+    q->fp = (f + 15) / 16 * 16;
+    q->o_act = 0;
+    // fp32, or two parts of bf16
+    q->o_part = align(pairs * q->fp * 4);
+    q->bytes = q->o_part + align(pairs * d * 4);
+    if (q->bytes < 256) q->bytes = 256;
+    return true;
+}
+
+static int moe_check(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype, int32_t m) {
+    if (dtype != GMM_F32 && dtype != GMM_BF16) return GMM_E_DTYPE;
+    if (n < 0 || d < 1 || f < 1 || e < 1 || m < 1 || m > TOP_MAX || m > e) return GMM_E_INVALID;
+    if (d > MOE_MAX_DIM || f > MOE_MAX_DIM || e > MOE_MAX_EXPERTS || n > MOE_MAX_PAIRS / m)
+        return GMM_E_UNSUPPORTED;
+    return GMM_OK;
+}
+
+template <typename T>
+static hipError_t launch_moe(const MoeArgs& a, hipStream_t st) {
+    if (a.gate) hipLaunchKernelGGL((k_moe_route<T>), dim3(a.n), dim3(RT_NT), 0, st, a);
+    hipLaunchKernelGGL((k_moe_in<T>), dim3((a.f + 15) / 16, a.slots), dim3(64 * MOE_W), 0, st, a);
+    hipLaunchKernelGGL((k_moe_out<T>), dim3((a.d + 15) / 16, a.slots), dim3(64 * MOE_W), 0, st, a);
+    const int64_t work = ((int64_t)a.n * a.d + 255) / 256;
+    hipLaunchKernelGGL((k_moe_join<T>), dim3((unsigned)(work < 16384 ? work : 16384)), dim3(256), 0, st,
+                       a);
+    return hipGetLastError();
+}
+
+}  // namespace gmm
+
+using namespace gmm;
+
+extern "C" {
+
+size_t gmm_moe_layer_workspace_bytes(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype,
+                                     int32_t m) {
+    MoePlan q;
+    if (moe_check(n, d, f, e, dtype, m) != GMM_OK) return 0;
+    return moe_plan(n, d, f, e, dtype, m, &q) ? q.bytes : 0;
+}
+
+int gmm_moe_layer(const void* x, int64_t n, int32_t d, int64_t ldx, const void* gate, int32_t e,
+                  const void* w_in, const void* w_out, int32_t f, int32_t dtype, int32_t m,
+                  int32_t share_all, int32_t* idx, float* resp, void* y, int64_t ldy,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = moe_check(n, d, f, e, dtype, m);
+    if (rc != GMM_OK) return rc;
+    if (ldx < d || ldy < d) return GMM_E_INVALID;
+    if (n > 0 && (!x || !w_in || !w_out || !idx || !resp || !y)) return GMM_E_INVALID;
+    MoePlan q;
+    moe_plan(n, d, f, e, dtype, m, &q);
+    if (!workspace || workspace_bytes < q.bytes || (uintptr_t)workspace % 256 != 0)
+        return GMM_E_WORKSPACE;
+    if (n == 0) return GMM_OK;
+    MoeArgs a{};
+    a.x = x;
+    a.gate = gate;
+    a.w_in = w_in;
+    a.w_out = w_out;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.n = (int32_t)n;
+    a.d = d;
+    a.f = f;
+    a.e = e;
+    a.m = m;
+    a.pairs = (int32_t)(n * m);
+    a.by_pair = a.pairs < e;
+    a.slots = a.by_pair ? a.pairs : e;
+    a.all = share_all != 0;
+    a.fp = q.fp;
+    a.idx = idx;
+    a.resp = resp;
+    a.act = (char*)workspace + q.o_act;
+    a.act_plane = (int64_t)a.pairs * q.fp;
+    a.part = (float*)((char*)workspace + q.o_part);
+    a.y = y;
+    const hipError_t err = dtype == GMM_F32 ? launch_moe<float>(a, (hipStream_t)stream)
+                                            : launch_moe<uint16_t>(a, (hipStream_t)stream);
+    return err == hipSuccess ? GMM_OK : GMM_E_HIP;
+}
+
+}  // extern "C"

@@ -37,25 +37,6 @@ __device__ __forceinline__ float target_logit(const ScoreArgs& p, int64_t row, i
     return t >= 0 && t < p.v ? Vec<T>::one((const T*)p.x + row * p.ldl + t) : 0.f;
 }
 
-// cnt sorted-or-not candidates (cv, ci) in LDS; the thread holding candidate c
-// writes it to rank's place in (ov, oi) when its rank is below m. Distinct
-// candidates have distinct ranks (indices differ); places that no candidate
-// takes must hold the empty entry before.
-__device__ __forceinline__ void top_rank(const float* cv, const int* ci, int cnt, int m, float* ov,
-                                         int* oi, int tid, int nt) {
-    for (int c = tid; c < cnt; c += nt) {
-        const float v = cv[c];
-        const int i = ci[c];
-        if (v == -INFINITY) continue;
-        int rank = 0;
-        for (int q = 0; q < cnt; ++q) rank += top_before(cv[q], ci[q], v, i);
-        if (rank < m) {
-            ov[rank] = v;
-            oi[rank] = i;
-        }
-    }
-}
-
 // NT threads per (row, part). parts == 1: writes the results; else the part's
 // statistics and list go to the workspace for k_score_join.
 template <typename T, int NT, bool TOP>

@@ -49,6 +49,10 @@ lib.gmm_head_score_backward_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32]
 lib.gmm_head_score_backward_workspace_bytes.restype = _sz
 lib.gmm_head_score_backward.argtypes = [_vp, _i64, _i32, _i64, _vp, _i32, _i64, _i32, _vp, _vp, _vp,
                                         _vp, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
+lib.gmm_moe_layer_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32]
+lib.gmm_moe_layer_workspace_bytes.restype = _sz
+lib.gmm_moe_layer.argtypes = [_vp, _i64, _i32, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                              _vp, _vp, _i64, _vp, _sz, _vp]
 lib.gmm_device_status.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.restype = ctypes.c_int
@@ -60,7 +64,7 @@ lib.gmm_profile_end.argtypes = [ctypes.POINTER(_f64), ctypes.POINTER(_i32), ctyp
                                 ctypes.POINTER(_i32)]
 for _f in (lib.gmm_em_step, lib.gmm_fit, lib.gmm_loglik, lib.gmm_assign_topm, lib.gmm_kmeans_step,
            lib.gmm_kmeans_fit, lib.gmm_ivf_build, lib.gmm_logits_score, lib.gmm_logits_score_backward,
-           lib.gmm_head_score, lib.gmm_head_score_backward, lib.gmm_device_status, lib.gmm_profile_begin, lib.gmm_profile_end):
+           lib.gmm_head_score, lib.gmm_head_score_backward, lib.gmm_moe_layer, lib.gmm_device_status, lib.gmm_profile_begin, lib.gmm_profile_end):
     _f.restype = ctypes.c_int
 
 (GMM_OK, GMM_E_INVALID, GMM_E_DTYPE, GMM_E_WORKSPACE, GMM_E_PARAMS, GMM_E_HIP,
@@ -403,6 +407,45 @@ def head_score_backward(hidden, weight, targets, norm, entropy=None, g_logprob=N
                                            t, norm.data_ptr(), h, gl, gh, scale, dh.data_ptr(), d,
                                            dw.data_ptr(), d, ws.data_ptr(), nb, _stream(dev)))
     return dh, dw
+
+
+def moe_layer(x, w_in, w_out, gate=None, m: int = 2, share_all: bool = False, idx=None, resp=None,
+              ws=None):
+    """Mixture-of-experts layer of x (N, D): (y (N, D), idx int32 (N, m), resp float32 (N, m)).
+
+    w_in (E, 2F, D) and w_out (E, D, F), contiguous, in x's type (float32 or
+    bfloat16). With gate (E, D) the m experts of largest gate logit are picked
+    and weighted by a softmax over them (over all experts with share_all);
+    without, idx and resp (N, m) give the picks and their weights, as
+    :func:`assign_topm` returns them. See gmm_moe_layer in ``include/gmm_em.h``.
+    """
+    dt, ldx = _rows2(x, "x")
+    n, d = x.shape
+    dev = x.device
+    e = w_in.shape[0]
+    f = w_out.shape[-1]
+    for t, nm, shape in ((w_in, "w_in", (e, 2 * f, d)), (w_out, "w_out", (e, d, f)),
+                         (gate, "gate", (e, d))):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != x.dtype or t.device != dev
+                              or not t.is_contiguous()):
+            raise ValueError(f"{nm} must be a contiguous tensor {shape} of x's type and device")
+    if (gate is None) != (idx is not None) or (idx is None) != (resp is None):
+        raise ValueError("give either gate, or idx and resp")
+    if gate is None:
+        m = idx.shape[1] if idx.dim() == 2 else -1
+        for t, nm, ty in ((idx, "idx", torch.int32), (resp, "resp", torch.float32)):
+            if t.dtype != ty or tuple(t.shape) != (n, m) or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"{nm} must be a contiguous (N, m) tensor of {ty} on x's device")
+    ws, nb = _scratch(lib.gmm_moe_layer_workspace_bytes(n, d, f, e, dt, m), ws, dev)
+    if gate is not None:
+        idx = torch.empty((n, m), dtype=torch.int32, device=dev)
+        resp = torch.empty((n, m), dtype=torch.float32, device=dev)
+    y = torch.empty((n, d), dtype=x.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.gmm_moe_layer(x.data_ptr(), n, d, ldx, _ptr(gate), e, w_in.data_ptr(),
+                                 w_out.data_ptr(), f, dt, m, int(share_all), idx.data_ptr(),
+                                 resp.data_ptr(), y.data_ptr(), d, ws.data_ptr(), nb, _stream(dev)))
+    return y, idx, resp
 
 
 def device_status(ws, device="cuda") -> int:

@@ -308,6 +308,35 @@ int gmm_head_score_backward(const void* hidden, int64_t n, int32_t d, int64_t ld
                             void* d_hidden, int64_t lddh, void* d_weight, int64_t lddw,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* A mixture-of-experts layer for a few rows. For row x of n rows of d values
+ * (leading dimension ldx >= d), with e experts of f features:
+ *   z = x G^T (gate: e x d, row-major); the m experts of largest z, largest
+ *   first (ties: smaller index first; NaN ranks last), go to idx[r][0..m) and
+ *   their shares to resp[r][0..m): the softmax of z over the picked experts, or
+ *   over all experts when share_all is not 0;
+ *   y = sum_j resp[r][j] W_out[c] (silu(W_a[c] x) * (W_b[c] x)),  c = idx[r][j].
+ * w_in (e x 2f x d, row-major) holds f rows W_a and then f rows W_b for each
+ * expert, w_out (e x d x f) the rows W_out. gate may be NULL: then idx and resp
+ * (device, n*m, as gmm_assign_topm writes them: a mixture as the router) are
+ * read instead of written; picks outside [0, e) are skipped, an expert picked
+ * twice by a row counts twice. x, gate, weights and y (leading dimension
+ * ldy >= d) are all fp32 or all bf16, at any alignment of an element. y must
+ * not overlap x.
+ * Products of bf16 are exact; every sum is fp32 in a fixed order (bitwise
+ * reproducible); the features between the two products keep 16 significant bits
+ * for bf16 data and 24 for fp32; y is rounded once. Each expert's weights are
+ * read once for every 64 rows that picked it, unpicked experts' not at all; with
+ * many rows per expert the layer is bound by its products instead.
+ * 1 <= m <= min(e, GMM_TOP_MAX); n may be 0; e <= 4096, n*m <= 2^20, d and f <= 2^20
+ * (GMM_E_UNSUPPORTED beyond). The workspace (device, 256-byte aligned) has
+ * gmm_moe_layer_workspace_bytes bytes (0: invalid or unsupported sizes). */
+size_t gmm_moe_layer_workspace_bytes(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype,
+                                     int32_t m);
+int gmm_moe_layer(const void* x, int64_t n, int32_t d, int64_t ldx, const void* gate, int32_t e,
+                  const void* w_in, const void* w_out, int32_t f, int32_t dtype, int32_t m,
+                  int32_t share_all, int32_t* idx, float* resp, void* y, int64_t ldy,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises the stream and returns GMM_E_PARAMS if the last call that used
  * this workspace found invalid parameter values, GMM_OK otherwise, or
  * GMM_E_HIP if the synchronisation failed. */
