@@ -228,25 +228,6 @@ __global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int 
 
 // ---- epilogues
 
-// reduction over the 16 lanes that share a row of the accumulators
-template <int N>
-__device__ __forceinline__ float ror16(float v) {
-    return __uint_as_float(
-        __builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x120 + N, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float max16(float v) {
-    v = fmaxf(v, ror16<8>(v));
-    v = fmaxf(v, ror16<4>(v));
-    v = fmaxf(v, ror16<2>(v));
-    return fmaxf(v, ror16<1>(v));
-}
-__device__ __forceinline__ float sum16(float v) {
-    v += ror16<8>(v);
-    v += ror16<4>(v);
-    v += ror16<2>(v);
-    return v + ror16<1>(v);
-}
-
 struct HeadArgs {
     GemmIn in;
     int32_t mt, nt;      // tiles

@@ -33,8 +33,9 @@ constexpr int MOE_MAX_EXPERTS = 4096;    // gate logits of a row in LDS
 constexpr int64_t MOE_MAX_PAIRS = 1 << 20;  // (row, pick) pairs per call
 constexpr int32_t MOE_MAX_DIM = 1 << 20;
 constexpr int MOE_WIN = 2048;            // pairs looked through at a time
-constexpr int MOE_W = 4;                 // waves per workgroup, over the contracted axis
 
+// Where the picks of one call fit a wave (pairs <= 64), every wave finds its
+// workgroup's expert and rows from one load and a ballot.
 struct MoeArgs {
     const void *x, *gate, *w_in, *w_out;
     int64_t ldx, ldy;
@@ -76,15 +77,12 @@ __device__ __forceinline__ f32x4 mfma_raw(const Raw16& a, const Raw16& b, f32x4 
     return c;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
-    return v;
-}
-
 // ---- the choice of experts
 
-constexpr int RT_NT = 1024;
+// Dot products of one row of x with RT_U gates at a time (all their loads in
+// flight), a wave for each group. Up to RT_PICK experts are ranked in one wave's
+// registers, more by counting in LDS.
+constexpr int RT_NT = 1024, RT_U = 4, RT_PICK = 512;
 template <typename T>
 __global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
     constexpr int VE = Vec<T>::VE;
@@ -95,23 +93,56 @@ __global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = blockIdx.x;
     const T* x = (const T*)p.x + row * p.ldx;
-    for (int e = wave; e < p.e; e += RT_NT / 64) {
-        const T* g = (const T*)p.gate + (int64_t)e * p.d;
-        float s = 0.f;
-        for (int k = lane * VE; k < p.d; k += 64 * VE) {
-            const Raw16 a = load_zero(x, k, (int64_t)p.d), b = load_zero(g, k, (int64_t)p.d);
+    for (int e0 = wave * RT_U; e0 < p.e; e0 += RT_NT / 64 * RT_U) {
+        float s[RT_U];
+        const T* g[RT_U];
 #pragma unroll
-            for (int u = 0; u < VE; ++u) s = fmaf(Vec<T>::get(a, u), Vec<T>::get(b, u), s);
+        for (int j = 0; j < RT_U; ++j) {
+            s[j] = 0.f;
+            g[j] = (const T*)p.gate + (int64_t)(e0 + j < p.e ? e0 + j : p.e - 1) * p.d;
         }
-        s = wave_sum(s);
-        if (lane == 0) {
-            z[e] = s;
-            key[e] = s > -3.402823466e38f ? s : -3.402823466e38f;  // NaN ranks last
-            id[e] = e;
+#pragma unroll 2
+        for (int k = lane * VE; k < p.d; k += 64 * VE) {
+            const Raw16 a = load_zero(x, k, (int64_t)p.d);
+            Raw16 b[RT_U];
+#pragma unroll
+            for (int j = 0; j < RT_U; ++j) b[j] = load_zero(g[j], k, (int64_t)p.d);
+#pragma unroll
+            for (int j = 0; j < RT_U; ++j)
+#pragma unroll
+                for (int u = 0; u < VE; ++u)
+                    s[j] = fmaf(Vec<T>::get(a, u), Vec<T>::get(b[j], u), s[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < RT_U; ++j) {
+            const float t = wave_sum(s[j]);
+            if (lane == 0 && e0 + j < p.e) {
+                z[e0 + j] = t;
+                key[e0 + j] = t > -3.402823466e38f ? t : -3.402823466e38f;  // NaN ranks last
+                id[e0 + j] = e0 + j;
+            }
         }
     }
     __syncthreads();
-    top_rank(key, id, p.e, p.m, ov, oi, tid, RT_NT);
+    if (p.e <= RT_PICK) {
+        if (wave == 0) {
+            constexpr int C = RT_PICK / 64;
+            float cv[C];
+            int ci[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                ci[c] = c * 64 + lane;
+                cv[c] = ci[c] < p.e ? key[ci[c]] : -INFINITY;
+            }
+            const TopList t = top_pick<C>(cv, ci, p.m, lane);
+            if (lane < p.m) {
+                ov[lane] = t.v;
+                oi[lane] = t.i;
+            }
+        }
+    } else {
+        top_rank(key, id, p.e, p.m, ov, oi, tid, RT_NT);
+    }
     __syncthreads();
     const float top = ov[0];
     float sum = 0.f;
@@ -122,8 +153,8 @@ __global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
         __syncthreads();
         sum = 0.f;
         for (int w = 0; w < RT_NT / 64; ++w) sum += part[w];
-    } else {
-        for (int j = 0; j < p.m; ++j) sum += exp_neg(z[oi[j]] - top);
+    } else if (wave == 0) {
+        sum = wave_sum(lane < p.m ? exp_neg(z[oi[lane]] - top) : 0.f);
     }
     if (tid < p.m) {
         p.idx[row * p.m + tid] = oi[tid];
@@ -132,22 +163,31 @@ __global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
 }
 
 // The pairs of window [w0, w0 + MOE_WIN) that picked expert e, in order.
-// Returns their count; all threads call it.
+// Returns their count; all W waves call it.
+template <int W>
 __device__ __forceinline__ int moe_list(const MoeArgs& p, int e, int w0, int* list, int* cnt) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    if (p.pairs <= 64) {  // every wave writes the same list
+        const bool in = lane < p.pairs && p.idx[lane] == e;
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
+        if (in) list[__popcll(mask & below)] = lane;
+        __builtin_amdgcn_wave_barrier();
+        return __popcll(mask);
+    }
     int base = 0;
-    for (int b = 0; b < MOE_WIN && w0 + b < p.pairs; b += 64 * MOE_W) {
+    for (int b = 0; b < MOE_WIN && w0 + b < p.pairs; b += 64 * W) {
         const int i = w0 + b + tid;
         const bool in = i < p.pairs && p.idx[i] == e;
         const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
         if (lane == 0) cnt[wave] = __popcll(mask);
         __syncthreads();
         int at = base;
-        for (int w = 0; w < MOE_W; ++w) {
+        for (int w = 0; w < W; ++w) {
             if (w < wave) at += cnt[w];
             base += cnt[w];
         }
-        if (in) list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = i;
+        if (in) list[at + __popcll(mask & below)] = i;
         __syncthreads();
     }
     return base;
@@ -155,20 +195,29 @@ __device__ __forceinline__ int moe_list(const MoeArgs& p, int e, int w0, int* li
 
 // The expert of this workgroup, or -1: by pair, the first pair that picked an
 // expert does its work. All threads call it.
+template <int W>
 __device__ __forceinline__ int moe_expert(const MoeArgs& p) {
-    if (!p.by_pair) return blockIdx.y;
-    const int e = p.idx[blockIdx.y];
+    const int slot = blockIdx.y;
+    if (!p.by_pair) return slot;
+    if (p.pairs <= 64) {
+        const int lane = threadIdx.x & 63;
+        const int mine = lane < p.pairs ? p.idx[lane] : -1;
+        const int e = __builtin_amdgcn_readlane(mine, slot);
+        const uint64_t same = __builtin_amdgcn_ballot_w64(mine == e);
+        return e < 0 || e >= p.e || __builtin_ctzll(same) != slot ? -1 : e;
+    }
+    const int e = p.idx[slot];
     int before = 0;
-    for (int i = threadIdx.x; i < (int)blockIdx.y; i += 64 * MOE_W) before |= p.idx[i] == e;
+    for (int i = threadIdx.x; i < slot; i += 64 * W) before |= p.idx[i] == e;
     before = __syncthreads_or(before);
     return before || e < 0 || e >= p.e ? -1 : e;
 }
 
 // ---- products
 
-// One group of U steps of the contracted axis, MOE_W apart, from step s.
+// One group of U steps of the contracted axis, W apart, from step s.
 // FULL: the steps lie within k_end.
-template <typename T, int R, int TT, int PB, int U, bool FULL>
+template <typename T, int R, int TT, int PB, int W, int U, bool FULL>
 __device__ __forceinline__ void moe_steps(const T* const* rows, const T* const* col, int64_t plane,
                                           int s, int k_end, f32x4 (*acc)[TT]) {
     constexpr int VE = Vec<T>::VE, STEP = 4 * VE;
@@ -182,7 +231,7 @@ __device__ __forceinline__ void moe_steps(const T* const* rows, const T* const* 
     };
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int k = (s + u * MOE_W) * STEP + h * VE;
+        const int k = (s + u * W) * STEP + h * VE;
 #pragma unroll
         for (int r = 0; r < R; ++r) a[r][u] = get(rows[r], k);
 #pragma unroll
@@ -202,38 +251,38 @@ __device__ __forceinline__ void moe_steps(const T* const* rows, const T* const* 
 }
 
 // acc[r][t] += W_r B_t over this wave's steps of the contracted axis (step s
-// belongs to wave s % MOE_W): R sets of 16 weight rows, of which rows[r] is
+// belongs to wave s % W): R sets of 16 weight rows, of which rows[r] is
 // this lane's, TT sets of 16 columns (col[t]), each in PB planes. Groups of
 // 8 steps in flight, then 4, 2 and 1.
-template <typename T, int R, int TT, int PB>
+template <typename T, int R, int TT, int PB, int W>
 __device__ __forceinline__ void moe_dot(const T* const* rows, const T* const* col, int64_t plane,
                                         int k_end, f32x4 (*acc)[TT]) {
     constexpr int STEP = 4 * Vec<T>::VE;
     const int full = k_end / STEP;
     int s = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if constexpr (TT == 1)
-        for (; s + 7 * MOE_W < full; s += 8 * MOE_W)
-            moe_steps<T, R, TT, PB, 8, true>(rows, col, plane, s, k_end, acc);
-    for (; s + 3 * MOE_W < full; s += 4 * MOE_W)
-        moe_steps<T, R, TT, PB, 4, true>(rows, col, plane, s, k_end, acc);
-    for (; s + MOE_W < full; s += 2 * MOE_W)
-        moe_steps<T, R, TT, PB, 2, true>(rows, col, plane, s, k_end, acc);
-    for (; s < full; s += MOE_W)
-        moe_steps<T, R, TT, PB, 1, true>(rows, col, plane, s, k_end, acc);
-    if (s * STEP < k_end) moe_steps<T, R, TT, PB, 1, false>(rows, col, plane, s, k_end, acc);
+    if constexpr (TT == 1 && R <= 2)
+        for (; s + 7 * W < full; s += 8 * W)
+            moe_steps<T, R, TT, PB, W, 8, true>(rows, col, plane, s, k_end, acc);
+    for (; s + 3 * W < full; s += 4 * W)
+        moe_steps<T, R, TT, PB, W, 4, true>(rows, col, plane, s, k_end, acc);
+    for (; s + W < full; s += 2 * W)
+        moe_steps<T, R, TT, PB, W, 2, true>(rows, col, plane, s, k_end, acc);
+    for (; s < full; s += W)
+        moe_steps<T, R, TT, PB, W, 1, true>(rows, col, plane, s, k_end, acc);
+    if (s * STEP < k_end) moe_steps<T, R, TT, PB, W, 1, false>(rows, col, plane, s, k_end, acc);
 }
 
 // Sums the waves' blocks: afterwards sh[b][lane][q] of wave 0's place holds the sum.
-template <int NB>
+template <int NB, int W>
 __device__ __forceinline__ void moe_join_waves(const f32x4* acc, f32x4* sh) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 #pragma unroll
     for (int b = 0; b < NB; ++b) sh[(wave * NB + b) * 64 + lane] = acc[b];
     __syncthreads();
-    for (int j = tid; j < NB * 64; j += 64 * MOE_W) {
+    for (int j = tid; j < NB * 64; j += 64 * W) {
         f32x4 s = sh[j];
 #pragma unroll
-        for (int w = 1; w < MOE_W; ++w) s += sh[w * NB * 64 + j];
+        for (int w = 1; w < W; ++w) s += sh[w * NB * 64 + j];
         sh[j] = s;
     }
     __syncthreads();
@@ -251,7 +300,7 @@ __device__ __forceinline__ void store_act(const MoeArgs& p, int64_t at, float v,
     a[p.act_plane + at] = rest == rest ? (uint16_t)f32_to_bf16(rest) : (uint16_t)0;
 }
 
-template <typename T, int TT>
+template <typename T, int TT, int W>
 __device__ __forceinline__ void moe_in_tile(const MoeArgs& p, int e, int f0, const int* list, int cnt,
                                             f32x4* sh) {
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15;
@@ -267,10 +316,10 @@ __device__ __forceinline__ void moe_in_tile(const MoeArgs& p, int e, int f0, con
     f32x4 acc[2][TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    moe_dot<T, 2, TT, 1>(rows, col, 0, p.d, acc);
-    moe_join_waves<2 * TT>(&acc[0][0], sh);
+    moe_dot<T, 2, TT, 1, W>(rows, col, 0, p.d, acc);
+    moe_join_waves<2 * TT, W>(&acc[0][0], sh);
     // block t: gate part, block TT + t: the other; C[4 h + q][i] at lane 16 h + i
-    for (int j = tid; j < TT * 64; j += 64 * MOE_W) {
+    for (int j = tid; j < TT * 64; j += 64 * W) {
         const int t = j >> 6, c = t * 16 + (j & 15), fq = f0 + 4 * ((j >> 4) & 3);
         if (c >= cnt) continue;
         const f32x4 a = sh[j], b = sh[TT * 64 + j];
@@ -282,67 +331,82 @@ __device__ __forceinline__ void moe_in_tile(const MoeArgs& p, int e, int f0, con
     __syncthreads();
 }
 
-template <typename T>
-__global__ __launch_bounds__(64 * MOE_W) void k_moe_in(MoeArgs p) {
-    __shared__ f32x4 sh[MOE_W * 8 * 64];
-    __shared__ int list[MOE_WIN], cnt[MOE_W];
-    const int e = moe_expert(p);
-    if (e < 0) return;
-    const int f0 = blockIdx.x * 16;
+// Runs tile<TT>(list, count) over the expert's rows: 64 at a time while more than
+// 16 are left, then 16.
+template <int W, typename F>
+__device__ __forceinline__ void moe_each(const MoeArgs& p, int e, int* list, int* cnt, F tile) {
     for (int w0 = 0; w0 < p.pairs; w0 += MOE_WIN) {
-        const int c = moe_list(p, e, w0, list, cnt);
+        const int c = moe_list<W>(p, e, w0, list, cnt);
         int at = 0;
-        for (; c - at > 16; at += 64) moe_in_tile<T, 4>(p, e, f0, list + at, c - at < 64 ? c - at : 64, sh);
-        if (at < c) moe_in_tile<T, 1>(p, e, f0, list + at, c - at, sh);
+        for (; c - at > 16; at += 64)
+            tile(std::integral_constant<int, 4>(), list + at, c - at < 64 ? c - at : 64);
+        if (at < c) tile(std::integral_constant<int, 1>(), list + at, c - at);
         __syncthreads();
     }
 }
 
-template <typename T, int TT>
+template <typename T, int W>
+__global__ __launch_bounds__(64 * W) void k_moe_in(MoeArgs p) {
+    __shared__ f32x4 sh[W * 8 * 64];
+    __shared__ int list[MOE_WIN], cnt[W];
+    const int e = moe_expert<W>(p);
+    if (e < 0) return;
+    const int f0 = blockIdx.x * 16;
+    moe_each<W>(p, e, list, cnt, [&](auto tt, const int* l, int c) {
+        moe_in_tile<T, decltype(tt)::value, W>(p, e, f0, l, c, sh);
+    });
+}
+
+template <typename T, int TT, int R, int W>
 __device__ __forceinline__ void moe_out_tile(const MoeArgs& p, int e, int d0, const int* list, int cnt,
                                              f32x4* sh) {
     constexpr int PB = std::is_same<T, uint16_t>::value ? 2 : 1;
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15;
-    const int row = d0 + i < p.d ? d0 + i : p.d - 1;
-    const T* rows[1] = {(const T*)p.w_out + ((int64_t)e * p.d + row) * p.f};
+    const T* rows[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = d0 + r * 16 + i < p.d ? d0 + r * 16 + i : p.d - 1;
+        rows[r] = (const T*)p.w_out + ((int64_t)e * p.d + row) * p.f;
+    }
     const T* col[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int c = t * 16 + i < cnt ? t * 16 + i : cnt - 1;
         col[t] = (const T*)p.act + (int64_t)list[c] * p.fp;
     }
-    f32x4 acc[1][TT];
+    f32x4 acc[R][TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    moe_dot<T, 1, TT, PB>(rows, col, p.act_plane, p.f, acc);
-    moe_join_waves<TT>(&acc[0][0], sh);
-    for (int j = tid; j < TT * 64; j += 64 * MOE_W) {
-        const int t = j >> 6, c = t * 16 + (j & 15), dq = d0 + 4 * ((j >> 4) & 3);
-        if (c >= cnt) continue;
-        const f32x4 a = sh[j];
-        const int pair = list[c];
-        const float r = p.resp[pair];
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (dq + q < p.d) p.part[(int64_t)pair * p.d + dq + q] = r * a[q];
-    }
-    __syncthreads();
-}
-
-template <typename T>
-__global__ __launch_bounds__(64 * MOE_W) void k_moe_out(MoeArgs p) {
-    __shared__ f32x4 sh[MOE_W * 4 * 64];
-    __shared__ int list[MOE_WIN], cnt[MOE_W];
-    const int e = moe_expert(p);
-    if (e < 0) return;
-    const int d0 = blockIdx.x * 16;
-    for (int w0 = 0; w0 < p.pairs; w0 += MOE_WIN) {
-        const int c = moe_list(p, e, w0, list, cnt);
-        int at = 0;
-        for (; c - at > 16; at += 64) moe_out_tile<T, 4>(p, e, d0, list + at, c - at < 64 ? c - at : 64, sh);
-        if (at < c) moe_out_tile<T, 1>(p, e, d0, list + at, c - at, sh);
+        for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    moe_dot<T, R, TT, PB, W>(rows, col, p.act_plane, p.f, acc);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        moe_join_waves<TT, W>(acc[r], sh);
+        for (int j = tid; j < TT * 64; j += 64 * W) {
+            const int t = j >> 6, c = t * 16 + (j & 15), dq = d0 + r * 16 + 4 * ((j >> 4) & 3);
+            if (c >= cnt) continue;
+            const f32x4 a = sh[j];
+            const int pair = list[c];
+            const float w = p.resp[pair];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (dq + q < p.d) p.part[(int64_t)pair * p.d + dq + q] = w * a[q];
+        }
         __syncthreads();
     }
+}
+
+template <typename T, int R, int W>
+__global__ __launch_bounds__(64 * W) void k_moe_out(MoeArgs p) {
+    __shared__ f32x4 sh[W * 4 * 64];
+    __shared__ int list[MOE_WIN], cnt[W];
+    const int e = moe_expert<W>(p);
+    if (e < 0) return;
+    const int d0 = blockIdx.x * 16 * R;
+    moe_each<W>(p, e, list, cnt, [&](auto tt, const int* l, int c) {
+        moe_out_tile<T, decltype(tt)::value, R, W>(p, e, d0, l, c, sh);
+    });
 }
 
 template <typename T>
@@ -390,8 +454,15 @@ static int moe_check(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype, 
 template <typename T>
 static hipError_t launch_moe(const MoeArgs& a, hipStream_t st) {
     if (a.gate) hipLaunchKernelGGL((k_moe_route<T>), dim3(a.n), dim3(RT_NT), 0, st, a);
-    hipLaunchKernelGGL((k_moe_in<T>), dim3((a.f + 15) / 16, a.slots), dim3(64 * MOE_W), 0, st, a);
-    hipLaunchKernelGGL((k_moe_out<T>), dim3((a.d + 15) / 16, a.slots), dim3(64 * MOE_W), 0, st, a);
+    const int ft = (a.f + 15) / 16, dt = (a.d + 15) / 16;
+    hipLaunchKernelGGL((k_moe_in<T, 4>), dim3(ft, a.slots), dim3(256), 0, st, a);
+    // enough tiles: 64 features share the loads of act; few: 16 waves share a tile
+    if ((int64_t)dt * a.slots >= 4096)
+        hipLaunchKernelGGL((k_moe_out<T, 4, 4>), dim3((dt + 3) / 4, a.slots), dim3(256), 0, st, a);
+    else if ((int64_t)dt * a.slots >= 512)
+        hipLaunchKernelGGL((k_moe_out<T, 1, 4>), dim3(dt, a.slots), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_moe_out<T, 1, 16>), dim3(dt, a.slots), dim3(1024), 0, st, a);
     const int64_t work = ((int64_t)a.n * a.d + 255) / 256;
     hipLaunchKernelGGL((k_moe_join<T>), dim3((unsigned)(work < 16384 ? work : 16384)), dim3(256), 0, st,
                        a);

@@ -43,8 +43,8 @@ template <typename T, int NT, bool TOP>
 __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
     constexpr int VE = Vec<T>::VE, NW = NT / 64;
     __shared__ float sst[NW][3];
-    __shared__ float sv[NW * TOP_MAX], ov[TOP_MAX];
-    __shared__ int si[NW * TOP_MAX], oi[TOP_MAX];
+    __shared__ float sv[NW * TOP_MAX];
+    __shared__ int si[NW * TOP_MAX];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int64_t item = blockIdx.x; item < p.n * p.parts; item += gridDim.x) {
         const int64_t row = item / p.parts;
@@ -111,31 +111,36 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
                     sv[wave * p.m + lane] = top.v;
                     si[wave * p.m + lane] = top.i;
                 }
-                if (tid < TOP_MAX) {
-                    ov[tid] = -INFINITY;
-                    oi[tid] = 0x7fffffff;
-                }
             }
             __syncthreads();
-            st = Stats{sst[0][0], sst[0][1], sst[0][2]};
+            // wave 0 joins the waves' statistics and lists
+            if (wave == 0) {
+                st.clear();
+                if (lane < NW) st = Stats{sst[lane][0], sst[lane][1], sst[lane][2]};
+                st.wave_join();
+                if constexpr (TOP) {
+                    constexpr int C = (NW * TOP_MAX + 63) / 64;
+                    float cv[C];
+                    int ci[C];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) st.join(sst[w][0], sst[w][1], sst[w][2]);
-            if constexpr (TOP) {
-                top_rank(sv, si, NW * p.m, p.m, ov, oi, tid, NT);
-                __syncthreads();
-                if (tid < p.m) {
-                    top.v = ov[tid];
-                    top.i = oi[tid];
+                    for (int c = 0; c < C; ++c) {
+                        const int at = c * 64 + lane;
+                        cv[c] = at < NW * p.m ? sv[at] : -INFINITY;
+                        ci[c] = at < NW * p.m ? si[at] : 0x7fffffff;
+                    }
+                    top = top_pick<C>(cv, ci, p.m, lane);
                 }
             }
         }
-        if (p.parts == 1) {
-            score_out(p, row, st, target_logit<T>(p, row, tid), top.v, top.i, tid);
-        } else {
-            if (tid == 0) p.part[item] = ScorePart{st.m, st.s, st.a};
-            if (TOP && tid < p.m) {
-                p.part_v[item * p.m + tid] = top.v;
-                p.part_i[item * p.m + tid] = top.i;
+        if (wave == 0) {
+            if (p.parts == 1) {
+                score_out(p, row, st, target_logit<T>(p, row, lane), top.v, top.i, lane);
+            } else {
+                if (lane == 0) p.part[item] = ScorePart{st.m, st.s, st.a};
+                if (TOP && lane < p.m) {
+                    p.part_v[item * p.m + lane] = top.v;
+                    p.part_i[item * p.m + lane] = top.i;
+                }
             }
         }
         if constexpr (NW > 1) __syncthreads();  // LDS is free for the next item
@@ -145,8 +150,7 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
 // One wave per row joins its parts' statistics and lists.
 template <typename T>
 __global__ __launch_bounds__(64) void k_score_join(ScoreArgs p) {
-    __shared__ float sv[SC_MAX_PARTS * TOP_MAX], ov[TOP_MAX];
-    __shared__ int si[SC_MAX_PARTS * TOP_MAX], oi[TOP_MAX];
+    constexpr int C = SC_MAX_PARTS * TOP_MAX / 64;
     const int lane = threadIdx.x;
     for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x) {
         Stats st;
@@ -157,20 +161,16 @@ __global__ __launch_bounds__(64) void k_score_join(ScoreArgs p) {
         }
         st.wave_join();
         const int cnt = p.parts * p.m;
-        for (int c = lane; c < cnt; c += 64) {
-            sv[c] = p.part_v[row * cnt + c];
-            si[c] = p.part_i[row * cnt + c];
+        float cv[C];
+        int ci[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = c * 64 + lane;
+            cv[c] = at < cnt ? p.part_v[row * cnt + at] : -INFINITY;
+            ci[c] = at < cnt ? p.part_i[row * cnt + at] : 0x7fffffff;
         }
-        if (lane < TOP_MAX) {
-            ov[lane] = -INFINITY;
-            oi[lane] = 0x7fffffff;
-        }
-        __syncthreads();
-        top_rank(sv, si, cnt, p.m, ov, oi, lane, 64);
-        __syncthreads();
-        score_out(p, row, st, target_logit<T>(p, row, lane), ov[lane & (TOP_MAX - 1)],
-                  oi[lane & (TOP_MAX - 1)], lane);
-        __syncthreads();
+        const TopList top = top_pick<C>(cv, ci, p.m, lane);
+        score_out(p, row, st, target_logit<T>(p, row, lane), top.v, top.i, lane);
     }
 }
 

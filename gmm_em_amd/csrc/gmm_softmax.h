@@ -70,6 +70,53 @@ __device__ __forceinline__ Raw16 load_vec(const T* p, int64_t i, int64_t end) {
     return r;
 }
 
+// ---- wave-wide reductions on the data-parallel lanes (no LDS)
+
+// v of another lane: 0x120 + N rotates each group of 16 lanes by N, 0x138
+// shifts the wave up by one lane (lane 0 keeps its own).
+template <int CTRL>
+__device__ __forceinline__ float lane_move(float v) {
+    const int u = (int)__float_as_uint(v);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(u, u, CTRL, 0xf, 0xf, false));
+}
+template <int CTRL>
+__device__ __forceinline__ int lane_move(int v) {
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
+}
+__device__ __forceinline__ float lane_get(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+// over each group of 16 lanes
+__device__ __forceinline__ float max16(float v) {
+    v = fmaxf(v, lane_move<0x128>(v));
+    v = fmaxf(v, lane_move<0x124>(v));
+    v = fmaxf(v, lane_move<0x122>(v));
+    return fmaxf(v, lane_move<0x121>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+    v += lane_move<0x128>(v);
+    v += lane_move<0x124>(v);
+    v += lane_move<0x122>(v);
+    return v + lane_move<0x121>(v);
+}
+// over the wave, the same in every lane
+__device__ __forceinline__ float wave_max(float v) {
+    v = max16(v);
+    return fmaxf(fmaxf(lane_get(v, 0), lane_get(v, 16)), fmaxf(lane_get(v, 32), lane_get(v, 48)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = sum16(v);
+    return (lane_get(v, 0) + lane_get(v, 16)) + (lane_get(v, 32) + lane_get(v, 48));
+}
+__device__ __forceinline__ int wave_min(int v) {
+    v = min(v, lane_move<0x128>(v));
+    v = min(v, lane_move<0x124>(v));
+    v = min(v, lane_move<0x122>(v));
+    v = min(v, lane_move<0x121>(v));
+    return min(min(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+               min(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+
 // Online softmax statistics of a set of scaled logits l: m = max l (or
 // -FLT_MAX where none is above it), s = sum exp(l - m), a = sum exp(l - m)
 // (l - m). An empty set, or one of -inf only, has s = 0. A NaN or +inf leaves
@@ -107,9 +154,9 @@ struct Stats {
     }
     // over the wave's 64 lanes, in a fixed order, the same in every lane
     __device__ __forceinline__ void wave_join() {
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            join(__shfl_xor(m, off), __shfl_xor(s, off), __shfl_xor(a, off));
+        raise(wave_max(m));
+        s = wave_sum(s);
+        a = wave_sum(a);
     }
     __device__ __forceinline__ bool empty() const { return s == 0.f; }
 };
@@ -117,16 +164,6 @@ struct Stats {
 // (v, i) before (v2, i2): larger value first, ties to the smaller index.
 __device__ __forceinline__ bool top_before(float v, int i, float v2, int i2) {
     return v > v2 || (v == v2 && i < i2);
-}
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) v = fmaxf(v, __shfl_xor(v, off));
-    return v;
-}
-
-__device__ __forceinline__ float lane_get(float v, int lane) {
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
 
 // A wave's sorted list of its m best (value, index) pairs: entry j in lane j,
@@ -144,8 +181,8 @@ struct TopList {
         const uint64_t before = __builtin_amdgcn_ballot_w64(top_before(v, i, nv, ni));
         const int pos = __popcll(before & ((uint64_t(1) << m) - 1));
         if (pos >= m) return;
-        const float uv = __shfl_up(v, 1);
-        const int ui = __shfl_up(i, 1);
+        const float uv = lane_move<0x138>(v);
+        const int ui = lane_move<0x138>(i);
         if (lane == pos) {
             v = nv;
             i = ni;
@@ -155,6 +192,33 @@ struct TopList {
         }
     }
 };
+
+// The m best of C * 64 candidates, C per lane, as a sorted list: m rounds of the
+// best value and, among its equals, the smallest index. -inf is the empty entry.
+template <int C>
+__device__ __forceinline__ TopList top_pick(float* cv, int* ci, int m, int lane) {
+    TopList out;
+    out.clear();
+    for (int j = 0; j < m; ++j) {
+        float v = cv[0];
+#pragma unroll
+        for (int c = 1; c < C; ++c) v = fmaxf(v, cv[c]);
+        const float best = wave_max(v);
+        if (best == -INFINITY) break;
+        int i = 0x7fffffff;
+#pragma unroll
+        for (int c = 0; c < C; ++c) i = cv[c] == best ? min(i, ci[c]) : i;
+        const int at = wave_min(i);
+        if (lane == j) {
+            out.v = best;
+            out.i = at;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (ci[c] == at) cv[c] = -INFINITY;
+    }
+    return out;
+}
 
 // cnt sorted-or-not candidates (cv, ci) in LDS; the thread holding candidate c
 // writes it to rank's place in (ov, oi) when its rank is below m. Distinct

@@ -307,6 +307,27 @@ def _scratch(need, ws, device):
     return ws, ws.numel() * ws.element_size()
 
 
+class _On:
+    """Makes ``device`` current for a call, where it is not; gives the stream's handle."""
+
+    __slots__ = ("device", "guard")
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        index = self.device.index
+        self.guard = None
+        if torch.cuda.current_device() != index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return torch._C._cuda_getCurrentRawStream(index)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
 def _score_outputs(n, m, targets, device):
     new = torch.empty
     f32 = torch.float32
@@ -328,10 +349,10 @@ def logits_score(logits, targets=None, m: int = 0, scale: float = 1.0, ws=None) 
     t = _row(targets, n, "targets", torch.int32, dev)
     ws, nb = _scratch(lib.gmm_logits_score_workspace_bytes(n, v, m), ws, dev)
     out = _score_outputs(n, m, targets, dev)
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         _check(lib.gmm_logits_score(logits.data_ptr(), n, v, ldl, dt, t, m, scale, _ptr(out[0]),
                                     _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(out[4]),
-                                    ws.data_ptr(), nb, _stream(dev)))
+                                    ws.data_ptr(), nb, stream))
     return out
 
 
@@ -355,9 +376,9 @@ def logits_score_backward(logits, targets, norm, entropy=None, g_logprob=None, g
     t, h, gl, gh = (_row(a, n, nm, ty, dev) for a, nm, ty in (
         (targets, "targets", torch.int32), (entropy, "entropy", f32),
         (g_logprob, "g_logprob", f32), (g_entropy, "g_entropy", f32)))
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         _check(lib.gmm_logits_score_backward(logits.data_ptr(), n, v, ldl, dt, t, norm.data_ptr(), h,
-                                             gl, gh, scale, out.data_ptr(), ldo, _stream(dev)))
+                                             gl, gh, scale, out.data_ptr(), ldo, stream))
     return out
 
 
@@ -379,10 +400,10 @@ def head_score(hidden, weight, targets=None, m: int = 0, scale: float = 1.0, ws=
     t = _row(targets, n, "targets", torch.int32, dev)
     ws, nb = _scratch(lib.gmm_head_score_workspace_bytes(n, d, v, dt, m), ws, dev)
     out = _score_outputs(n, m, targets, dev)
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         _check(lib.gmm_head_score(hidden.data_ptr(), n, d, ldh, weight.data_ptr(), v, ldw, dt, t, m,
                                   scale, _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]),
-                                  _ptr(out[4]), ws.data_ptr(), nb, _stream(dev)))
+                                  _ptr(out[4]), ws.data_ptr(), nb, stream))
     return out
 
 
@@ -402,10 +423,10 @@ def head_score_backward(hidden, weight, targets, norm, entropy=None, g_logprob=N
     ws, nb = _scratch(lib.gmm_head_score_backward_workspace_bytes(n, d, v, dt), ws, dev)
     dh = torch.empty((n, d), dtype=hidden.dtype, device=dev)
     dw = torch.empty((v, d), dtype=weight.dtype, device=dev)
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         _check(lib.gmm_head_score_backward(hidden.data_ptr(), n, d, ldh, weight.data_ptr(), v, ldw, dt,
                                            t, norm.data_ptr(), h, gl, gh, scale, dh.data_ptr(), d,
-                                           dw.data_ptr(), d, ws.data_ptr(), nb, _stream(dev)))
+                                           dw.data_ptr(), d, ws.data_ptr(), nb, stream))
     return dh, dw
 
 
@@ -441,10 +462,10 @@ def moe_layer(x, w_in, w_out, gate=None, m: int = 2, share_all: bool = False, id
         idx = torch.empty((n, m), dtype=torch.int32, device=dev)
         resp = torch.empty((n, m), dtype=torch.float32, device=dev)
     y = torch.empty((n, d), dtype=x.dtype, device=dev)
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         _check(lib.gmm_moe_layer(x.data_ptr(), n, d, ldx, _ptr(gate), e, w_in.data_ptr(),
                                  w_out.data_ptr(), f, dt, m, int(share_all), idx.data_ptr(),
-                                 resp.data_ptr(), y.data_ptr(), d, ws.data_ptr(), nb, _stream(dev)))
+                                 resp.data_ptr(), y.data_ptr(), d, ws.data_ptr(), nb, stream))
     return y, idx, resp
 
 
