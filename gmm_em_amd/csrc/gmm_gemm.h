@@ -89,10 +89,14 @@ struct Gemm {
                                                  BUF_RSRC_WORD3);
     }
 
-    // the tile at rows m0 and columns n0, into acc
-    // (V8: bf16x8 or f16x8, the operands' type)
+    // Steps [first, last) of the tile at rows m0 and columns n0, into acc (V8: bf16x8 or
+    // f16x8, the operands' type; a step is GK values of one plane product).
+    // Each step is two halves of 32 values; a half's operands are read from LDS
+    // while the half before is multiplied, and a step's copies are issued when
+    // its buffer's last half has been read, a full step before they are needed.
     template <typename V8>
-    __device__ __forceinline__ void run(const GemmIn& in, int m0, int n0, unsigned char* lds) {
+    __device__ __forceinline__ void run(const GemmIn& in, int m0, int n0, int first, int last,
+                                        unsigned char* lds) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WN, wn = wave % WN;
@@ -102,9 +106,8 @@ struct Gemm {
 #pragma unroll
             for (int y = 0; y < TN; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
         const int ks = in.kp / GK;
-        const int steps = ks * in.pairs;
         const uint32_t ra = (uint32_t)in.lda * 2, rb = (uint32_t)in.ldb * 2;
-        int pair = 0, kk = 0;  // of the step to be copied next
+        int pair = first / ks, kk = first - pair * ks;  // of the step to be copied next
         auto issue = [&](int buf) {
             int pa, pb;
             gemm_pair(in.pairs, pair, &pa, &pb);
@@ -120,43 +123,53 @@ struct Gemm {
                 ++pair;
             }
         };
-        issue(0);
-        for (int s = 0; s < steps; ++s) {
-            __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of step s have landed
-            __syncthreads();                // ... and every wave's; the other buffer is free
-            if (s + 1 < steps) issue((s + 1) & 1);
-            const unsigned char* da = lds + (s & 1) * STAGE;
+        auto read = [&](V8(&fa)[TM], V8(&fb)[TN], int buf, int c) {
+            const unsigned char* da = lds + buf * STAGE;
             const unsigned char* db = da + A_BYTES;
 #pragma unroll
-            for (int c = 0; c < GK / 32; ++c) {
-                V8 fa[TM], fb[TN];
+            for (int x = 0; x < TM; ++x)
+                fa[x] = *(const V8*)(da + at((wm * TM + x) * 16 + i, 4 * c + h));
 #pragma unroll
-                for (int y = 0; y < TN; ++y)
-                    fb[y] = *(const V8*)(db + at((wn * TN + y) * 16 + i, 4 * c + h));
+            for (int y = 0; y < TN; ++y)
+                fb[y] = *(const V8*)(db + at((wn * TN + y) * 16 + i, 4 * c + h));
+        };
+        auto multiply = [&](const V8(&fa)[TM], const V8(&fb)[TN]) {
 #pragma unroll
-                for (int x = 0; x < TM; ++x)
-                    fa[x] = *(const V8*)(da + at((wm * TM + x) * 16 + i, 4 * c + h));
+            for (int x = 0; x < TM; ++x)
 #pragma unroll
-                for (int x = 0; x < TM; ++x)
-#pragma unroll
-                    for (int y = 0; y < TN; ++y)
-                        acc[x][y] = mfma32(fa[x], fb[y], acc[x][y]);
-            }
+                for (int y = 0; y < TN; ++y) acc[x][y] = mfma32(fa[x], fb[y], acc[x][y]);
+        };
+        const int steps = last - first;
+        issue(0);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (steps > 1) issue(1);
+        V8 fa[2][TM], fb[2][TN];
+        read(fa[0], fb[0], 0, 0);
+        for (int s = 0; s < steps; ++s) {
+            const int buf = s & 1;
+            read(fa[1], fb[1], buf, 1);
+            multiply(fa[0], fb[0]);
+            // this wave's copies of step s + 1 have landed and its reads of step s are done
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();  // ... and every wave's
+            if (s + 2 < steps) issue(buf);
+            if (s + 1 < steps) read(fa[0], fb[0], buf ^ 1, 0);
+            multiply(fa[1], fb[1]);
         }
         __syncthreads();  // LDS is free for the epilogue
     }
+    template <typename V8>
+    __device__ __forceinline__ void run(const GemmIn& in, int m0, int n0, unsigned char* lds) {
+        run<V8>(in, m0, n0, 0, in.kp / GK * in.pairs, lds);
+    }
 
-    // f(row in the tile of this lane's first of four rows, column, the four values)
-    template <typename F>
-    __device__ __forceinline__ void each(F f) const {
-        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-        const int wm = wave / WN, wn = wave % WN;
-        const int h = lane >> 4, i = lane & 15;
-#pragma unroll
-        for (int x = 0; x < TM; ++x)
-#pragma unroll
-            for (int y = 0; y < TN; ++y)
-                f((wm * TM + x) * 16 + 4 * h, (wn * TN + y) * 16 + i, acc[x][y]);
+    // row of this lane's first of four rows of blocks x, its column in blocks y
+    static __device__ __forceinline__ int row(int x) {
+        return ((threadIdx.x >> 6) / WN * TM + x) * 16 + 4 * ((threadIdx.x & 63) >> 4);
+    }
+    static __device__ __forceinline__ int col(int y) {
+        return ((threadIdx.x >> 6) % WN * TN + y) * 16 + (threadIdx.x & 15);
     }
 };
 

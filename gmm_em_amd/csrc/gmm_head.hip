@@ -13,6 +13,12 @@
 // dh = dx W and dW = dx^T h. For bf16 data dx is rounded to bf16, the type of
 // the matrix units' operands; for fp32 data it is kept in three planes like
 // the operands.
+//
+// Orientation: the tiles' rows are the axis that the outputs are contiguous in
+// (codes for logits, dims for the gradients), their columns the rows of h (or
+// the codes, for dW). A lane then holds four neighbouring values of an output
+// row at a time, and of only TN rows: a row's softmax statistics are sums
+// within a lane and over four lanes, and its constants stay in registers.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -30,8 +36,10 @@ constexpr int32_t HEAD_MAX_DIM = 1 << 20;
 constexpr int32_t HEAD_MAX_CODES = 1 << 22;  // row strides of dx: 32-bit tile offsets
 constexpr int64_t HEAD_MAX_LD = (int64_t)1 << 22;
 constexpr size_t HEAD_LOGIT_BYTES = (size_t)256 << 20;  // fp32 logits of one chunk of rows
-constexpr size_t HEAD_PART_BYTES = (size_t)256 << 20;   // tile statistics of one chunk
+constexpr size_t HEAD_PART_BYTES = (size_t)64 << 20;    // tile statistics of one chunk
 constexpr size_t HEAD_DX_BYTES = (size_t)1 << 30;       // dx of one chunk, both orders
+constexpr size_t HEAD_SPLIT_BYTES = (size_t)128 << 20;  // partial sums of a split product
+constexpr int HEAD_MAX_SPLIT = 16;
 
 // ---- operand planes
 
@@ -95,7 +103,7 @@ __global__ __launch_bounds__(256) void k_planes(const T* x, int64_t rows, int d,
 
 // ---- fp16's powers of two
 
-constexpr int RANGE_BLOCKS = 256;
+constexpr int RANGE_BLOCKS = 1024;
 
 // The exponent e for which a value with these magnitude bits, times 2^e, lies in
 // [2^14, 2^15); 0 for zero and for what is not finite.
@@ -229,11 +237,12 @@ __global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int 
 // ---- epilogues
 
 struct HeadArgs {
-    GemmIn in;
-    int32_t mt, nt;      // tiles
-    ScoreArgs s;         // rows of this chunk (s.n = in.m, s.v = in.n)
+    GemmIn in;           // a: codes, b: rows of h
+    int32_t mt, nt;      // tiles of codes and rows
+    int32_t rows;        // rows of this chunk (in.n)
+    ScoreArgs s;         // s.v = in.m
     float* x;            // logits or target logits of the chunk
-    ScorePart* part;     // [rows][nt]
+    ScorePart* part;     // [rows][mt]
     const float *norm, *entropy, *g_logprob, *g_entropy;
     uint16_t *dx, *dxt;  // planes [rows][vp], [v][np]
     int64_t plane_dx, plane_dxt;
@@ -254,7 +263,19 @@ __host__ __device__ __forceinline__ ScoreGradArgs grad_args(const HeadArgs& p) {
     return a;
 }
 
-// Statistics of each row over the tile's columns, and the targets' logits.
+// over the four lanes 16 apart that share a column of the accumulators
+__device__ __forceinline__ float max4(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum4(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// Statistics of each row over the tile's codes, and the targets' logits. Sums
+// are of 2^(c (x - max)) with c = scale log2 e: the exponential's argument in
+// one step from the accumulator; a is put back to base e at the end.
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
     using G = Gemm<BM, BN, WM, WN>;
@@ -265,50 +286,79 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
     G g;
     g.template run<bf16x8>(p.in, m0, n0, lds);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave / WN, wn = wave % WN, h = lane >> 4, i = lane & 15;
-    float* sh = (float*)lds;              // [WN][BM][3]
-    int* tg = (int*)(sh + WN * BM * 3);   // [BM] targets of the rows
-    if (tid < BM) tg[tid] = p.s.targets && m0 + tid < p.in.m ? p.s.targets[m0 + tid] : -1;
-    __syncthreads();
-    const int col0 = n0 + wn * G::TN * 16 + i;
+    float* sh = (float*)lds;  // [WM][BN][3]
+    const float c2 = p.s.scale * 1.44269504088896341f;
+    const bool edge = m0 + BM > p.in.m;  // some of the tile's codes are not there
+    const int code0 = m0 + G::row(0);
 #pragma unroll
-    for (int x = 0; x < G::TM; ++x) {
+    for (int y = 0; y < G::TN; ++y) {
+        const int r = n0 + G::col(y);
+        if (edge) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int r = (wm * G::TM + x) * 16 + 4 * h + q;
-            const int t = tg[r];
-            float mx = -INFINITY;
+            for (int x = 0; x < G::TM; ++x)
 #pragma unroll
-            for (int y = 0; y < G::TN; ++y) {
-                const int col = col0 + y * 16;
-                if (col == t && col < p.in.n) p.x[m0 + r] = g.acc[x][y][q];
-                mx = fmaxf(mx, col < p.in.n ? g.acc[x][y][q] : -INFINITY);
-            }
-            Stats st;
-            st.clear();
-            st.m = fmaxf(st.m, max16(mx) * p.s.scale);
+                for (int q = 0; q < 4; ++q)
+                    if (code0 + x * 16 + q >= p.in.m) g.acc[x][y][q] = -INFINITY;
+        }
+        float mx = -3.402823466e38f;
 #pragma unroll
-            for (int y = 0; y < G::TN; ++y)
-                if (col0 + y * 16 < p.in.n) st.add(fmaf(g.acc[x][y][q], p.s.scale, -st.m));
-            st.s = sum16(st.s);
-            st.a = sum16(st.a);
-            if (i == 0) {
-                float* o = sh + (wn * BM + r) * 3;
-                o[0] = st.m;
-                o[1] = st.s;
-                o[2] = st.a;
+        for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx = fmaxf(mx, g.acc[x][y][q]);
+        mx = max4(mx);
+        float s = 0.f, a = 0.f;
+        if (edge || mx < -1e30f) {
+            // masked codes: 0 * -inf stays 0
+#pragma unroll
+            for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float d = fmaxf((g.acc[x][y][q] - mx) * c2, -1000.f);
+                    const float e = g.acc[x][y][q] != g.acc[x][y][q] ? NAN : __builtin_amdgcn_exp2f(d);
+                    s += e;
+                    a = fmaf(e, d, a);
+                }
+        } else {
+            const float mc = mx * c2;
+#pragma unroll
+            for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float d = fmaf(g.acc[x][y][q], c2, -mc);
+                    const float e = __builtin_amdgcn_exp2f(d);
+                    s += e;
+                    a = fmaf(e, d, a);
+                }
+        }
+        s = sum4(s);
+        a = sum4(a) * 0.693147180559945309f;
+        if (lane < 16) {
+            float* o = sh + (wave / WN * BN + G::col(y)) * 3;
+            o[0] = mx * p.s.scale;
+            o[1] = s;
+            o[2] = a;
+        }
+        if (p.s.targets && r < p.in.n) {
+            const int t = p.s.targets[r], u = t - code0;
+            if (t < p.in.m && u >= 0 && u < 16 * G::TM && (u & 12) == 0) {
+                float v = 0.f;
+#pragma unroll
+                for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v = u == x * 16 + q ? g.acc[x][y][q] : v;
+                p.x[r] = v;
             }
         }
     }
     __syncthreads();
-    if (tid < BM && m0 + tid < p.in.m) {
+    if (tid < BN && n0 + tid < p.in.n) {
         Stats st{sh[tid * 3], sh[tid * 3 + 1], sh[tid * 3 + 2]};
 #pragma unroll
-        for (int w = 1; w < WN; ++w) {
-            const float* o = sh + (w * BM + tid) * 3;
+        for (int w = 1; w < WM; ++w) {
+            const float* o = sh + (w * BN + tid) * 3;
             st.join(o[0], o[1], o[2]);
         }
-        p.part[(int64_t)(m0 + tid) * p.nt + tn] = ScorePart{st.m, st.s, st.a};
+        p.part[(int64_t)(n0 + tid) * p.mt + tm] = ScorePart{st.m, st.s, st.a};
     }
 }
 
@@ -316,11 +366,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
 __global__ __launch_bounds__(256) void k_head_join(HeadArgs p) {
     const int lane = threadIdx.x & 63;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= p.in.m) return;
+    if (row >= p.rows) return;
     Stats st;
     st.clear();
-    for (int t = lane; t < p.nt; t += 64) {
-        const ScorePart q = p.part[row * p.nt + t];
+    for (int t = lane; t < p.mt; t += 64) {
+        const ScorePart q = p.part[row * p.mt + t];
         st.join(q.m, q.s, q.a);
     }
     st.wave_join();
@@ -337,79 +387,151 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_logits(HeadArgs p) {
     const int m0 = tm * BM, n0 = tn * BN;
     G g;
     g.template run<bf16x8>(p.in, m0, n0, lds);
-    g.each([&](int r, int c, f32x4 v) {
+    const bool fours = p.in.m % 4 == 0;  // rows start at 16-byte boundaries
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (m0 + r + q < p.in.m && n0 + c < p.in.n)
-                p.x[(int64_t)(m0 + r + q) * p.in.n + n0 + c] = v[q];
-    });
+    for (int y = 0; y < G::TN; ++y) {
+        const int r = n0 + G::col(y);
+        if (r >= p.in.n) continue;
+        float* o = p.x + (int64_t)r * p.in.m;
+#pragma unroll
+        for (int x = 0; x < G::TM; ++x) {
+            const int c = m0 + G::row(x);
+            if (fours) {
+                if (c < p.in.m) *(f32x4*)(o + c) = g.acc[x][y];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < p.in.m) o[c + q] = g.acc[x][y][q];
+            }
+        }
+    }
 }
 
-// dx of a chunk of rows, in both orders; 0 in the padding.
+// dx of a chunk of rows, in both orders; 0 in the padding. The order with rows
+// contiguous goes through LDS, one plane at a time, a row of codes after another.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
     using G = Gemm<BM, BN, WM, WN>;
     constexpr int P = Planes<T>::P;
-    __shared__ __align__(16) unsigned char lds[G::LDS];
+    constexpr bool F16 = std::is_same<T, uint16_t>::value;
+    constexpr int STR = BN * 2 + 16;  // bytes of a code's rows: four codes apart lie in other banks
+    __shared__ __align__(16) unsigned char lds[G::LDS > BM * STR ? G::LDS : BM * STR];
     int tm, tn;
     if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
     const int m0 = tm * BM, n0 = tn * BN;
     G g;
     g.template run<bf16x8>(p.in, m0, n0, lds);
-    constexpr bool F16 = std::is_same<T, uint16_t>::value;
-    GradRow* rows = (GradRow*)lds;
-    float* up = (float*)(rows + BM);  // [BM] the rows' powers of two
     const int tid = threadIdx.x;
     const float up_all = F16 ? ldexpf(1.f, range_exp(p.range)) : 1.f;
-    if (tid < BM && m0 + tid < p.in.m) {
-        rows[tid] = grad_row(grad_args(p), m0 + tid);
-        if (F16) up[tid] = ldexpf(1.f, p.row_exp[m0 + tid]);
-    }
-    __syncthreads();
-    g.each([&](int r, int c, f32x4 v) {
-        const int col = n0 + c;
-        if (col >= p.vp) return;
-        uint16_t o[P][4], ot[P][4];  // dx, and dx for the other order
+    const int code0 = m0 + G::row(0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const bool in = m0 + r + q < p.in.m && col < p.in.n;
-            const float y = in ? rows[r + q].at(v[q], col) : 0.f;
-            if (F16) {
-                o[0][q] = in ? f32_to_f16(y * up[r + q]) : 0;
-                ot[0][q] = f32_to_f16(y * up_all);
-            } else {
-                uint16_t cut[P];
-                Planes<T>::cut(y, cut);
+    for (int y = 0; y < G::TN; ++y) {
+        const int r = n0 + G::col(y);
+        const bool there = r < p.in.n;
+        GradRow k{};
+        float up = 1.f;
+        if (there) {
+            k = grad_row(grad_args(p), r);
+            if (F16) up = ldexpf(1.f, p.row_exp[r]);
+        }
+        const float base = fmaf(k.gh, k.h, k.glp);
 #pragma unroll
-                for (int k = 0; k < P; ++k) o[k][q] = ot[k][q] = cut[k];
+        for (int x = 0; x < G::TM; ++x) {
+            const int c = code0 + x * 16;
+            uint16_t o[P][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float lp = fmaf(g.acc[x][y][q], k.scale, -k.m) - k.logs;
+                const float pr = exp_neg(lp);
+                const float hot = c + q == k.t ? k.glp : 0.f;
+                float v = k.scale * fmaf(-pr, fmaf(k.gh, lp, base), hot);
+                if (!there || c + q >= p.in.m) v = 0.f;
+                g.acc[x][y][q] = v;
+                if (F16) {
+                    o[0][q] = f32_to_f16(v * up);
+                } else {
+                    uint16_t cut[P];
+                    Planes<T>::cut(v, cut);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) o[j][q] = cut[j];
+                }
             }
-        }
+            if (there && c < p.vp)  // vp is a multiple of 64: whole fours
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (m0 + r + q < p.in.m)
-                    p.dx[k * p.plane_dx + (int64_t)(m0 + r + q) * p.vp + col] = o[k][q];
-            if (col < p.in.n && m0 + r < p.np)  // np is a multiple of 64: whole fours
-                *(uint2*)(p.dxt + k * p.plane_dxt + (int64_t)col * p.np + m0 + r) =
-                    uint2{(uint32_t)ot[k][0] | ((uint32_t)ot[k][1] << 16),
-                          (uint32_t)ot[k][2] | ((uint32_t)ot[k][3] << 16)};
+                for (int j = 0; j < P; ++j)
+                    *(uint2*)(p.dx + j * p.plane_dx + (int64_t)r * p.vp + c) =
+                        uint2{(uint32_t)o[j][0] | ((uint32_t)o[j][1] << 16),
+                              (uint32_t)o[j][2] | ((uint32_t)o[j][3] << 16)};
         }
-    });
+    }
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        if (j > 0) __syncthreads();
+#pragma unroll
+        for (int y = 0; y < G::TN; ++y)
+#pragma unroll
+            for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint16_t cut[P];
+                    if (F16)
+                        cut[0] = f32_to_f16(g.acc[x][y][q] * up_all);
+                    else
+                        Planes<T>::cut(g.acc[x][y][q], cut);
+                    *(uint16_t*)(lds + (G::row(x) + q) * STR + G::col(y) * 2) = cut[j];
+                }
+        __syncthreads();
+        // 8 rows of a code per lane
+        for (int u = tid; u < BM * (BN / 8); u += 64 * WM * WN) {
+            const int c = u / (BN / 8), r = u % (BN / 8) * 8;
+            if (m0 + c < p.in.m && n0 + r < p.np)  // np is a multiple of 64
+                *(uint4*)(p.dxt + j * p.plane_dxt + (int64_t)(m0 + c) * p.np + n0 + r) =
+                    *(const uint4*)(lds + c * STR + r * 2);
+        }
+    }
 }
 
 struct GradOut {
-    GemmIn in;
+    GemmIn in;         // a: dims, b: rows of the output
     int32_t mt, nt;
-    const float* add;  // sum of the earlier chunks, m x n, or null
+    int32_t split;     // parts of the contracted axis: blockIdx.y
+    float* part;       // [split][n][m], split > 1
+    const float* add;  // sum of the earlier chunks, n x m, or null
     float* sum;        // where the sum so far goes, or null: the result goes to out
     void* out;
     int64_t ldo;
-    // fp16 operands: the powers of two that they were multiplied by, a's for
+    // fp16 operands: the powers of two that they were multiplied by, b's for
     // each row where row_exp is given
     const uint32_t *range_a, *range_b;
     const int32_t* row_exp;
 };
+
+// Four neighbouring values of row r from dim c on, summed over the split already.
+template <typename T>
+__device__ __forceinline__ void grad_store(const GradOut& p, int64_t r, int c, f32x4 v, int back) {
+    if (std::is_same<T, uint16_t>::value) {
+        const int e = p.row_exp ? back - p.row_exp[r] : back;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = ldexpf(v[q], e);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (c + q >= p.in.m) break;
+        float y = v[q];
+        if (p.add) y += p.add[r * p.in.m + c + q];
+        if (p.sum)
+            p.sum[r * p.in.m + c + q] = y;
+        else
+            ((T*)p.out)[r * p.ldo + c + q] = Vec<T>::store(y);
+    }
+}
+
+// the power of two to take out of a's and b's sums
+template <typename T>
+__device__ __forceinline__ int grad_back(const GradOut& p) {
+    if (!std::is_same<T, uint16_t>::value) return 0;
+    return -range_exp(p.range_a) - (p.row_exp ? 0 : range_exp(p.range_b));
+}
 
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
@@ -419,25 +541,52 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
     if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
     const int m0 = tm * BM, n0 = tn * BN;
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
+    const int steps = p.in.kp / GK * p.in.pairs;
+    const int z = blockIdx.y;
     G g;
-    g.template run<std::conditional_t<F16, f16x8, bf16x8>>(p.in, m0, n0, lds);
-    int back = 0;
-    if (F16) back = -range_exp(p.range_b) - (p.row_exp ? 0 : range_exp(p.range_a));
-    g.each([&](int r, int c, f32x4 v) {
+    g.template run<std::conditional_t<F16, f16x8, bf16x8>>(
+        p.in, m0, n0, (int)((int64_t)steps * z / p.split), (int)((int64_t)steps * (z + 1) / p.split),
+        lds);
+    const int back = p.split > 1 ? 0 : grad_back<T>(p);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t row = m0 + r + q;
-            const int col = n0 + c;
-            if (row >= p.in.m || col >= p.in.n) continue;
-            float y = v[q];
-            if (F16) y = ldexpf(y, p.row_exp ? back - p.row_exp[row] : back);
-            if (p.add) y += p.add[row * p.in.n + col];
-            if (p.sum)
-                p.sum[row * p.in.n + col] = y;
-            else
-                ((T*)p.out)[row * p.ldo + col] = Vec<T>::store(y);
+    for (int y = 0; y < G::TN; ++y) {
+        const int r = n0 + G::col(y);
+        if (r >= p.in.n) continue;
+#pragma unroll
+        for (int x = 0; x < G::TM; ++x) {
+            const int c = m0 + G::row(x);
+            if (c >= p.in.m) continue;
+            if (p.split > 1) {
+                float* o = p.part + ((int64_t)z * p.in.n + r) * p.in.m + c;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < p.in.m) o[q] = g.acc[x][y][q];
+            } else {
+                grad_store<T>(p, r, c, g.acc[x][y], back);
+            }
         }
-    });
+    }
+}
+
+// The sum over a split product's parts, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
+    const int back = grad_back<T>(p);
+    const int per = (p.in.m + 3) / 4;
+    const int64_t total = (int64_t)p.in.n * per;
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total;
+         j += (int64_t)gridDim.x * 256) {
+        const int64_t r = j / per;
+        const int c = (int)(j - r * per) * 4;
+        f32x4 v{0.f, 0.f, 0.f, 0.f};
+        for (int z = 0; z < p.split; ++z) {
+            const float* o = p.part + ((int64_t)z * p.in.n + r) * p.in.m + c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (c + q < p.in.m) v[q] += o[q];
+        }
+        grad_store<T>(p, r, c, v, back);
+    }
 }
 
 // ---- host side
@@ -445,27 +594,69 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
 static size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 static int pad(int64_t k) { return (int)((k + GK - 1) / GK * GK); }
 
-// Workgroups' tile: 256 x 256 where at least 200 of them fill the chip's 256
-// CUs, else 128 x 128.
-template <typename F>
-static void with_tile(int64_t m, int64_t n, F f) {
-    const int64_t big = ((m + 255) / 256) * ((n + 255) / 256);
-    if (big >= 200)
-        f(std::integral_constant<int, 256>());
-    else
-        f(std::integral_constant<int, 128>());
-}
-
-template <int B>
+// Workgroup tiles: codes or dims by rows.
+template <int ID>
 struct Tile;
 template <>
-struct Tile<256> {
+struct Tile<0> {
     static constexpr int BM = 256, BN = 256, WM = 2, WN = 4;
 };
 template <>
-struct Tile<128> {
+struct Tile<1> {
+    static constexpr int BM = 192, BN = 256, WM = 2, WN = 4;
+};
+template <>
+struct Tile<2> {
     static constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
 };
+template <>
+struct Tile<3> {
+    static constexpr int BM = 64, BN = 64, WM = 2, WN = 2;
+};
+
+// The tile and the split of the contracted axis that take least time by a
+// model of it: rounds of workgroups over the chip, each of a fixed part and a
+// part per step, and the writing and reading of a split's partial sums.
+// per_step: measured over long products, per workgroup with the chip full.
+struct TileCost {
+    int bm, bn, at_once;  // workgroups on the chip
+    float per_step, fixed;  // microseconds
+};
+constexpr TileCost TILE_COST[4] = {
+    {256, 256, 256, 1.42f, 6.f}, {192, 256, 256, 1.12f, 6.f}, {128, 128, 512, 0.92f, 4.f},
+    {64, 64, 1024, 0.55f, 3.f}};
+
+struct Choice {
+    int tile, split;
+};
+static Choice choose_tile(int64_t m, int64_t n, int64_t steps, int max_split) {
+    Choice best{0, 1};
+    double least = 1e300;
+    for (int t = 0; t < 4; ++t) {
+        const TileCost& c = TILE_COST[t];
+        const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
+        for (int s = 1; s <= max_split && s <= steps; ++s) {
+            if (s > 1 && (size_t)s * m * n * 4 > HEAD_SPLIT_BYTES) break;
+            const int64_t rounds = (tiles * s + c.at_once - 1) / c.at_once;
+            double us = rounds * (c.fixed + c.per_step * (double)((steps + s - 1) / s));
+            if (s > 1) us += 4.0 + (double)m * n * 8 * s / 4.0e6;
+            if (us < least) {
+                least = us;
+                best = Choice{t, s};
+            }
+        }
+    }
+    return best;
+}
+template <typename F>
+static void with_tile(int tile, F f) {
+    switch (tile) {
+        case 0: f(std::integral_constant<int, 0>()); break;
+        case 1: f(std::integral_constant<int, 1>()); break;
+        case 2: f(std::integral_constant<int, 2>()); break;
+        default: f(std::integral_constant<int, 3>()); break;
+    }
+}
 
 // Workspace of a head call: operands that need laying out, then the chunk's
 // scratch. Offsets in bytes; a part that is not needed takes none.
@@ -473,7 +664,7 @@ struct HeadPlan {
     int planes, pairs, dp, vp, np;
     int64_t chunk;      // rows per chunk, a multiple of 256
     bool pack_h, pack_w;
-    size_t o_w, o_h, o_x, o_part, o_wt, o_ht, o_dx, o_dxt, o_sum, o_score, o_range, o_exp, bytes;
+    size_t o_w, o_h, o_x, o_part, o_wt, o_ht, o_dx, o_dxt, o_sum, o_split, o_score, o_range, o_exp, bytes;
 };
 
 static bool direct(const void* p, int32_t d, int64_t ld, int dtype) {
@@ -492,7 +683,7 @@ static HeadPlan head_plan(int64_t n, int32_t d, int32_t v, int dtype, int32_t m,
     q.vp = pad(v);
     q.pack_h = pack_h;
     q.pack_w = pack_w;
-    const int64_t tiles = (v + 127) / 128;
+    const int64_t tiles = (v + 63) / 64;
     size_t row, most;
     if (grad) {
         row = (size_t)q.planes * q.vp * 4;
@@ -527,6 +718,8 @@ static HeadPlan head_plan(int64_t n, int32_t d, int32_t v, int dtype, int32_t m,
     q.o_dx = take(grad ? ps * c * q.vp : 0);
     q.o_dxt = take(grad ? ps * v * q.np : 0);
     q.o_sum = take(grad && q.chunk < n ? (size_t)v * d * 4 : 0);
+    const size_t most_out = (size_t)(q.chunk > v ? q.chunk : v) * d * 4 * HEAD_MAX_SPLIT;
+    q.o_split = take(grad ? (most_out < HEAD_SPLIT_BYTES ? most_out : HEAD_SPLIT_BYTES) : 0);
     const bool f16 = grad && dtype == GMM_BF16;
     q.o_range = take(f16 ? 3 * RANGE_BLOCKS * sizeof(uint32_t) : 0);
     q.o_exp = take(f16 ? (size_t)n * sizeof(int32_t) : 0);
@@ -561,12 +754,30 @@ static unsigned tile_grid(int mt, int nt) {
     return (unsigned)(((int64_t)mt * nt + 7) / 8 * 8);
 }
 
-template <int B, typename K, typename A>
-static void launch_tiles(K kernel, A& a, hipStream_t st) {
-    using C = Tile<B>;
+template <int ID, typename K, typename A>
+static void launch_tiles(K kernel, A& a, int split, hipStream_t st) {
+    using C = Tile<ID>;
     a.mt = (a.in.m + C::BM - 1) / C::BM;
     a.nt = (a.in.n + C::BN - 1) / C::BN;
-    hipLaunchKernelGGL(kernel, dim3(tile_grid(a.mt, a.nt)), dim3(64 * C::WM * C::WN), 0, st, a);
+    hipLaunchKernelGGL(kernel, dim3(tile_grid(a.mt, a.nt), split), dim3(64 * C::WM * C::WN), 0, st, a);
+}
+
+// out = the product of o.in, with the tile and split that suit it.
+template <typename T>
+static void launch_grad(GradOut& o, float* part, hipStream_t st) {
+    const Choice c = choose_tile(o.in.m, o.in.n, (int64_t)o.in.kp / GK * o.in.pairs, HEAD_MAX_SPLIT);
+    o.split = c.split;
+    o.part = part;
+    with_tile(c.tile, [&](auto b) {
+        constexpr int B = decltype(b)::value;
+        using C = Tile<B>;
+        launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, c.split, st);
+    });
+    if (c.split > 1) {
+        const int64_t work = ((int64_t)o.in.n * ((o.in.m + 3) / 4) + 255) / 256;
+        hipLaunchKernelGGL((k_head_sum<T>), dim3((unsigned)(work < 16384 ? work : 16384)), dim3(256), 0,
+                           st, o);
+    }
 }
 
 struct HeadIn {
@@ -580,30 +791,31 @@ template <typename T>
 static void head_weight(const HeadIn& x, const HeadPlan& q, char* ws, GemmIn* g, hipStream_t st) {
     g->pairs = q.pairs;
     g->kp = q.dp;
-    g->n = x.v;
+    g->m = x.v;
     if (q.pack_w) {
-        g->b = (const uint16_t*)(ws + q.o_w);
-        g->ldb = q.dp;
-        g->plane_b = (int64_t)x.v * q.dp;
-        planes<T>(x.w, x.v, x.d, x.ldw, q.dp, ws + q.o_w, g->plane_b, st);
+        g->a = (const uint16_t*)(ws + q.o_w);
+        g->lda = q.dp;
+        g->plane_a = (int64_t)x.v * q.dp;
+        planes<T>(x.w, x.v, x.d, x.ldw, q.dp, ws + q.o_w, g->plane_a, st);
     } else {
-        g->b = (const uint16_t*)x.w;
-        g->ldb = x.ldw;
+        g->a = (const uint16_t*)x.w;
+        g->lda = x.ldw;
     }
 }
 template <typename T>
-static void head_rows(const HeadIn& x, const HeadPlan& q, char* ws, int64_t r0, int64_t rows, GemmIn* g,
+static void head_rows(const HeadIn& x, const HeadPlan& q, char* ws, int64_t r0, int64_t rows, HeadArgs* a,
                       hipStream_t st) {
     const T* h = (const T*)x.h + r0 * x.ldh;
-    g->m = (int32_t)rows;
+    GemmIn* g = &a->in;
+    g->n = a->rows = (int32_t)rows;
     if (q.pack_h) {
-        g->a = (const uint16_t*)(ws + q.o_h);
-        g->lda = q.dp;
-        g->plane_a = q.chunk * q.dp;
-        planes<T>(h, rows, x.d, x.ldh, q.dp, ws + q.o_h, g->plane_a, st);
+        g->b = (const uint16_t*)(ws + q.o_h);
+        g->ldb = q.dp;
+        g->plane_b = q.chunk * q.dp;
+        planes<T>(h, rows, x.d, x.ldh, q.dp, ws + q.o_h, g->plane_b, st);
     } else {
-        g->a = (const uint16_t*)h;
-        g->lda = x.ldh;
+        g->b = (const uint16_t*)h;
+        g->ldb = x.ldh;
     }
 }
 
@@ -616,7 +828,7 @@ static hipError_t head_score(const HeadIn& x, const HeadPlan& q, ScoreArgs s, ch
     a.part = (ScorePart*)(ws + q.o_part);
     for (int64_t r0 = 0; r0 < x.n; r0 += q.chunk) {
         const int64_t rows = x.n - r0 < q.chunk ? x.n - r0 : q.chunk;
-        head_rows<T>(x, q, ws, r0, rows, &a.in, st);
+        head_rows<T>(x, q, ws, r0, rows, &a, st);
         a.s = s;
         a.s.n = rows;
         if (s.targets) {
@@ -629,13 +841,14 @@ static hipError_t head_score(const HeadIn& x, const HeadPlan& q, ScoreArgs s, ch
             a.s.top_idx = s.top_idx + r0 * s.m;
             a.s.top_logprob = s.top_logprob + r0 * s.m;
         }
-        with_tile(rows, x.v, [&](auto b) {
+        const Choice c = choose_tile(x.v, rows, (int64_t)q.dp / GK * q.pairs, 1);
+        with_tile(c.tile, [&](auto b) {
             constexpr int B = decltype(b)::value;
             using C = Tile<B>;
             if (s.m > 0)
-                launch_tiles<B>(k_head_logits<C::BM, C::BN, C::WM, C::WN>, a, st);
+                launch_tiles<B>(k_head_logits<C::BM, C::BN, C::WM, C::WN>, a, 1, st);
             else
-                launch_tiles<B>(k_head_stats<C::BM, C::BN, C::WM, C::WN>, a, st);
+                launch_tiles<B>(k_head_stats<C::BM, C::BN, C::WM, C::WN>, a, 1, st);
         });
         if (s.m > 0) {
             ScoreArgs l = a.s;
@@ -659,6 +872,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
     uint16_t* ht = (uint16_t*)(ws + q.o_ht);
     uint32_t* range = (uint32_t*)(ws + q.o_range);  // W, h, dx
     int32_t* row_exp = (int32_t*)(ws + q.o_exp);
+    float* part = (float*)(ws + q.o_split);
     if (std::is_same<T, uint16_t>::value) {
         RangeArgs r{};
         r.h = (const uint16_t*)x.h;
@@ -682,7 +896,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
     const HeadArgs all = a;
     for (int64_t r0 = 0; r0 < x.n; r0 += q.chunk) {
         const int64_t rows = x.n - r0 < q.chunk ? x.n - r0 : q.chunk;
-        head_rows<T>(x, q, ws, r0, rows, &a.in, st);
+        head_rows<T>(x, q, ws, r0, rows, &a, st);
         a.np = pad(rows);
         a.row_exp = row_exp + r0;
         a.plane_dxt = (int64_t)x.v * a.np;
@@ -691,42 +905,35 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         a.entropy = all.entropy ? all.entropy + r0 : nullptr;
         a.g_logprob = all.g_logprob ? all.g_logprob + r0 : nullptr;
         a.g_entropy = all.g_entropy ? all.g_entropy + r0 : nullptr;
-        with_tile(rows, x.v, [&](auto b) {
+        const Choice c = choose_tile(x.v, rows, (int64_t)q.dp / GK * q.pairs, 1);
+        with_tile(c.tile, [&](auto b) {
             constexpr int B = decltype(b)::value;
             using C = Tile<B>;
-            launch_tiles<B>(k_head_dx<T, C::BM, C::BN, C::WM, C::WN>, a, st);
+            launch_tiles<B>(k_head_dx<T, C::BM, C::BN, C::WM, C::WN>, a, 1, st);
         });
         if (dh) {
             GradOut o{};
-            o.in = GemmIn{a.dx, wt, q.vp, q.vp, a.plane_dx, plane_wt, (int32_t)rows, x.d, q.vp,
+            o.in = GemmIn{wt, a.dx, q.vp, q.vp, plane_wt, a.plane_dx, x.d, (int32_t)rows, q.vp,
                           q.pairs};
             o.out = (T*)dh + r0 * lddh;
             o.ldo = lddh;
-            o.range_b = range;
+            o.range_a = range;
             o.row_exp = row_exp + r0;
-            with_tile(rows, x.d, [&](auto b) {
-                constexpr int B = decltype(b)::value;
-                using C = Tile<B>;
-                launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, st);
-            });
+            launch_grad<T>(o, part, st);
         }
         if (dw) {
-            planes_t<T>((const T*)x.h + r0 * x.ldh, rows, x.d, x.ldh, a.np,
-                        range + RANGE_BLOCKS, ht, plane_ht, st);
+            planes_t<T>((const T*)x.h + r0 * x.ldh, rows, x.d, x.ldh, a.np, range + RANGE_BLOCKS, ht,
+                        plane_ht, st);
             GradOut o{};
-            o.in = GemmIn{a.dxt, ht, a.np, a.np, a.plane_dxt, plane_ht, x.v, x.d, a.np, q.pairs};
+            o.in = GemmIn{ht, a.dxt, a.np, a.np, plane_ht, a.plane_dxt, x.d, x.v, a.np, q.pairs};
             float* sum = (float*)(ws + q.o_sum);
             o.add = r0 > 0 ? sum : nullptr;
             o.sum = r0 + q.chunk < x.n ? sum : nullptr;
             o.out = dw;
             o.ldo = lddw;
-            o.range_a = range + 2 * RANGE_BLOCKS;
-            o.range_b = range + RANGE_BLOCKS;
-            with_tile(x.v, x.d, [&](auto b) {
-                constexpr int B = decltype(b)::value;
-                using C = Tile<B>;
-                launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, st);
-            });
+            o.range_a = range + RANGE_BLOCKS;
+            o.range_b = range + 2 * RANGE_BLOCKS;
+            launch_grad<T>(o, part, st);
         }
     }
     return hipGetLastError();

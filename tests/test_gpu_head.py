@@ -99,9 +99,12 @@ def test_rows_of_any_stride(ops, dtype):
 
 
 def test_chunks_of_rows(ops):
-    # more rows than one chunk holds: statistics (174,592), logits (1,024 of 65,536 codes)
+    # many rows; then more rows than one chunk holds: statistics (5,376 rows of
+    # 65,536 codes in 64 MiB), logits (1,024 in 256 MiB)
     h, w, t = _inputs(200_003, 64, 130, torch.bfloat16, 4)
     _check(ops, h, w, t, 0, 1.0, "chunks")
+    h, w, t = _inputs(5700, 64, 65_536, torch.bfloat16, 14)
+    _check(ops, h, w, t, 0, 1.0, "chunks of statistics")
     h, w, t = _inputs(2500, 64, 65_536, torch.bfloat16, 5, grid=True)
     _check(ops, h, w, t, 2, 1.0, "chunks of logits")
 
