@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gmm_device.h"
 
 namespace gmm {
@@ -56,6 +58,7 @@ struct Gemm {
     static constexpr int A_BYTES = BM * GK * 2, B_BYTES = BN * GK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int LDS = 2 * STAGE;
+    static constexpr int COPIES = STAGE / 1024 / (NT / 64);  // per wave and step
 
     f32x4 acc[TM][TN];
 
@@ -94,6 +97,10 @@ struct Gemm {
     // Each step is two halves of 32 values; a half's operands are read from LDS
     // while the half before is multiplied, and a step's copies are issued when
     // its buffer's last half has been read, a full step before they are needed.
+    // Measured without epilogue, 256 x 256 tiles: 8192^3 746 us (1474 TFLOP/s),
+    // 16384 x 8192 x 768 148 us (1389); with the wait left to the scheduler, which
+    // moves it before the products, 164 us; with the copies and reads in front of
+    // the products instead of between them 180 us.
     template <typename V8>
     __device__ __forceinline__ void run(const GemmIn& in, int m0, int n0, int first, int last,
                                         unsigned char* lds) {
@@ -139,6 +146,20 @@ struct Gemm {
 #pragma unroll
                 for (int y = 0; y < TN; ++y) acc[x][y] = mfma32(fa[x], fb[y], acc[x][y]);
         };
+        // the order of a half: its copies and LDS reads one by one between the products
+        auto spread = [&](const int copies) {
+#pragma unroll
+            for (int g = 0; g < copies; ++g) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // matrix product
+                __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // memory read
+            }
+#pragma unroll
+            for (int g = 0; g < TM + TN; ++g) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x8, TM * TN, 0);
+        };
         const int steps = last - first;
         issue(0);
         __builtin_amdgcn_s_waitcnt(0);
@@ -146,17 +167,34 @@ struct Gemm {
         if (steps > 1) issue(1);
         V8 fa[2][TM], fb[2][TN];
         read(fa[0], fb[0], 0, 0);
-        for (int s = 0; s < steps; ++s) {
-            const int buf = s & 1;
+        // one step; ahead: steps that follow it (2: at least two)
+        auto step = [&](int buf, auto ahead) {
+            constexpr int AHEAD = decltype(ahead)::value;
             read(fa[1], fb[1], buf, 1);
             multiply(fa[0], fb[0]);
-            // this wave's copies of step s + 1 have landed and its reads of step s are done
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();  // ... and every wave's
-            if (s + 2 < steps) issue(buf);
-            if (s + 1 < steps) read(fa[0], fb[0], buf ^ 1, 0);
+            spread(0);
+            // the wait stays behind the products: the copies of step s + 1 have
+            // had a whole step to land
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (AHEAD > 0) {
+                // this wave's copies of step s + 1 have landed, its reads of step s are done
+                __builtin_amdgcn_s_waitcnt(0);
+                __syncthreads();  // ... and every wave's
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (AHEAD > 1) issue(buf);
+                read(fa[0], fb[0], buf ^ 1, 0);
+            }
             multiply(fa[1], fb[1]);
+            if constexpr (AHEAD > 0) spread(AHEAD > 1 ? COPIES : 0);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int s = 0;
+        for (; s + 2 < steps; ++s) step(s & 1, std::integral_constant<int, 2>());
+        if (s + 1 < steps) {
+            step(s & 1, std::integral_constant<int, 1>());
+            ++s;
         }
+        step(s & 1, std::integral_constant<int, 0>());
         __syncthreads();  // LDS is free for the epilogue
     }
     template <typename V8>
