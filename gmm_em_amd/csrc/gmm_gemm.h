@@ -9,7 +9,9 @@
 //
 // A workgroup of WM x WN waves computes a BM x BN tile, 64 of the contracted
 // axis per step: both operands' steps are copied from memory straight into LDS
-// (two buffers; the next step's copies run under this step's products), 128
+// (two buffers; the next step's copies run under this step's products; the
+// buffers are variables of their own, so that the compiler sees that a read of one does
+// not wait for the copies into the other), 128
 // bytes a row, its 16-byte pieces rotated by the row (piece p of row r lies at
 // p ^ (r & 7)), so that the 16 rows that a wave reads at once lie in different
 // banks. Rows past the operand's last read as 0 (the buffer's range check).
@@ -36,9 +38,13 @@ __device__ __forceinline__ f32x4 mfma32(f16x8 a, f16x8 b, f32x4 c) {
 
 constexpr int GK = 64;  // contracted values per step
 
+// An operand is either rows as a caller has them (row stride ld, GK values from one
+// step to the next) or panels: the GK values of a step of all rows lie together
+// (row stride GK), so that a tile's step is one piece of memory.
 struct GemmIn {
-    const uint16_t *a, *b;       // planes of M x kp and N x kp values, 16 bits each
+    const uint16_t *a, *b;       // M x kp and N x kp values, 16 bits each
     int64_t lda, ldb;            // row strides (values)
+    int64_t step_a, step_b;      // from one step to the next (values)
     int64_t plane_a, plane_b;    // plane strides (values)
     int32_t m, n, kp;            // kp: contracted length, a multiple of GK
     int32_t pairs;               // plane products: 1 or 6
@@ -51,13 +57,13 @@ __device__ __forceinline__ void gemm_pair(int pairs, int p, int* pa, int* pb) {
     *pb = (0x118 >> (2 * q)) & 3;  // 0 2 1 0 1 0
 }
 
-template <int BM, int BN, int WM, int WN>
+// ONE: operands of one plane.
+template <int BM, int BN, int WM, int WN, bool ONE>
 struct Gemm {
     static constexpr int NT = 64 * WM * WN;
     static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
     static constexpr int A_BYTES = BM * GK * 2, B_BYTES = BN * GK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int LDS = 2 * STAGE;
     static constexpr int COPIES = STAGE / 1024 / (NT / 64);  // per wave and step
 
     f32x4 acc[TM][TN];
@@ -67,33 +73,67 @@ struct Gemm {
 
     // copies BR rows of one step: wave w takes every NT / 64-th group of 8 rows
     template <int BR>
-    static __device__ __forceinline__ void copy(__amdgpu_buffer_rsrc_t rs, uint32_t row_bytes, int k,
+    static __device__ __forceinline__ void copy(__amdgpu_buffer_rsrc_t rs, uint32_t row_bytes,
                                                 unsigned char* dst, int wave, int lane) {
+        // row (8 grp + r) & 7 == r: the piece that belongs at place p is p ^ r
         const int r = lane >> 3, p = lane & 7;
+        const uint32_t off = (uint32_t)(wave * 8 + r) * row_bytes + (uint32_t)((p ^ r) << 4);
 #pragma unroll
-        for (int g = 0; g < BR / 8 / (NT / 64); ++g) {
-            const int grp = g * (NT / 64) + wave;
-            // row (8 grp + r) & 7 == r: the piece that belongs at place p is p ^ r
-            const uint32_t off = (uint32_t)(grp * 8 + r) * row_bytes + (uint32_t)((p ^ r) << 4);
+        for (int g = 0; g < BR / 8 / (NT / 64); ++g)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rs, (__attribute__((address_space(3))) void*)(dst + grp * 1024), 16, (int)off,
-                k * 2, 0, 0);
-        }
+                rs, (__attribute__((address_space(3))) void*)(dst + (g * (NT / 64) + wave) * 1024), 16,
+                (int)(off + g * (NT / 8) * row_bytes), 0, 0, 0);
     }
 
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const uint16_t* base, int64_t ld,
-                                                                  int64_t r0, int64_t total, int br,
-                                                                  int kp) {
-        const int64_t left = total - r0;
-        const int64_t cnt = left < br ? left : br;
-        // the last row ends at its kp-th value
-        const int64_t bytes = cnt > 0 ? ((cnt - 1) * ld + kp) * 2 : 0;
-        return __builtin_amdgcn_make_buffer_rsrc((void*)(base + r0 * ld), (short)0, (int)bytes,
-                                                 BUF_RSRC_WORD3);
+    const uint16_t *next_a, *next_b;  // the step to be copied next, from the tile's first row
+    int bytes_a, bytes_b;             // from there to the end of the step's last row
+    int steps;                        // of the tile
+    int left, pair;                   // steps left in the plane product, its number
+
+    static __device__ __forceinline__ int span(int64_t ld, int r0, int total, int br) {
+        const int cnt = total - r0 < br ? total - r0 : br;
+        return cnt > 0 ? (int)(((int64_t)(cnt - 1) * ld + GK) * 2) : 0;
     }
 
-    // Steps [first, last) of the tile at rows m0 and columns n0, into acc (V8: bf16x8 or
-    // f16x8, the operands' type; a step is GK values of one plane product).
+    // copies the next step into the buffer at d; m, n: the tile; real: there is a next
+    // step (else nothing is read: every place is past the end)
+    __device__ __forceinline__ void issue(const GemmIn& in, int m, int n, bool real, unsigned char* d) {
+        const int lane = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        copy<BM>(__builtin_amdgcn_make_buffer_rsrc((void*)next_a, (short)0, real ? bytes_a : 0, BUF_RSRC_WORD3),
+                 (uint32_t)in.lda * 2, d, wave, lane);
+        copy<BN>(__builtin_amdgcn_make_buffer_rsrc((void*)next_b, (short)0, real ? bytes_b : 0, BUF_RSRC_WORD3),
+                 (uint32_t)in.ldb * 2, d + A_BYTES, wave, lane);
+        next_a += in.step_a;
+        next_b += in.step_b;
+        if constexpr (!ONE)
+            if (--left == 0) seek(in, m, n, pair + 1, 0);
+    }
+    __device__ __forceinline__ void seek(const GemmIn& in, int m, int n, int p, int kk) {
+        int pa, pb;
+        gemm_pair(ONE ? 1 : in.pairs, p, &pa, &pb);
+        next_a = in.a + pa * in.plane_a + kk * in.step_a + m * in.lda;
+        next_b = in.b + pb * in.plane_b + kk * in.step_b + n * in.ldb;
+        pair = p;
+        left = in.kp / GK - kk;
+    }
+
+    // Starts steps [first, last) of the tile at rows m and columns n: their first two
+    // are copied into l0 and l1, STAGE bytes each (free, by the caller's barrier). A
+    // step is GK values of one plane product.
+    __device__ __forceinline__ void begin(const GemmIn& in, int m, int n, int first, int last,
+                                          unsigned char* l0, unsigned char* l1) {
+        const int ks = in.kp / GK;
+        steps = last - first;
+        bytes_a = span(in.lda, m, in.m, BM);
+        bytes_b = span(in.ldb, n, in.n, BN);
+        seek(in, m, n, first / ks, first % ks);
+        issue(in, m, n, true, l0);
+        issue(in, m, n, steps > 1, l1);
+    }
+
+    // The products of the steps begun, into acc (V8: bf16x8 or f16x8, the operands'
+    // type); LDS is free afterwards.
     // Each step is two halves of 32 values; a half's operands are read from LDS
     // while the half before is multiplied, and a step's copies are issued when
     // its buffer's last half has been read, a full step before they are needed.
@@ -102,8 +142,8 @@ struct Gemm {
     // moves it before the products, 164 us; with the copies and reads in front of
     // the products instead of between them 180 us.
     template <typename V8>
-    __device__ __forceinline__ void run(const GemmIn& in, int m0, int n0, int first, int last,
-                                        unsigned char* lds) {
+    __device__ __forceinline__ void finish(const GemmIn& in, int m, int n, unsigned char* l0,
+                                           unsigned char* l1) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WN, wn = wave % WN;
@@ -112,26 +152,7 @@ struct Gemm {
         for (int x = 0; x < TM; ++x)
 #pragma unroll
             for (int y = 0; y < TN; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int ks = in.kp / GK;
-        const uint32_t ra = (uint32_t)in.lda * 2, rb = (uint32_t)in.ldb * 2;
-        int pair = first / ks, kk = first - pair * ks;  // of the step to be copied next
-        auto issue = [&](int buf) {
-            int pa, pb;
-            gemm_pair(in.pairs, pair, &pa, &pb);
-            const __amdgpu_buffer_rsrc_t sa =
-                rows(in.a + pa * in.plane_a, in.lda, m0, in.m, BM, in.kp);
-            const __amdgpu_buffer_rsrc_t sb =
-                rows(in.b + pb * in.plane_b, in.ldb, n0, in.n, BN, in.kp);
-            unsigned char* d = lds + buf * STAGE;
-            copy<BM>(sa, ra, kk * GK, d, wave, lane);
-            copy<BN>(sb, rb, kk * GK, d + A_BYTES, wave, lane);
-            if (++kk == ks) {
-                kk = 0;
-                ++pair;
-            }
-        };
-        auto read = [&](V8(&fa)[TM], V8(&fb)[TN], int buf, int c) {
-            const unsigned char* da = lds + buf * STAGE;
+        auto read = [&](V8(&fa)[TM], V8(&fb)[TN], const unsigned char* da, int c) {
             const unsigned char* db = da + A_BYTES;
 #pragma unroll
             for (int x = 0; x < TM; ++x)
@@ -160,47 +181,38 @@ struct Gemm {
             }
             __builtin_amdgcn_sched_group_barrier(0x8, TM * TN, 0);
         };
-        const int steps = last - first;
-        issue(0);
-        __builtin_amdgcn_s_waitcnt(0);
+        // the first step's copies have landed; the second's may be in flight
+        __builtin_amdgcn_s_waitcnt((COPIES & 15) | (7 << 4) | (15 << 8) | ((COPIES >> 4) << 14));
         __syncthreads();
-        if (steps > 1) issue(1);
         V8 fa[2][TM], fb[2][TN];
-        read(fa[0], fb[0], 0, 0);
-        // one step; ahead: steps that follow it (2: at least two)
-        auto step = [&](int buf, auto ahead) {
-            constexpr int AHEAD = decltype(ahead)::value;
-            read(fa[1], fb[1], buf, 1);
+        read(fa[0], fb[0], l0, 0);
+        int togo = steps;
+        // one step, in buffer cur. The last steps copy nothing and read a buffer that
+        // is not multiplied: one body for all.
+        auto step = [&](unsigned char* cur, unsigned char* other) {
+            read(fa[1], fb[1], cur, 1);
             multiply(fa[0], fb[0]);
             spread(0);
             // the wait stays behind the products: the copies of step s + 1 have
             // had a whole step to land
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (AHEAD > 0) {
-                // this wave's copies of step s + 1 have landed, its reads of step s are done
-                __builtin_amdgcn_s_waitcnt(0);
-                __syncthreads();  // ... and every wave's
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (AHEAD > 1) issue(buf);
-                read(fa[0], fb[0], buf ^ 1, 0);
-            }
-            multiply(fa[1], fb[1]);
-            if constexpr (AHEAD > 0) spread(AHEAD > 1 ? COPIES : 0);
+            // this wave's copies of step s + 1 have landed, its reads of step s are done
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();  // ... and every wave's
             __builtin_amdgcn_sched_barrier(0);
+            issue(in, m, n, togo > 2, cur);
+            read(fa[0], fb[0], other, 0);
+            multiply(fa[1], fb[1]);
+            spread(COPIES);
+            __builtin_amdgcn_sched_barrier(0);
+            return --togo > 0;
         };
-        int s = 0;
-        for (; s + 2 < steps; ++s) step(s & 1, std::integral_constant<int, 2>());
-        if (s + 1 < steps) {
-            step(s & 1, std::integral_constant<int, 1>());
-            ++s;
+        while (step(l0, l1) && step(l1, l0)) {
         }
-        step(s & 1, std::integral_constant<int, 0>());
+        __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();  // LDS is free for the epilogue
     }
-    template <typename V8>
-    __device__ __forceinline__ void run(const GemmIn& in, int m0, int n0, unsigned char* lds) {
-        run<V8>(in, m0, n0, 0, in.kp / GK * in.pairs, lds);
-    }
+    static __device__ __forceinline__ int all_steps(const GemmIn& in) { return in.kp / GK * in.pairs; }
 
     // row of this lane's first of four rows of blocks x, its column in blocks y
     static __device__ __forceinline__ int row(int x) {
@@ -211,21 +223,45 @@ struct Gemm {
     }
 };
 
-// Tile of workgroup b among mt x nt: the workgroups that one XCD receives
-// (every eighth) take neighbouring tiles, walked in bands of 8 tile rows, so
-// that its L2 serves their shared rows of A and B. The grid has 8 ceil(mt nt / 8)
-// workgroups; false: none.
-__device__ __forceinline__ bool gemm_tile(int64_t b, int mt, int nt, int* tm, int* tn) {
-    const int64_t total = (int64_t)mt * nt, per = (total + 7) / 8;
-    const int64_t id = (b & 7) * per + (b >> 3);
+// Tile b of a walk over mt x nt tiles: the tiles that one XCD receives (every
+// eighth b) are neighbours, walked in bands of 8 tile rows, so that its L2 serves their
+// shared rows of A and B. b runs over 8 ceil(mt nt / 8) values; false: no tile.
+__device__ __forceinline__ bool gemm_tile(uint32_t b, uint32_t mt, uint32_t nt, int* tm, int* tn) {
+    const uint32_t total = mt * nt, per = (total + 7) / 8;
+    const uint32_t id = (b & 7) * per + (b >> 3);
     if ((b >> 3) >= per || id >= total) return false;
-    const int64_t band = (int64_t)8 * nt;
-    const int b0 = (int)(id / band) * 8;
-    const int rows = mt - b0 < 8 ? mt - b0 : 8;
-    const int64_t in = id - (int64_t)b0 * nt;
-    *tm = b0 + (int)(in % rows);
+    const uint32_t band = id / (8 * nt), in = id - band * 8 * nt;
+    const uint32_t rows = mt - band * 8 < 8 ? mt - band * 8 : 8;
+    *tm = (int)(band * 8 + in % rows);
     *tn = (int)(in / rows);
     return true;
+}
+
+// Runs epilogue(g, m0, n0) for this workgroup's tiles (workgroup, + grid, + 2 grids, ...;
+// the grid is a multiple of 8); the next tile's first copies run under a tile's
+// epilogue, which therefore has LDS of its own. m0, n0: the epilogue's tile.
+template <typename V8, typename G, int BM, int BN, typename F>
+__device__ __forceinline__ void gemm_walk(const GemmIn& in, int mt, int nt, unsigned char* l0,
+                                          unsigned char* l1, F epilogue) {
+    const uint32_t end = ((uint32_t)mt * nt + 7) / 8 * 8;
+    uint32_t b = blockIdx.x;
+    int tm = 0, tn = 0;
+    auto next = [&]() {
+        for (; b < end; b += gridDim.x)
+            if (gemm_tile(b, mt, nt, &tm, &tn)) return true;
+        return false;
+    };
+    if (!next()) return;
+    G g;
+    g.begin(in, tm * BM, tn * BN, 0, G::all_steps(in), l0, l1);
+    for (bool more = true; more;) {
+        const int m0 = tm * BM, n0 = tn * BN;
+        g.template finish<V8>(in, m0, n0, l0, l1);
+        b += gridDim.x;
+        more = next();
+        if (more) g.begin(in, tm * BM, tn * BN, 0, G::all_steps(in), l0, l1);
+        epilogue(g, m0, n0);
+    }
 }
 
 }  // namespace gmm

@@ -33,8 +33,8 @@
 namespace gmm {
 
 constexpr int32_t HEAD_MAX_DIM = 1 << 20;
-constexpr int32_t HEAD_MAX_CODES = 1 << 22;  // row strides of dx: 32-bit tile offsets
-constexpr int64_t HEAD_MAX_LD = (int64_t)1 << 22;
+constexpr int32_t HEAD_MAX_CODES = 1 << 22;
+constexpr int64_t HEAD_MAX_LD = (int64_t)1 << 22;  // 256 rows span at most 2^31 bytes
 constexpr size_t HEAD_LOGIT_BYTES = (size_t)256 << 20;  // fp32 logits of one chunk of rows
 constexpr size_t HEAD_PART_BYTES = (size_t)64 << 20;    // tile statistics of one chunk
 constexpr size_t HEAD_DX_BYTES = (size_t)1 << 30;       // dx of one chunk, both orders
@@ -74,7 +74,13 @@ struct Planes<uint16_t> {
     }
 };
 
-// out[plane][r][c] for c < kp, 0 past the d-th value; 8 values per thread.
+// Operands laid out here lie in panels (gmm_gemm.h): [plane][c / 64][r][c % 64].
+// Row-major they would be read as 256 pieces of 128 bytes, 32 KB apart, per step.
+__device__ __forceinline__ int64_t panel_at(int64_t rows, int64_t r, int64_t c) {
+    return ((c / GK) * rows + r) * GK + c % GK;
+}
+
+// The planes of x for c < kp, 0 past the d-th value; 8 values per thread.
 template <typename T>
 __global__ __launch_bounds__(256) void k_planes(const T* x, int64_t rows, int d, int64_t ld, int kp,
                                                 uint16_t* out, int64_t plane) {
@@ -97,7 +103,7 @@ __global__ __launch_bounds__(256) void k_planes(const T* x, int64_t rows, int d,
             for (int q = 0; q < P; ++q) o[q].v[k] = p[q];
         }
 #pragma unroll
-        for (int q = 0; q < P; ++q) *(uint4*)(out + q * plane + r * kp + c) = o[q].q;
+        for (int q = 0; q < P; ++q) *(uint4*)(out + q * plane + panel_at(rows, r, c)) = o[q].q;
     }
 }
 
@@ -197,7 +203,7 @@ __device__ __forceinline__ uint16_t f32_to_f16(float f) {
 
 // ---- transposed operands
 
-// out[plane][c][r] for c < d and r < rp, 0 past the last row: 64 x 64 tiles
+// The planes of x^T: d rows of rp values, 0 past the last row of x: 64 x 64 tiles
 // turned through LDS. bf16 values become fp16 times the power of two of `range`.
 template <typename T>
 __global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int d, int64_t ld, int rp,
@@ -229,7 +235,7 @@ __global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int 
             if (c0 + c < d)
 #pragma unroll
                 for (int q = 0; q < P; ++q)
-                    out[q * plane + (int64_t)(c0 + c) * rp + r0 + tx] = tile[q][c][tx];
+                    out[q * plane + panel_at(d, c0 + c, r0 + tx)] = tile[q][c][tx];
         __syncthreads();
     }
 }
@@ -244,7 +250,7 @@ struct HeadArgs {
     float* x;            // logits or target logits of the chunk
     ScorePart* part;     // [rows][mt]
     const float *norm, *entropy, *g_logprob, *g_entropy;
-    uint16_t *dx, *dxt;  // planes [rows][vp], [v][np]
+    uint16_t *dx, *dxt;  // planes of rows x vp and v x np, in panels
     int64_t plane_dx, plane_dxt;
     int32_t vp, np;
     const uint32_t* range;   // of dx over all rows
@@ -276,90 +282,87 @@ __device__ __forceinline__ float sum4(float v) {
 // Statistics of each row over the tile's codes, and the targets' logits. Sums
 // are of 2^(c (x - max)) with c = scale log2 e: the exponential's argument in
 // one step from the accumulator; a is put back to base e at the end.
-template <int BM, int BN, int WM, int WN>
+template <bool ONE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
-    using G = Gemm<BM, BN, WM, WN>;
-    __shared__ __align__(16) unsigned char lds[G::LDS];
-    int tm, tn;
-    if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
-    const int m0 = tm * BM, n0 = tn * BN;
-    G g;
-    g.template run<bf16x8>(p.in, m0, n0, lds);
+    using G = Gemm<BM, BN, WM, WN, ONE>;
+    __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
+    __shared__ float sh[WM * BN * 3];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    float* sh = (float*)lds;  // [WM][BN][3]
     const float c2 = p.s.scale * 1.44269504088896341f;
-    const bool edge = m0 + BM > p.in.m;  // some of the tile's codes are not there
-    const int code0 = m0 + G::row(0);
+    gemm_walk<bf16x8, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
+        const bool edge = m0 + BM > p.in.m;  // some of the tile's codes are not there
+        const int code0 = m0 + G::row(0);
 #pragma unroll
-    for (int y = 0; y < G::TN; ++y) {
-        const int r = n0 + G::col(y);
-        if (edge) {
-#pragma unroll
-            for (int x = 0; x < G::TM; ++x)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (code0 + x * 16 + q >= p.in.m) g.acc[x][y][q] = -INFINITY;
-        }
-        float mx = -3.402823466e38f;
-#pragma unroll
-        for (int x = 0; x < G::TM; ++x)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mx = fmaxf(mx, g.acc[x][y][q]);
-        mx = max4(mx);
-        float s = 0.f, a = 0.f;
-        if (edge || mx < -1e30f) {
-            // masked codes: 0 * -inf stays 0
-#pragma unroll
-            for (int x = 0; x < G::TM; ++x)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float d = fmaxf((g.acc[x][y][q] - mx) * c2, -1000.f);
-                    const float e = g.acc[x][y][q] != g.acc[x][y][q] ? NAN : __builtin_amdgcn_exp2f(d);
-                    s += e;
-                    a = fmaf(e, d, a);
-                }
-        } else {
-            const float mc = mx * c2;
-#pragma unroll
-            for (int x = 0; x < G::TM; ++x)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float d = fmaf(g.acc[x][y][q], c2, -mc);
-                    const float e = __builtin_amdgcn_exp2f(d);
-                    s += e;
-                    a = fmaf(e, d, a);
-                }
-        }
-        s = sum4(s);
-        a = sum4(a) * 0.693147180559945309f;
-        if (lane < 16) {
-            float* o = sh + (wave / WN * BN + G::col(y)) * 3;
-            o[0] = mx * p.s.scale;
-            o[1] = s;
-            o[2] = a;
-        }
-        if (p.s.targets && r < p.in.n) {
-            const int t = p.s.targets[r], u = t - code0;
-            if (t < p.in.m && u >= 0 && u < 16 * G::TM && (u & 12) == 0) {
-                float v = 0.f;
+        for (int y = 0; y < G::TN; ++y) {
+            const int r = n0 + G::col(y);
+            if (edge) {
 #pragma unroll
                 for (int x = 0; x < G::TM; ++x)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) v = u == x * 16 + q ? g.acc[x][y][q] : v;
-                p.x[r] = v;
+                    for (int q = 0; q < 4; ++q)
+                        if (code0 + x * 16 + q >= p.in.m) g.acc[x][y][q] = -INFINITY;
+            }
+            float mx = -3.402823466e38f;
+#pragma unroll
+            for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mx = fmaxf(mx, g.acc[x][y][q]);
+            mx = max4(mx);
+            float s = 0.f, a = 0.f;
+            if (edge || mx < -1e30f) {
+                // masked codes: 0 * -inf stays 0
+#pragma unroll
+                for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float d = fmaxf((g.acc[x][y][q] - mx) * c2, -1000.f);
+                        const float e = g.acc[x][y][q] != g.acc[x][y][q] ? NAN : __builtin_amdgcn_exp2f(d);
+                        s += e;
+                        a = fmaf(e, d, a);
+                    }
+            } else {
+                const float mc = mx * c2;
+#pragma unroll
+                for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float d = fmaf(g.acc[x][y][q], c2, -mc);
+                        const float e = __builtin_amdgcn_exp2f(d);
+                        s += e;
+                        a = fmaf(e, d, a);
+                    }
+            }
+            s = sum4(s);
+            a = sum4(a) * 0.693147180559945309f;
+            if (lane < 16) {
+                float* o = sh + (wave / WN * BN + G::col(y)) * 3;
+                o[0] = mx * p.s.scale;
+                o[1] = s;
+                o[2] = a;
+            }
+            if (p.s.targets && r < p.in.n) {
+                const int t = p.s.targets[r], u = t - code0;
+                if (t < p.in.m && u >= 0 && u < 16 * G::TM && (u & 12) == 0) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v = u == x * 16 + q ? g.acc[x][y][q] : v;
+                    p.x[r] = v;
+                }
             }
         }
-    }
-    __syncthreads();
-    if (tid < BN && n0 + tid < p.in.n) {
-        Stats st{sh[tid * 3], sh[tid * 3 + 1], sh[tid * 3 + 2]};
+        __syncthreads();
+        if (tid < BN && n0 + tid < p.in.n) {
+            Stats st{sh[tid * 3], sh[tid * 3 + 1], sh[tid * 3 + 2]};
 #pragma unroll
-        for (int w = 1; w < WM; ++w) {
-            const float* o = sh + (w * BN + tid) * 3;
-            st.join(o[0], o[1], o[2]);
+            for (int w = 1; w < WM; ++w) {
+                const float* o = sh + (w * BN + tid) * 3;
+                st.join(o[0], o[1], o[2]);
+            }
+            p.part[(int64_t)(n0 + tid) * p.mt + m0 / BM] = ScorePart{st.m, st.s, st.a};
         }
-        p.part[(int64_t)(n0 + tid) * p.mt + tm] = ScorePart{st.m, st.s, st.a};
-    }
+    });
 }
 
 // One wave per row joins its tiles' statistics.
@@ -378,15 +381,16 @@ __global__ __launch_bounds__(256) void k_head_join(HeadArgs p) {
 }
 
 // fp32 logits of a chunk of rows, row stride v.
-template <int BM, int BN, int WM, int WN>
+template <bool ONE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_logits(HeadArgs p) {
-    using G = Gemm<BM, BN, WM, WN>;
-    __shared__ __align__(16) unsigned char lds[G::LDS];
+    using G = Gemm<BM, BN, WM, WN, ONE>;
+    __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
     int tm, tn;
     if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
     const int m0 = tm * BM, n0 = tn * BN;
     G g;
-    g.template run<bf16x8>(p.in, m0, n0, lds);
+    g.begin(p.in, m0, n0, 0, G::all_steps(p.in), l0, l1);
+    g.template finish<bf16x8>(p.in, m0, n0, l0, l1);
     const bool fours = p.in.m % 4 == 0;  // rows start at 16-byte boundaries
 #pragma unroll
     for (int y = 0; y < G::TN; ++y) {
@@ -408,87 +412,90 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_logits(HeadArgs p) {
 }
 
 // dx of a chunk of rows, in both orders; 0 in the padding. The order with rows
-// contiguous goes through LDS, one plane at a time, a row of codes after another.
+// contiguous is turned in LDS, 16 codes of each wave row at a time through two
+// buffers (a code's rows in 32-byte pieces rotated by four codes, so that the four
+// codes that a wave writes at once lie in different banks).
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
-    using G = Gemm<BM, BN, WM, WN>;
+    using G = Gemm<BM, BN, WM, WN, std::is_same<T, uint16_t>::value>;
     constexpr int P = Planes<T>::P;
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
-    constexpr int STR = BN * 2 + 16;  // bytes of a code's rows: four codes apart lie in other banks
-    __shared__ __align__(16) unsigned char lds[G::LDS > BM * STR ? G::LDS : BM * STR];
-    int tm, tn;
-    if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
-    const int m0 = tm * BM, n0 = tn * BN;
-    G g;
-    g.template run<bf16x8>(p.in, m0, n0, lds);
+    constexpr int NT = G::NT, TURN = WM * 16 * BN * 2;
+    __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE], turns[2 * TURN];
     const int tid = threadIdx.x;
     const float up_all = F16 ? ldexpf(1.f, range_exp(p.range)) : 1.f;
-    const int code0 = m0 + G::row(0);
+    gemm_walk<bf16x8, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
+        GradRow k[G::TN];
+        float up[G::TN], base[G::TN];
 #pragma unroll
-    for (int y = 0; y < G::TN; ++y) {
-        const int r = n0 + G::col(y);
-        const bool there = r < p.in.n;
-        GradRow k{};
-        float up = 1.f;
-        if (there) {
-            k = grad_row(grad_args(p), r);
-            if (F16) up = ldexpf(1.f, p.row_exp[r]);
+        for (int y = 0; y < G::TN; ++y) {
+            const int r = n0 + G::col(y);
+            k[y] = GradRow{};
+            up[y] = 1.f;
+            if (r < p.in.n) {
+                k[y] = grad_row(grad_args(p), r);
+                if (F16) up[y] = ldexpf(1.f, p.row_exp[r]);
+            }
+            base[y] = fmaf(k[y].gh, k[y].h, k[y].glp);
         }
-        const float base = fmaf(k.gh, k.h, k.glp);
 #pragma unroll
         for (int x = 0; x < G::TM; ++x) {
-            const int c = code0 + x * 16;
-            uint16_t o[P][4];
+            const int c = m0 + G::row(x);
+            uint16_t ot[P][G::TN][4];  // for the turned order
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float lp = fmaf(g.acc[x][y][q], k.scale, -k.m) - k.logs;
-                const float pr = exp_neg(lp);
-                const float hot = c + q == k.t ? k.glp : 0.f;
-                float v = k.scale * fmaf(-pr, fmaf(k.gh, lp, base), hot);
-                if (!there || c + q >= p.in.m) v = 0.f;
-                g.acc[x][y][q] = v;
-                if (F16) {
-                    o[0][q] = f32_to_f16(v * up);
-                } else {
-                    uint16_t cut[P];
-                    Planes<T>::cut(v, cut);
-#pragma unroll
-                    for (int j = 0; j < P; ++j) o[j][q] = cut[j];
-                }
-            }
-            if (there && c < p.vp)  // vp is a multiple of 64: whole fours
-#pragma unroll
-                for (int j = 0; j < P; ++j)
-                    *(uint2*)(p.dx + j * p.plane_dx + (int64_t)r * p.vp + c) =
-                        uint2{(uint32_t)o[j][0] | ((uint32_t)o[j][1] << 16),
-                              (uint32_t)o[j][2] | ((uint32_t)o[j][3] << 16)};
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-        if (j > 0) __syncthreads();
-#pragma unroll
-        for (int y = 0; y < G::TN; ++y)
-#pragma unroll
-            for (int x = 0; x < G::TM; ++x)
+            for (int y = 0; y < G::TN; ++y) {
+                const int r = n0 + G::col(y);
+                const bool there = r < p.in.n;
+                uint16_t o[P][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint16_t cut[P];
-                    if (F16)
-                        cut[0] = f32_to_f16(g.acc[x][y][q] * up_all);
-                    else
-                        Planes<T>::cut(g.acc[x][y][q], cut);
-                    *(uint16_t*)(lds + (G::row(x) + q) * STR + G::col(y) * 2) = cut[j];
+                    const float lp = fmaf(g.acc[x][y][q], k[y].scale, -k[y].m) - k[y].logs;
+                    const float pr = exp_neg(lp);
+                    const float hot = c + q == k[y].t ? k[y].glp : 0.f;
+                    float v = k[y].scale * fmaf(-pr, fmaf(k[y].gh, lp, base[y]), hot);
+                    if (!there || c + q >= p.in.m) v = 0.f;
+                    if (F16) {
+                        o[0][q] = f32_to_f16(v * up[y]);
+                        ot[0][y][q] = f32_to_f16(v * up_all);
+                    } else {
+                        uint16_t cut[P];
+                        Planes<T>::cut(v, cut);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) o[j][q] = ot[j][y][q] = cut[j];
+                    }
                 }
-        __syncthreads();
-        // 8 rows of a code per lane
-        for (int u = tid; u < BM * (BN / 8); u += 64 * WM * WN) {
-            const int c = u / (BN / 8), r = u % (BN / 8) * 8;
-            if (m0 + c < p.in.m && n0 + r < p.np)  // np is a multiple of 64
-                *(uint4*)(p.dxt + j * p.plane_dxt + (int64_t)(m0 + c) * p.np + n0 + r) =
-                    *(const uint4*)(lds + c * STR + r * 2);
+                if (there && c < p.vp)  // vp is a multiple of 64: whole fours
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        *(uint2*)(p.dx + j * p.plane_dx + panel_at(p.in.n, r, c)) =
+                            uint2{(uint32_t)o[j][0] | ((uint32_t)o[j][1] << 16),
+                                  (uint32_t)o[j][2] | ((uint32_t)o[j][3] << 16)};
+            }
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                unsigned char* turn = turns + ((x * P + j) & 1) * TURN;
+#pragma unroll
+                for (int y = 0; y < G::TN; ++y)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        // code of the 16 WM: wave row, 4 h + q
+                        const int e = (tid >> 6) / WN * 16 + 4 * ((tid & 63) >> 4) + q;
+                        *(uint16_t*)(turn + e * BN * 2 + ((G::col(y) * 2) ^ ((e & 12) << 3))) =
+                            ot[j][y][q];
+                    }
+                __syncthreads();
+                // 8 rows of a code per lane, 64 rows of each code after another
+#pragma unroll
+                for (int u = tid; u < WM * 16 * (BN / 8); u += NT) {
+                    const int e = u / 8 % (WM * 16), r = u / 8 / (WM * 16) * 64 + u % 8 * 8;
+                    const int code = m0 + e / 16 * (BM / WM) + x * 16 + e % 16;
+                    if (code < p.in.m && n0 + r < p.np)  // np is a multiple of 64
+                        *(uint4*)(p.dxt + j * p.plane_dxt + panel_at(p.in.m, code, n0 + r)) =
+                            *(const uint4*)(turn + e * BN * 2 + ((r * 2) ^ ((e & 12) << 3)));
+                }
+            }
         }
-    }
+    });
 }
 
 struct GradOut {
@@ -500,6 +507,7 @@ struct GradOut {
     float* sum;        // where the sum so far goes, or null: the result goes to out
     void* out;
     int64_t ldo;
+    int32_t fours;     // wide stores: see grad_store
     // fp16 operands: the powers of two that they were multiplied by, b's for
     // each row where row_exp is given
     const uint32_t *range_a, *range_b;
@@ -507,6 +515,7 @@ struct GradOut {
 };
 
 // Four neighbouring values of row r from dim c on, summed over the split already.
+// p.fours: every row starts at a multiple of four values, m is one too.
 template <typename T>
 __device__ __forceinline__ void grad_store(const GradOut& p, int64_t r, int c, f32x4 v, int back) {
     if (std::is_same<T, uint16_t>::value) {
@@ -514,13 +523,27 @@ __device__ __forceinline__ void grad_store(const GradOut& p, int64_t r, int c, f
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = ldexpf(v[q], e);
     }
+    const int64_t at = r * p.in.m + c;
+    if (p.fours) {
+        if (p.add) v += *(const f32x4*)(p.add + at);
+        if (p.sum) {
+            *(f32x4*)(p.sum + at) = v;
+        } else if constexpr (std::is_same<T, uint16_t>::value) {
+            *(uint2*)((T*)p.out + r * p.ldo + c) =
+                uint2{f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16),
+                      f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16)};
+        } else {
+            *(f32x4*)((T*)p.out + r * p.ldo + c) = v;
+        }
+        return;
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if (c + q >= p.in.m) break;
         float y = v[q];
-        if (p.add) y += p.add[r * p.in.m + c + q];
+        if (p.add) y += p.add[at + q];
         if (p.sum)
-            p.sum[r * p.in.m + c + q] = y;
+            p.sum[at + q] = y;
         else
             ((T*)p.out)[r * p.ldo + c + q] = Vec<T>::store(y);
     }
@@ -535,19 +558,19 @@ __device__ __forceinline__ int grad_back(const GradOut& p) {
 
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
-    using G = Gemm<BM, BN, WM, WN>;
-    __shared__ __align__(16) unsigned char lds[G::LDS];
+    using G = Gemm<BM, BN, WM, WN, std::is_same<T, uint16_t>::value>;
+    __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
     int tm, tn;
     if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
     const int m0 = tm * BM, n0 = tn * BN;
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
-    const int steps = p.in.kp / GK * p.in.pairs;
+    const int steps = G::all_steps(p.in);
     const int z = blockIdx.y;
     G g;
-    g.template run<std::conditional_t<F16, f16x8, bf16x8>>(
-        p.in, m0, n0, (int)((int64_t)steps * z / p.split), (int)((int64_t)steps * (z + 1) / p.split),
-        lds);
+    g.begin(p.in, m0, n0, (int)((int64_t)steps * z / p.split),
+            (int)((int64_t)steps * (z + 1) / p.split), l0, l1);
     const int back = p.split > 1 ? 0 : grad_back<T>(p);
+    g.template finish<std::conditional_t<F16, f16x8, bf16x8>>(p.in, m0, n0, l0, l1);
 #pragma unroll
     for (int y = 0; y < G::TN; ++y) {
         const int r = n0 + G::col(y);
@@ -558,9 +581,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
             if (c >= p.in.m) continue;
             if (p.split > 1) {
                 float* o = p.part + ((int64_t)z * p.in.n + r) * p.in.m + c;
+                if (p.in.m % 4 == 0) {
+                    *(f32x4*)o = g.acc[x][y];
+                } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (c + q < p.in.m) o[q] = g.acc[x][y][q];
+                    for (int q = 0; q < 4; ++q)
+                        if (c + q < p.in.m) o[q] = g.acc[x][y][q];
+                }
             } else {
                 grad_store<T>(p, r, c, g.acc[x][y], back);
             }
@@ -579,11 +606,16 @@ __global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
         const int64_t r = j / per;
         const int c = (int)(j - r * per) * 4;
         f32x4 v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
         for (int z = 0; z < p.split; ++z) {
             const float* o = p.part + ((int64_t)z * p.in.n + r) * p.in.m + c;
+            if (p.in.m % 4 == 0) {
+                v += *(const f32x4*)o;
+            } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c + q < p.in.m) v[q] += o[q];
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < p.in.m) v[q] += o[q];
+            }
         }
         grad_store<T>(p, r, c, v, back);
     }
@@ -593,7 +625,6 @@ __global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
 
 static size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 static int pad(int64_t k) { return (int)((k + GK - 1) / GK * GK); }
-
 // Workgroup tiles: codes or dims by rows.
 template <int ID>
 struct Tile;
@@ -743,23 +774,26 @@ static void planes(const void* x, int64_t rows, int d, int64_t ld, int kp, void*
 }
 template <typename T>
 static void planes_t(const void* x, int64_t rows, int d, int64_t ld, int rp, const uint32_t* range,
-                     void* out, int64_t plane, hipStream_t st) {
+                     void* out, hipStream_t st) {
     const int64_t work = (int64_t)((d + 63) / 64) * (rp / 64);
     const unsigned grid = (unsigned)(work < 65536 ? work : 65536);
     hipLaunchKernelGGL((k_planes_t<T>), dim3(grid), dim3(256), 0, st, (const T*)x, rows, d, ld, rp,
-                       range, (uint16_t*)out, plane);
+                       range, (uint16_t*)out, (int64_t)d * rp);
 }
 
 static unsigned tile_grid(int mt, int nt) {
     return (unsigned)(((int64_t)mt * nt + 7) / 8 * 8);
 }
 
+// walk: the kernel's workgroups walk over the tiles, as many as the chip holds.
 template <int ID, typename K, typename A>
-static void launch_tiles(K kernel, A& a, int split, hipStream_t st) {
+static void launch_tiles(K kernel, A& a, int split, bool walk, hipStream_t st) {
     using C = Tile<ID>;
     a.mt = (a.in.m + C::BM - 1) / C::BM;
     a.nt = (a.in.n + C::BN - 1) / C::BN;
-    hipLaunchKernelGGL(kernel, dim3(tile_grid(a.mt, a.nt), split), dim3(64 * C::WM * C::WN), 0, st, a);
+    unsigned grid = tile_grid(a.mt, a.nt);
+    if (walk && grid > (unsigned)TILE_COST[ID].at_once) grid = TILE_COST[ID].at_once;
+    hipLaunchKernelGGL(kernel, dim3(grid, split), dim3(64 * C::WM * C::WN), 0, st, a);
 }
 
 // out = the product of o.in, with the tile and split that suit it.
@@ -768,10 +802,11 @@ static void launch_grad(GradOut& o, float* part, hipStream_t st) {
     const Choice c = choose_tile(o.in.m, o.in.n, (int64_t)o.in.kp / GK * o.in.pairs, HEAD_MAX_SPLIT);
     o.split = c.split;
     o.part = part;
+    o.fours = o.in.m % 4 == 0 && o.ldo % 4 == 0 && (uintptr_t)o.out % (4 * sizeof(T)) == 0;
     with_tile(c.tile, [&](auto b) {
         constexpr int B = decltype(b)::value;
         using C = Tile<B>;
-        launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, c.split, st);
+        launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, c.split, false, st);
     });
     if (c.split > 1) {
         const int64_t work = ((int64_t)o.in.n * ((o.in.m + 3) / 4) + 255) / 256;
@@ -794,12 +829,14 @@ static void head_weight(const HeadIn& x, const HeadPlan& q, char* ws, GemmIn* g,
     g->m = x.v;
     if (q.pack_w) {
         g->a = (const uint16_t*)(ws + q.o_w);
-        g->lda = q.dp;
+        g->lda = GK;
+        g->step_a = (int64_t)x.v * GK;
         g->plane_a = (int64_t)x.v * q.dp;
         planes<T>(x.w, x.v, x.d, x.ldw, q.dp, ws + q.o_w, g->plane_a, st);
     } else {
         g->a = (const uint16_t*)x.w;
         g->lda = x.ldw;
+        g->step_a = GK;
     }
 }
 template <typename T>
@@ -810,12 +847,14 @@ static void head_rows(const HeadIn& x, const HeadPlan& q, char* ws, int64_t r0, 
     g->n = a->rows = (int32_t)rows;
     if (q.pack_h) {
         g->b = (const uint16_t*)(ws + q.o_h);
-        g->ldb = q.dp;
-        g->plane_b = q.chunk * q.dp;
+        g->ldb = GK;
+        g->step_b = rows * GK;
+        g->plane_b = rows * q.dp;
         planes<T>(h, rows, x.d, x.ldh, q.dp, ws + q.o_h, g->plane_b, st);
     } else {
         g->b = (const uint16_t*)h;
         g->ldb = x.ldh;
+        g->step_b = GK;
     }
 }
 
@@ -844,11 +883,12 @@ static hipError_t head_score(const HeadIn& x, const HeadPlan& q, ScoreArgs s, ch
         const Choice c = choose_tile(x.v, rows, (int64_t)q.dp / GK * q.pairs, 1);
         with_tile(c.tile, [&](auto b) {
             constexpr int B = decltype(b)::value;
+            constexpr bool ONE = Planes<T>::P == 1;
             using C = Tile<B>;
             if (s.m > 0)
-                launch_tiles<B>(k_head_logits<C::BM, C::BN, C::WM, C::WN>, a, 1, st);
+                launch_tiles<B>(k_head_logits<ONE, C::BM, C::BN, C::WM, C::WN>, a, 1, false, st);
             else
-                launch_tiles<B>(k_head_stats<C::BM, C::BN, C::WM, C::WN>, a, 1, st);
+                launch_tiles<B>(k_head_stats<ONE, C::BM, C::BN, C::WM, C::WN>, a, 1, true, st);
         });
         if (s.m > 0) {
             ScoreArgs l = a.s;
@@ -867,7 +907,6 @@ template <typename T>
 static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void* dh, int64_t lddh,
                             void* dw, int64_t lddw, char* ws, hipStream_t st) {
     head_weight<T>(x, q, ws, &a.in, st);
-    const int64_t plane_wt = (int64_t)x.d * q.vp, plane_ht = (int64_t)x.d * q.np;
     uint16_t* wt = (uint16_t*)(ws + q.o_wt);
     uint16_t* ht = (uint16_t*)(ws + q.o_ht);
     uint32_t* range = (uint32_t*)(ws + q.o_range);  // W, h, dx
@@ -887,11 +926,10 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         r.row_exp = row_exp;
         hipLaunchKernelGGL(k_head_range, dim3(RANGE_BLOCKS), dim3(256), 0, st, r);
     }
-    if (dh) planes_t<T>(x.w, x.v, x.d, x.ldw, q.vp, range, wt, plane_wt, st);
+    if (dh) planes_t<T>(x.w, x.v, x.d, x.ldw, q.vp, range, wt, st);
     a.range = range + 2 * RANGE_BLOCKS;
     a.dx = (uint16_t*)(ws + q.o_dx);
     a.dxt = (uint16_t*)(ws + q.o_dxt);
-    a.plane_dx = q.chunk * q.vp;
     a.vp = q.vp;
     const HeadArgs all = a;
     for (int64_t r0 = 0; r0 < x.n; r0 += q.chunk) {
@@ -899,6 +937,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         head_rows<T>(x, q, ws, r0, rows, &a, st);
         a.np = pad(rows);
         a.row_exp = row_exp + r0;
+        a.plane_dx = rows * q.vp;
         a.plane_dxt = (int64_t)x.v * a.np;
         a.s.targets = all.s.targets ? all.s.targets + r0 : nullptr;
         a.norm = all.norm + 2 * r0;
@@ -909,12 +948,12 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         with_tile(c.tile, [&](auto b) {
             constexpr int B = decltype(b)::value;
             using C = Tile<B>;
-            launch_tiles<B>(k_head_dx<T, C::BM, C::BN, C::WM, C::WN>, a, 1, st);
+            launch_tiles<B>(k_head_dx<T, C::BM, C::BN, C::WM, C::WN>, a, 1, true, st);
         });
         if (dh) {
             GradOut o{};
-            o.in = GemmIn{wt, a.dx, q.vp, q.vp, plane_wt, a.plane_dx, x.d, (int32_t)rows, q.vp,
-                          q.pairs};
+            o.in = GemmIn{wt, a.dx, GK, GK, (int64_t)x.d * GK, rows * GK, (int64_t)x.d * q.vp, a.plane_dx,
+                          x.d, (int32_t)rows, q.vp, q.pairs};
             o.out = (T*)dh + r0 * lddh;
             o.ldo = lddh;
             o.range_a = range;
@@ -923,9 +962,10 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         }
         if (dw) {
             planes_t<T>((const T*)x.h + r0 * x.ldh, rows, x.d, x.ldh, a.np, range + RANGE_BLOCKS, ht,
-                        plane_ht, st);
+                        st);
             GradOut o{};
-            o.in = GemmIn{ht, a.dxt, a.np, a.np, plane_ht, a.plane_dxt, x.d, x.v, a.np, q.pairs};
+            o.in = GemmIn{ht, a.dxt, GK, GK, (int64_t)x.d * GK, (int64_t)x.v * GK, (int64_t)x.d * a.np,
+                          a.plane_dxt, x.d, x.v, a.np, q.pairs};
             float* sum = (float*)(ws + q.o_sum);
             o.add = r0 > 0 ? sum : nullptr;
             o.sum = r0 + q.chunk < x.n ? sum : nullptr;
