@@ -219,16 +219,22 @@ __global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int 
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int64_t r0 = b / ct * 64;
         const int c0 = (int)(b % ct) * 64;
-        for (int r = ty; r < 64; r += 4) {
-            uint16_t p[P];
-            const bool in = r0 + r < rows && c0 + tx < d;
-            const float y = in ? Vec<T>::one(x + (r0 + r) * ld + c0 + tx) : 0.f;
-            if (F16)
-                p[0] = f32_to_f16(y * up);
-            else
-                Planes<T>::cut(y, p);
+        float y[16];  // all of a thread's loads in flight
 #pragma unroll
-            for (int q = 0; q < P; ++q) tile[q][tx][r] = p[q];
+        for (int k = 0; k < 16; ++k) {
+            const int r = ty + 4 * k;
+            const bool in = r0 + r < rows && c0 + tx < d;
+            y[k] = in ? Vec<T>::one(x + (r0 + r) * ld + c0 + tx) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            uint16_t p[P];
+            if (F16)
+                p[0] = f32_to_f16(y[k] * up);
+            else
+                Planes<T>::cut(y[k], p);
+#pragma unroll
+            for (int q = 0; q < P; ++q) tile[q][tx][ty + 4 * k] = p[q];
         }
         __syncthreads();
         for (int c = ty; c < 64; c += 4)
@@ -606,7 +612,7 @@ __global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
         const int64_t r = j / per;
         const int c = (int)(j - r * per) * 4;
         f32x4 v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
         for (int z = 0; z < p.split; ++z) {
             const float* o = p.part + ((int64_t)z * p.in.n + r) * p.in.m + c;
             if (p.in.m % 4 == 0) {

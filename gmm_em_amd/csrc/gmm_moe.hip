@@ -32,6 +32,7 @@ namespace gmm {
 constexpr int MOE_MAX_EXPERTS = 4096;    // gate logits of a row in LDS
 constexpr int64_t MOE_MAX_PAIRS = 1 << 20;  // (row, pick) pairs per call
 constexpr int32_t MOE_MAX_DIM = 1 << 20;
+constexpr int MOE_FEW_ROWS = 2;          // rows whose second product is made row by row
 constexpr int MOE_WIN = 2048;            // pairs looked through at a time
 
 // Where the picks of one call fit a wave (pairs <= 64), every wave finds its
@@ -409,6 +410,40 @@ __global__ __launch_bounds__(64 * W) void k_moe_out(MoeArgs p) {
     });
 }
 
+// Few rows: one workgroup makes 16 features of one row from all its experts and
+// writes y itself (experts that rows share are read again, from the caches).
+// 16 waves split the contracted axis; a wave's sums over the experts stay in its
+// accumulators, scaled by the shares, in the picks' order.
+constexpr int MOE_ROW_W = 16;
+template <typename T>
+__global__ __launch_bounds__(64 * MOE_ROW_W) void k_moe_out_row(MoeArgs p) {
+    constexpr int PB = std::is_same<T, uint16_t>::value ? 2 : 1;
+    __shared__ f32x4 sh[MOE_ROW_W * 64];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15;
+    const int t = blockIdx.y, d0 = blockIdx.x * 16;
+    const int row = d0 + i < p.d ? d0 + i : p.d - 1;
+    f32x4 y{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < p.m; ++j) {
+        const int pair = t * p.m + j;
+        const int e = p.idx[pair];
+        if (e < 0 || e >= p.e) continue;
+        const T* rows[1] = {(const T*)p.w_out + ((int64_t)e * p.d + row) * p.f};
+        const T* col[1] = {(const T*)p.act + (int64_t)pair * p.fp};
+        f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+        moe_dot<T, 1, 1, PB, MOE_ROW_W>(rows, col, p.act_plane, p.f, acc);
+        y += p.resp[pair] * acc[0][0];
+    }
+    moe_join_waves<1, MOE_ROW_W>(&y, sh);
+    // all 16 columns are this row: column 0's four features per lane 16 h
+    if (tid < 64 && i == 0) {
+        const f32x4 v = sh[lane];
+        const int c = d0 + 4 * (lane >> 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (c + q < p.d) ((T*)p.y)[(int64_t)t * p.ldy + c + q] = Vec<T>::store(v[q]);
+    }
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void k_moe_join(MoeArgs p) {
     const int64_t total = (int64_t)p.n * p.d;
@@ -456,6 +491,10 @@ static hipError_t launch_moe(const MoeArgs& a, hipStream_t st) {
     if (a.gate) hipLaunchKernelGGL((k_moe_route<T>), dim3(a.n), dim3(RT_NT), 0, st, a);
     const int ft = (a.f + 15) / 16, dt = (a.d + 15) / 16;
     hipLaunchKernelGGL((k_moe_in<T, 4>), dim3(ft, a.slots), dim3(256), 0, st, a);
+    if (a.n <= MOE_FEW_ROWS) {
+        hipLaunchKernelGGL((k_moe_out_row<T>), dim3(dt, a.n), dim3(64 * MOE_ROW_W), 0, st, a);
+        return hipGetLastError();
+    }
     // enough tiles: 64 features share the loads of act; few: 16 waves share a tile
     if ((int64_t)dt * a.slots >= 4096)
         hipLaunchKernelGGL((k_moe_out<T, 4, 4>), dim3((dt + 3) / 4, a.slots), dim3(256), 0, st, a);

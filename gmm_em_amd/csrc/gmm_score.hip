@@ -2,22 +2,24 @@
 // logits, and their gradient (gmm_logits_score, gmm_logits_score_backward,
 // declared in include/gmm_em.h).
 //
-// Scores: with l = scale * x, one pass over a row keeps the running maximum
-// m, s = sum exp(l - m) and a = sum exp(l - m)(l - m) (restated when m
-// rises), so that
+// Scores: with l = scale * x, one pass over a row keeps, per thread, the maximum m,
+// s = sum exp(l - m) and a = sum exp(l - m)(l - m) (restated when m rises), so that
 //   log p_t = (l_t - m) - log s      entropy = log s - a / s
-// with nothing of the row stored. Sums run per thread, then over the lanes and
+// with nothing of the row stored; the threads' sums are joined over the lanes and
 // the waves in a fixed order.
-// Alternatives: each wave keeps its m best so far in its lanes. Values that
-// cannot enter are dismissed by one comparison per lane and chunk (the
-// lane's maximum, needed anyway, against the list's last entry); otherwise the
-// m-th largest of the lane maxima bounds the list's last entry from below, and
-// only the few values at or above it are inserted one by one.
+// Alternatives: the threads form 64 groups; the m-th largest of the groups' maxima is a
+// bound that m values of the row reach and hardly more than m do (about
+// 64 ln(64 / (64 - m))). The values of the few threads whose maximum reaches it are
+// read again by all threads (they are in the caches), those at the bound are gathered
+// in LDS, and one wave picks the m best. Where ties or a mask put more values at the bound than LDS holds, the m
+// best are found one by one over the whole row.
 // Gradient: dx = scale (g_lp ([v = t] - p) - g_H p (log p + H)) with p from the
 // stored m and log s: each logit is read once and its gradient written once.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "gmm_em.h"
 #include "gmm_internal.h"
@@ -26,8 +28,8 @@
 
 namespace gmm {
 
-// Threads per row; vectors of 16 bytes in flight per thread.
-constexpr int SC_U = 4;
+constexpr int SC_U = 4;       // vectors of 16 bytes in flight per thread
+constexpr int SC_CAND = 256;  // gathered values
 
 // The logit of the row's target (thread 0; where there is none, unused).
 template <typename T>
@@ -37,99 +39,203 @@ __device__ __forceinline__ float target_logit(const ScoreArgs& p, int64_t row, i
     return t >= 0 && t < p.v ? Vec<T>::one((const T*)p.x + row * p.ldl + t) : 0.f;
 }
 
+// The largest value of each group of G = NT / 64 neighbouring lanes.
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+    if (G > 1) v = fmaxf(v, lane_move<0xb1>(v));   // the lane next to it
+    if (G > 2) v = fmaxf(v, lane_move<0x4e>(v));   // the other two of four
+    if (G > 4) v = fmaxf(v, lane_move<0x141>(v));  // the other four of eight
+    if (G > 8) v = fmaxf(v, lane_move<0x140>(v));  // the other eight of sixteen
+    return v;
+}
+
+// A part of a row, read in vectors: vector j of NT * SC_U threads' worth starts at value
+// j VE; one that would pass the end is the last whole one instead, and the
+// values that belong to others are -inf in it.
+template <typename T>
+struct RowPart {
+    static constexpr int VE = Vec<T>::VE;
+    const T* x;
+    int len;
+    __device__ __forceinline__ int first(int at) const { return len < VE ? 0 : min(at, len - VE); }
+    __device__ __forceinline__ Raw16 get(int at) const {
+        if (len < VE) return load_vec(x, (int64_t)at, (int64_t)len);
+        return *reinterpret_cast<const Raw16*>((const char*)x + (uint32_t)first(at) * sizeof(T));
+    }
+    __device__ __forceinline__ void mask(Raw16& r, int at) const {
+        if (at + VE > len && len >= VE) {
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                if (k < at - first(at)) Vec<T>::put(r, k, -INFINITY);
+        }
+    }
+};
+
 // NT threads per (row, part). parts == 1: writes the results; else the part's
 // statistics and list go to the workspace for k_score_join.
+// Bound by its reads: 4096 rows of 32768 bf16 values in 51 us without alternatives
+// (5.3 TB/s), 57 us with 4; the insertion of every value above a wave's own m-th best
+// into its sorted list took 73.
 template <typename T, int NT, bool TOP>
 __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
-    constexpr int VE = Vec<T>::VE, NW = NT / 64;
-    __shared__ float sst[NW][3];
-    __shared__ float sv[NW * TOP_MAX];
-    __shared__ int si[NW * TOP_MAX];
+    constexpr int VE = Vec<T>::VE, NW = NT / 64, G = NT / 64, CHUNK = NT * VE * SC_U;
+    __shared__ float sst[NW][3], gmax[64], cv[SC_CAND], best_v;
+    __shared__ int ci[SC_CAND], hot[NT], hots, count, best_i;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const float c2 = p.scale * 1.44269504088896341f;
     for (int64_t item = blockIdx.x; item < p.n * p.parts; item += gridDim.x) {
         const int64_t row = item / p.parts;
         const int part = (int)(item - row * p.parts);
         const int64_t i0 = (int64_t)part * p.part_len;
-        const int64_t i1 = i0 + p.part_len < p.v ? i0 + p.part_len : p.v;
-        const T* x = (const T*)p.x + row * p.ldl;
+        const RowPart<T> x{(const T*)p.x + row * p.ldl + i0,
+                           (int)(p.v - i0 < p.part_len ? p.v - i0 : p.part_len)};
         Stats st;
         st.clear();
-        TopList top;
-        top.clear();
-        for (int64_t b = i0; b < i1; b += (int64_t)NT * VE * SC_U) {
+        float cm = -INFINITY;  // largest l of this thread
+        for (int b = 0; b < x.len; b += CHUNK) {
             Raw16 raw[SC_U];
 #pragma unroll
-            for (int u = 0; u < SC_U; ++u)
-                raw[u] = load_vec(x, b + ((int64_t)u * NT + tid) * VE, i1);
-            float cm = -INFINITY;
+            for (int u = 0; u < SC_U; ++u) raw[u] = x.get(b + (u * NT + tid) * VE);
+            if (b + CHUNK > x.len) {
+#pragma unroll
+                for (int u = 0; u < SC_U; ++u) x.mask(raw[u], b + (u * NT + tid) * VE);
+            }
+            float xm = -INFINITY;
 #pragma unroll
             for (int u = 0; u < SC_U; ++u)
 #pragma unroll
-                for (int k = 0; k < VE; ++k) cm = fmaxf(cm, Vec<T>::get(raw[u], k));
-            cm *= p.scale;
-            st.raise(fmaxf(st.m, cm));
+                for (int k = 0; k < VE; ++k) xm = fmaxf(xm, Vec<T>::get(raw[u], k));
+            cm = fmaxf(cm, xm * p.scale);
+            st.raise(fmaxf(st.m, xm * p.scale));
+            if (__builtin_amdgcn_ballot_w64(fabsf(st.m) > 1e30f)) {
+                // far out: the scaled maximum times log2 e would pass the range
 #pragma unroll
-            for (int u = 0; u < SC_U; ++u)
+                for (int u = 0; u < SC_U; ++u)
 #pragma unroll
-                for (int k = 0; k < VE; ++k) st.add(fmaf(Vec<T>::get(raw[u], k), p.scale, -st.m));
-            if constexpr (TOP) {
-                const float least = top.least(p.m);
-                if (__builtin_amdgcn_ballot_w64(cm > least)) {
-                    // the m-th largest lane maximum: at least m values reach it
-                    float cur = cm, bound = -INFINITY;
-                    for (int j = 0; j < p.m; ++j) {
-                        bound = wave_max(cur);
-                        const uint64_t at = __builtin_amdgcn_ballot_w64(cur == bound);
-                        if (at && lane == __builtin_ctzll(at)) cur = -INFINITY;
+                    for (int k = 0; k < VE; ++k)
+                        st.add(fmaf(Vec<T>::get(raw[u], k), p.scale, -st.m));
+            } else {
+                // 2^(c2 x - m log2 e): one step to the exponential's argument; a in base 2
+                const float mc = st.m * 1.44269504088896341f;
+                float s = 0.f, a = 0.f;
+#pragma unroll
+                for (int u = 0; u < SC_U; ++u)
+#pragma unroll
+                    for (int k = 0; k < VE; ++k) {
+                        const float d = fmaf(Vec<T>::get(raw[u], k), c2, -mc);
+                        const float e = __builtin_amdgcn_exp2f(d);
+                        s += e;
+                        a = fmaf(e, fmaxf(d, -1000.f), a);
                     }
-#pragma unroll
-                    for (int u = 0; u < SC_U; ++u)
-#pragma unroll
-                        for (int k = 0; k < VE; ++k) {
-                            const float l = Vec<T>::get(raw[u], k) * p.scale;
-                            uint64_t in = __builtin_amdgcn_ballot_w64(l >= bound && l > least);
-                            while (in) {
-                                const int from = __builtin_ctzll(in);
-                                in &= in - 1;
-                                const int64_t i =
-                                    b + ((int64_t)u * NT + wave * 64 + from) * VE + k;
-                                top.insert(lane_get(l, from), (int)i, p.m, lane);
-                            }
-                        }
-                }
+                st.s += s;
+                st.a = fmaf(a, 0.693147180559945309f, st.a);
             }
         }
         st.wave_join();
+        float gm = TOP ? group_max<G>(cm) : 0.f;
         if constexpr (NW > 1) {
             if (lane == 0) {
                 sst[wave][0] = st.m;
                 sst[wave][1] = st.s;
                 sst[wave][2] = st.a;
             }
-            if constexpr (TOP) {
-                if (lane < p.m) {
-                    sv[wave * p.m + lane] = top.v;
-                    si[wave * p.m + lane] = top.i;
-                }
-            }
-            __syncthreads();
-            // wave 0 joins the waves' statistics and lists
+            if (TOP && lane % G == 0) gmax[tid / G] = gm;
+        }
+        if (TOP && tid == 0) hots = count = 0;
+        __syncthreads();
+        if constexpr (NW > 1) {
             if (wave == 0) {
                 st.clear();
                 if (lane < NW) st = Stats{sst[lane][0], sst[lane][1], sst[lane][2]};
                 st.wave_join();
-                if constexpr (TOP) {
-                    constexpr int C = (NW * TOP_MAX + 63) / 64;
-                    float cv[C];
-                    int ci[C];
+            }
+            if (TOP) gm = gmax[lane];
+        }
+        TopList top;
+        top.clear();
+        if constexpr (TOP) {
+            const uint32_t bound = order_bound(gm, p.m);
+            auto in = [&](float l) { return l > -INFINITY && order_of(l) >= bound; };
+            if (in(cm)) hot[atomicAdd(&hots, 1)] = tid;
+            __syncthreads();
+            // the hot threads' values, a value per thread at a time
+            const uint32_t mine = (x.len + CHUNK - 1) / CHUNK * SC_U * VE;  // values of a thread
+            const uint32_t total = (uint32_t)hots * mine;  // at most the row, rounded up
+            for (uint32_t e = tid; e < total; e += NT) {
+                const int h = (int)(e / mine), j = (int)(e - h * mine);
+                const int u = j / VE, k = j % VE;
+                const int at = u / SC_U * CHUNK + (u % SC_U * NT + hot[h]) * VE + k;
+                if (at < x.len) {
+                    const float l = Vec<T>::one(x.x + at) * p.scale;
+                    if (in(l)) {
+                        const int to = atomicAdd(&count, 1);
+                        if (to < SC_CAND) {
+                            cv[to] = l;
+                            ci[to] = (int)i0 + at;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            int cnt = count;
+            if (cnt > SC_CAND) {
+                // one by one: the best that comes after the one before
+                float lv = INFINITY;
+                int li = -1;
+                for (int j = 0; j < p.m; ++j) {
+                    float bv = -INFINITY;
+                    int bi = 0x7fffffff;
+                    for (int at = tid * VE; at < x.len; at += NT * VE) {
+                        const Raw16 r = load_vec(x.x, (int64_t)at, (int64_t)x.len);
+#pragma unroll
+                        for (int k = 0; k < VE; ++k) {
+                            const float l = Vec<T>::get(r, k) * p.scale;
+                            const int i = (int)i0 + at + k;
+                            if (top_before(lv, li, l, i) && top_before(l, i, bv, bi)) {
+                                bv = l;
+                                bi = i;
+                            }
+                        }
+                    }
+                    float* rv = cv + TOP_MAX;  // the waves' best, after the results
+                    int* ri = ci + TOP_MAX;
+                    const float wv = wave_max(bv);
+                    const int wi = wave_min(bv == wv ? bi : 0x7fffffff);
+                    if (lane == 0) {
+                        rv[wave] = wv;
+                        ri[wave] = wi;
+                    }
+                    __syncthreads();
+                    if (wave == 0) {
+                        const float v = lane < NW ? rv[lane] : -INFINITY;
+                        const float mv = wave_max(v);
+                        const int mi = wave_min(lane < NW && v == mv ? ri[lane] : 0x7fffffff);
+                        if (lane == 0) {
+                            best_v = cv[j] = mv;
+                            best_i = ci[j] = mi;
+                        }
+                    }
+                    __syncthreads();
+                    lv = best_v;
+                    li = lv > -INFINITY ? best_i : 0x7fffffff;  // nothing comes after the last
+                }
+                cnt = p.m;
+            }
+            if (wave == 0) {
+                auto pick = [&](auto per) {
+                    constexpr int C = decltype(per)::value;
+                    float v[C];
+                    int i[C];
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        const int at = c * 64 + lane;
-                        cv[c] = at < NW * p.m ? sv[at] : -INFINITY;
-                        ci[c] = at < NW * p.m ? si[at] : 0x7fffffff;
+                        const int e = c * 64 + lane;
+                        v[c] = e < cnt ? cv[e] : -INFINITY;
+                        i[c] = e < cnt ? ci[e] : 0x7fffffff;
                     }
-                    top = top_pick<C>(cv, ci, p.m, lane);
-                }
+                    return top_pick<C>(v, i, p.m, lane);
+                };
+                top = cnt <= 64 ? pick(std::integral_constant<int, 1>())
+                                : pick(std::integral_constant<int, SC_CAND / 64>());
             }
         }
         if (wave == 0) {
@@ -143,7 +249,7 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
                 }
             }
         }
-        if constexpr (NW > 1) __syncthreads();  // LDS is free for the next item
+        __syncthreads();  // LDS is free for the next item
     }
 }
 
@@ -211,10 +317,10 @@ __global__ __launch_bounds__(SG_NT) void k_score_grad(ScoreGradArgs p) {
 ScorePlan score_plan(int64_t n, int32_t v, int32_t m) {
     ScorePlan q;
     q.parts = 1;
-    // few long rows: parts of at least 16384 values until 512 blocks run
-    if (n < 256) {
-        const int64_t most = v / 16384;
-        int64_t want = n > 0 ? 512 / n : 1;
+    // few long rows: parts of at least 32768 values until 256 blocks run
+    if (n < 128) {
+        const int64_t most = v / 32768;
+        int64_t want = n > 0 ? 256 / n : 1;
         if (want > most) want = most;
         if (want > SC_MAX_PARTS) want = SC_MAX_PARTS;
         if (want > 1) q.parts = (int)want;
@@ -242,11 +348,16 @@ static void launch_score_nt(const ScoreArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((k_score<T, NT, false>), grid, dim3(NT), 0, st, a);
 }
 
+// Threads per (row, part): one wave where it has at most 8 chunks to go through (8192
+// rows of 5000 bf16 values, m = 8: 37 us, with 256 threads 47), else 256; as many as
+// there can be where there are few rows for the chip.
 template <typename T>
 static void launch_score_t(const ScoreArgs& a, hipStream_t st) {
-    if (a.part_len <= 2048)
+    constexpr int64_t PER = SC_U * Vec<T>::VE;
+    const bool few = a.n * a.parts < 512;
+    if (a.part_len <= 64 * PER || (!few && a.part_len <= 8 * 64 * PER))
         launch_score_nt<T, 64>(a, st);
-    else if (a.n * a.parts >= 512)
+    else if (!few)
         launch_score_nt<T, 256>(a, st);
     else
         launch_score_nt<T, 1024>(a, st);

@@ -42,6 +42,7 @@ struct Vec<float> {
     static __device__ __forceinline__ void set(Raw16& r, int k, float v) {
         r.w[k] = __float_as_uint(v);
     }
+    static __device__ __forceinline__ void put(Raw16& r, int k, float v) { set(r, k, v); }
     static __device__ __forceinline__ float store(float v) { return v; }
 };
 template <>
@@ -54,6 +55,11 @@ struct Vec<uint16_t> {
     static __device__ __forceinline__ void set(Raw16& r, int k, float v) {
         const uint32_t b = f32_to_bf16(v);
         r.w[k >> 1] = (k & 1) ? ((r.w[k >> 1] & 0xffffu) | (b << 16)) : b;
+    }
+    // replaces value k (set() takes the values in order)
+    static __device__ __forceinline__ void put(Raw16& r, int k, float v) {
+        const uint32_t b = f32_to_bf16(v);
+        r.w[k >> 1] = (k & 1) ? ((r.w[k >> 1] & 0xffffu) | (b << 16)) : ((r.w[k >> 1] & 0xffff0000u) | b);
     }
     static __device__ __forceinline__ uint16_t store(float v) { return (uint16_t)f32_to_bf16(v); }
 };
@@ -166,8 +172,8 @@ __device__ __forceinline__ bool top_before(float v, int i, float v2, int i2) {
     return v > v2 || (v == v2 && i < i2);
 }
 
-// A wave's sorted list of its m best (value, index) pairs: entry j in lane j,
-// the empty entry is (-inf, INT_MAX). -inf and NaN never enter.
+// A wave's sorted list of m (value, index) pairs: entry j in lane j, the empty entry
+// is (-inf, INT_MAX).
 struct TopList {
     float v;
     int i;
@@ -175,23 +181,26 @@ struct TopList {
         v = -INFINITY;
         i = 0x7fffffff;
     }
-    __device__ __forceinline__ float least(int m) const { return lane_get(v, m - 1); }
-    // wave-uniform nv, ni
-    __device__ __forceinline__ void insert(float nv, int ni, int m, int lane) {
-        const uint64_t before = __builtin_amdgcn_ballot_w64(top_before(v, i, nv, ni));
-        const int pos = __popcll(before & ((uint64_t(1) << m) - 1));
-        if (pos >= m) return;
-        const float uv = lane_move<0x138>(v);
-        const int ui = lane_move<0x138>(i);
-        if (lane == pos) {
-            v = nv;
-            i = ni;
-        } else if (lane > pos) {
-            v = uv;
-            i = ui;
-        }
-    }
 };
+
+// Whole number in the order of the float (NaN apart).
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t u = __float_as_uint(v + 0.f);  // -0 counts as 0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// A bound that at least m of the wave's 64 values reach: the m-th largest, cut
+// to its upper 20 bits, found bit by bit by counting.
+__device__ __forceinline__ uint32_t order_bound(float v, int m) {
+    const uint32_t key = order_of(v);
+    uint32_t t = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 12; --bit) {
+        const uint32_t c = t | (1u << bit);
+        if (__popcll(__builtin_amdgcn_ballot_w64(key >= c)) >= m) t = c;
+    }
+    return t;
+}
 
 // The m best of C * 64 candidates, C per lane, as a sorted list: m rounds of the
 // best value and, among its equals, the smallest index. -inf is the empty entry.
