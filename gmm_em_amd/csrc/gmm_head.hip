@@ -80,30 +80,43 @@ __device__ __forceinline__ int64_t panel_at(int64_t rows, int64_t r, int64_t c) 
     return ((c / GK) * rows + r) * GK + c % GK;
 }
 
+// An operand to be laid out: rows x d values of a caller's matrix.
+struct Layout {
+    const void* x;
+    int64_t rows, ld;
+    uint16_t* out;
+};
+// One launch lays out W and the first rows of h (blockIdx.y): rows == 0 is none.
+struct LayoutPair {
+    Layout o[2];
+    int32_t d;
+};
+
 // The planes of x for c < kp, 0 past the d-th value; 8 values per thread.
 template <typename T>
-__global__ __launch_bounds__(256) void k_planes(const T* x, int64_t rows, int d, int64_t ld, int kp,
-                                                uint16_t* out, int64_t plane) {
+__global__ __launch_bounds__(256) void k_planes(LayoutPair p, int kp) {
     constexpr int P = Planes<T>::P;
+    const Layout o = p.o[blockIdx.y];
     const int per = kp / 8;
-    const int64_t total = rows * per;
+    const int64_t total = o.rows * per, plane = o.rows * kp;
     for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total;
          j += (int64_t)gridDim.x * 256) {
         const int64_t r = j / per;
         const int c = (int)(j - r * per) * 8;
+        const T* x = (const T*)o.x + r * o.ld;
         union {
             uint16_t v[8];
             uint4 q;
-        } o[P];
+        } u[P];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            uint16_t p[P];
-            Planes<T>::cut(c + k < d ? Vec<T>::one(x + r * ld + c + k) : 0.f, p);
+            uint16_t cut[P];
+            Planes<T>::cut(c + k < p.d ? Vec<T>::one(x + c + k) : 0.f, cut);
 #pragma unroll
-            for (int q = 0; q < P; ++q) o[q].v[k] = p[q];
+            for (int q = 0; q < P; ++q) u[q].v[k] = cut[q];
         }
 #pragma unroll
-        for (int q = 0; q < P; ++q) *(uint4*)(out + q * plane + panel_at(rows, r, c)) = o[q].q;
+        for (int q = 0; q < P; ++q) *(uint4*)(o.out + q * plane + panel_at(o.rows, r, c)) = u[q].q;
     }
 }
 
@@ -203,19 +216,19 @@ __device__ __forceinline__ uint16_t f32_to_f16(float f) {
 
 // ---- transposed operands
 
-// The planes of x^T: d rows of rp values, 0 past the last row of x: 64 x 64 tiles
-// turned through LDS. bf16 values become fp16 times the power of two of `range`.
+// The planes of x^T: d rows of x's rows, padded with 0 to a multiple of 64: 64 x 64 tiles
+// turned through LDS. bf16 values become fp16 times the power of two of `range`
+// (W's and h's).
 template <typename T>
-__global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int d, int64_t ld, int rp,
-                                                  const uint32_t* range, uint16_t* out,
-                                                  int64_t plane) {
+__global__ __launch_bounds__(256) void k_planes_t(LayoutPair p, const uint32_t* range) {
     constexpr int P = Planes<T>::P;
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
     __shared__ uint16_t tile[P][64][66];
-    const int ct = (d + 63) / 64;
-    const int64_t total = (int64_t)ct * (rp / 64);
+    const Layout o = p.o[blockIdx.y];
+    const int ct = (p.d + 63) / 64;
+    const int64_t rp = (o.rows + 63) / 64 * 64, total = ct * (rp / 64), plane = p.d * rp;
     const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    const float up = F16 ? ldexpf(1.f, range_exp(range)) : 1.f;
+    const float up = F16 ? ldexpf(1.f, range_exp(range + blockIdx.y * RANGE_BLOCKS)) : 1.f;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int64_t r0 = b / ct * 64;
         const int c0 = (int)(b % ct) * 64;
@@ -223,25 +236,25 @@ __global__ __launch_bounds__(256) void k_planes_t(const T* x, int64_t rows, int 
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const int r = ty + 4 * k;
-            const bool in = r0 + r < rows && c0 + tx < d;
-            y[k] = in ? Vec<T>::one(x + (r0 + r) * ld + c0 + tx) : 0.f;
+            const bool in = r0 + r < o.rows && c0 + tx < p.d;
+            y[k] = in ? Vec<T>::one((const T*)o.x + (r0 + r) * o.ld + c0 + tx) : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            uint16_t p[P];
+            uint16_t cut[P];
             if (F16)
-                p[0] = f32_to_f16(y[k] * up);
+                cut[0] = f32_to_f16(y[k] * up);
             else
-                Planes<T>::cut(y[k], p);
+                Planes<T>::cut(y[k], cut);
 #pragma unroll
-            for (int q = 0; q < P; ++q) tile[q][tx][ty + 4 * k] = p[q];
+            for (int q = 0; q < P; ++q) tile[q][tx][ty + 4 * k] = cut[q];
         }
         __syncthreads();
         for (int c = ty; c < 64; c += 4)
-            if (c0 + c < d)
+            if (c0 + c < p.d)
 #pragma unroll
                 for (int q = 0; q < P; ++q)
-                    out[q * plane + panel_at(d, c0 + c, r0 + tx)] = tile[q][c][tx];
+                    o.out[q * plane + panel_at(p.d, c0 + c, r0 + tx)] = tile[q][c][tx];
         __syncthreads();
     }
 }
@@ -770,21 +783,18 @@ static bool head_shape_ok(int64_t n, int32_t d, int32_t v) {
 static bool head_supported(int32_t d, int32_t v) { return d <= HEAD_MAX_DIM && v <= HEAD_MAX_CODES; }
 
 template <typename T>
-static void planes(const void* x, int64_t rows, int d, int64_t ld, int kp, void* out, int64_t plane,
-                   hipStream_t st) {
+static void planes(const LayoutPair& p, int kp, hipStream_t st) {
+    const int64_t rows = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
     const int64_t work = (rows * (kp / 8) + 255) / 256;
     const unsigned grid = (unsigned)(work < 65536 ? work : 65536);
-    if (grid)
-        hipLaunchKernelGGL((k_planes<T>), dim3(grid), dim3(256), 0, st, (const T*)x, rows, d, ld, kp,
-                           (uint16_t*)out, plane);
+    if (grid) hipLaunchKernelGGL((k_planes<T>), dim3(grid, 2), dim3(256), 0, st, p, kp);
 }
 template <typename T>
-static void planes_t(const void* x, int64_t rows, int d, int64_t ld, int rp, const uint32_t* range,
-                     void* out, hipStream_t st) {
-    const int64_t work = (int64_t)((d + 63) / 64) * (rp / 64);
+static void planes_t(const LayoutPair& p, const uint32_t* range, hipStream_t st) {
+    const int64_t rows = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
+    const int64_t work = (int64_t)((p.d + 63) / 64) * ((rows + 63) / 64);
     const unsigned grid = (unsigned)(work < 65536 ? work : 65536);
-    hipLaunchKernelGGL((k_planes_t<T>), dim3(grid), dim3(256), 0, st, (const T*)x, rows, d, ld, rp,
-                       range, (uint16_t*)out, (int64_t)d * rp);
+    if (grid) hipLaunchKernelGGL((k_planes_t<T>), dim3(grid, 2), dim3(256), 0, st, p, range);
 }
 
 static unsigned tile_grid(int mt, int nt) {
@@ -827,48 +837,48 @@ struct HeadIn {
     int32_t d, v, dtype;
 };
 
-// Lays out W once, then per chunk of rows fills a.in for the logits' product.
-template <typename T>
-static void head_weight(const HeadIn& x, const HeadPlan& q, char* ws, GemmIn* g, hipStream_t st) {
-    g->pairs = q.pairs;
-    g->kp = q.dp;
-    g->m = x.v;
-    if (q.pack_w) {
-        g->a = (const uint16_t*)(ws + q.o_w);
-        g->lda = GK;
-        g->step_a = (int64_t)x.v * GK;
-        g->plane_a = (int64_t)x.v * q.dp;
-        planes<T>(x.w, x.v, x.d, x.ldw, q.dp, ws + q.o_w, g->plane_a, st);
-    } else {
-        g->a = (const uint16_t*)x.w;
-        g->lda = x.ldw;
-        g->step_a = GK;
-    }
-}
+// The logits' product for `rows` rows from r0 on: lays out what needs it (W with the
+// first rows).
 template <typename T>
 static void head_rows(const HeadIn& x, const HeadPlan& q, char* ws, int64_t r0, int64_t rows, HeadArgs* a,
                       hipStream_t st) {
     const T* h = (const T*)x.h + r0 * x.ldh;
     GemmIn* g = &a->in;
+    LayoutPair p{};
+    p.d = x.d;
+    g->pairs = q.pairs;
+    g->kp = q.dp;
+    g->m = x.v;
     g->n = a->rows = (int32_t)rows;
+    if (q.pack_w) {
+        g->a = (const uint16_t*)(ws + q.o_w);
+        g->lda = GK;
+        g->step_a = (int64_t)x.v * GK;
+        g->plane_a = (int64_t)x.v * q.dp;
+        if (r0 == 0) p.o[0] = Layout{x.w, x.v, x.ldw, (uint16_t*)(ws + q.o_w)};
+    } else {
+        g->a = (const uint16_t*)x.w;
+        g->lda = x.ldw;
+        g->step_a = GK;
+    }
     if (q.pack_h) {
         g->b = (const uint16_t*)(ws + q.o_h);
         g->ldb = GK;
         g->step_b = rows * GK;
         g->plane_b = rows * q.dp;
-        planes<T>(h, rows, x.d, x.ldh, q.dp, ws + q.o_h, g->plane_b, st);
+        p.o[1] = Layout{h, rows, x.ldh, (uint16_t*)(ws + q.o_h)};
     } else {
         g->b = (const uint16_t*)h;
         g->ldb = x.ldh;
         g->step_b = GK;
     }
+    planes<T>(p, q.dp, st);
 }
 
 template <typename T>
 static hipError_t head_score(const HeadIn& x, const HeadPlan& q, ScoreArgs s, char* ws,
                              hipStream_t st) {
     HeadArgs a{};
-    head_weight<T>(x, q, ws, &a.in, st);
     a.x = (float*)(ws + q.o_x);
     a.part = (ScorePart*)(ws + q.o_part);
     for (int64_t r0 = 0; r0 < x.n; r0 += q.chunk) {
@@ -912,7 +922,6 @@ static hipError_t head_score(const HeadIn& x, const HeadPlan& q, ScoreArgs s, ch
 template <typename T>
 static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void* dh, int64_t lddh,
                             void* dw, int64_t lddw, char* ws, hipStream_t st) {
-    head_weight<T>(x, q, ws, &a.in, st);
     uint16_t* wt = (uint16_t*)(ws + q.o_wt);
     uint16_t* ht = (uint16_t*)(ws + q.o_ht);
     uint32_t* range = (uint32_t*)(ws + q.o_range);  // W, h, dx
@@ -932,7 +941,6 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         r.row_exp = row_exp;
         hipLaunchKernelGGL(k_head_range, dim3(RANGE_BLOCKS), dim3(256), 0, st, r);
     }
-    if (dh) planes_t<T>(x.w, x.v, x.d, x.ldw, q.vp, range, wt, st);
     a.range = range + 2 * RANGE_BLOCKS;
     a.dx = (uint16_t*)(ws + q.o_dx);
     a.dxt = (uint16_t*)(ws + q.o_dxt);
@@ -956,6 +964,11 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
             using C = Tile<B>;
             launch_tiles<B>(k_head_dx<T, C::BM, C::BN, C::WM, C::WN>, a, 1, true, st);
         });
+        LayoutPair turned{};
+        turned.d = x.d;
+        if (dh && r0 == 0) turned.o[0] = Layout{x.w, x.v, x.ldw, wt};
+        if (dw) turned.o[1] = Layout{(const T*)x.h + r0 * x.ldh, rows, x.ldh, ht};
+        planes_t<T>(turned, range, st);
         if (dh) {
             GradOut o{};
             o.in = GemmIn{wt, a.dx, GK, GK, (int64_t)x.d * GK, rows * GK, (int64_t)x.d * q.vp, a.plane_dx,
@@ -967,8 +980,6 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
             launch_grad<T>(o, part, st);
         }
         if (dw) {
-            planes_t<T>((const T*)x.h + r0 * x.ldh, rows, x.d, x.ldh, a.np, range + RANGE_BLOCKS, ht,
-                        st);
             GradOut o{};
             o.in = GemmIn{ht, a.dxt, GK, GK, (int64_t)x.d * GK, (int64_t)x.v * GK, (int64_t)x.d * a.np,
                           a.plane_dxt, x.d, x.v, a.np, q.pairs};
