@@ -7,6 +7,12 @@
 // plane products that reach 2^-24 of it, smallest first, in the same fp32
 // accumulators. bf16 and fp16 operands have one plane.
 //
+// B may also lie with the contracted axis across (TB): panels of 64 of its rows,
+// [n / 64][k][64], as the product before wrote them with those rows contiguous. Its
+// fragments are then read with the LDS's transposing load (16 lanes read four
+// k of 16 rows and get four k of one row each), and k past the operand's end
+// reads as 0.
+//
 // A workgroup of WM x WN waves computes a BM x BN tile, 64 of the contracted
 // axis per step: both operands' steps are copied from memory straight into LDS
 // (two buffers; the next step's copies run under this step's products; the
@@ -48,6 +54,7 @@ struct GemmIn {
     int64_t plane_a, plane_b;    // plane strides (values)
     int32_t m, n, kp;            // kp: contracted length, a multiple of GK
     int32_t pairs;               // plane products: 1 or 6
+    int32_t kb;                  // TB: values of the contracted axis that b has
 };
 
 // Plane products, smallest first: (lo,hi) (hi,lo) (mid,mid) (mid,hi) (hi,mid) (hi,hi).
@@ -57,8 +64,8 @@ __device__ __forceinline__ void gemm_pair(int pairs, int p, int* pa, int* pb) {
     *pb = (0x118 >> (2 * q)) & 3;  // 0 2 1 0 1 0
 }
 
-// ONE: operands of one plane.
-template <int BM, int BN, int WM, int WN, bool ONE>
+// ONE: operands of one plane. TB: b lies with the contracted axis across.
+template <int BM, int BN, int WM, int WN, bool ONE, bool TB = false>
 struct Gemm {
     static constexpr int NT = 64 * WM * WN;
     static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
@@ -85,8 +92,44 @@ struct Gemm {
                 (int)(off + g * (NT / 8) * row_bytes), 0, 0, 0);
     }
 
+    // TB: this wave's 8-row groups of a step are neighbours, in one panel
+    static constexpr int PER = BN / 8 / (NT / 64);
+    static __device__ __forceinline__ int turn_key(int k) {
+        return (((k >> 3) & 3) ^ ((k >> 1) & 1)) << 1;
+    }
+    static __device__ __forceinline__ void copy_across(__amdgpu_buffer_rsrc_t rs, unsigned char* dst,
+                                                       int wave, int lane) {
+        const int r = lane >> 3, p = lane & 7;
+#pragma unroll
+        for (int g = 0; g < PER; ++g) {
+            const int grp = wave * PER + g;
+            const int k = grp % 8 * 8 + r;  // of the panel's 64
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (__attribute__((address_space(3))) void*)(dst + grp * 1024), 16,
+                k * 128 + ((p ^ turn_key(k)) << 4), 0, 0, 0);
+        }
+    }
+    // rows 16 b .. 16 b + 15 of the tile, half c of a step: lane 16 h + i gets 8 k of row i
+    template <typename V8>
+    static __device__ __forceinline__ V8 read_across(const unsigned char* d, int b, int c, int h, int i) {
+        typedef short s4 __attribute__((ext_vector_type(4)));
+        union {
+            s4 part[2];
+            V8 v;
+        } u;
+        const int chunk = b % 4 * 2 + ((i & 3) >> 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int k = 32 * c + 8 * h + 4 * t + (i >> 2);
+            const unsigned char* at =
+                d + b / 4 * 8192 + k * 128 + ((chunk ^ turn_key(k)) << 4) + (i & 1) * 8;
+            u.part[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at);
+        }
+        return u.v;
+    }
+
     const uint16_t *next_a, *next_b;  // the step to be copied next, from the tile's first row
-    int bytes_a, bytes_b;             // from there to the end of the step's last row
+    int bytes_a, bytes_b;             // from there to the end of the step's last row (TB: of the panel)
     int steps;                        // of the tile
     int left, pair;                   // steps left in the plane product, its number
 
@@ -102,8 +145,21 @@ struct Gemm {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         copy<BM>(__builtin_amdgcn_make_buffer_rsrc((void*)next_a, (short)0, real ? bytes_a : 0, BUF_RSRC_WORD3),
                  (uint32_t)in.lda * 2, d, wave, lane);
-        copy<BN>(__builtin_amdgcn_make_buffer_rsrc((void*)next_b, (short)0, real ? bytes_b : 0, BUF_RSRC_WORD3),
-                 (uint32_t)in.ldb * 2, d + A_BYTES, wave, lane);
+        const uint16_t* pb = next_b;
+        if constexpr (TB) {  // a wave's own panel: uniform, but not to the compiler
+            const uint64_t u = (uint64_t)next_b;
+            pb = (const uint16_t*)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32) |
+                                   (uint32_t)__builtin_amdgcn_readfirstlane((int)u));
+            bytes_b = __builtin_amdgcn_readfirstlane(bytes_b);
+        }
+        const __amdgpu_buffer_rsrc_t sb = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)pb, (short)0, real ? bytes_b : 0, BUF_RSRC_WORD3);
+        if constexpr (TB) {
+            copy_across(sb, d + A_BYTES, wave, lane);
+            bytes_b = bytes_b > GK * 128 ? bytes_b - GK * 128 : 0;
+        } else {
+            copy<BN>(sb, (uint32_t)in.ldb * 2, d + A_BYTES, wave, lane);
+        }
         next_a += in.step_a;
         next_b += in.step_b;
         if constexpr (!ONE)
@@ -114,6 +170,11 @@ struct Gemm {
         gemm_pair(ONE ? 1 : in.pairs, p, &pa, &pb);
         next_a = in.a + pa * in.plane_a + kk * in.step_a + m * in.lda;
         next_b = in.b + pb * in.plane_b + kk * in.step_b + n * in.ldb;
+        if constexpr (TB) {
+            const int row = n + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * PER / 8 * 64;
+            next_b += (int64_t)(row - n) * in.ldb;
+            bytes_b = row < in.n && in.kb > kk * GK ? (in.kb - kk * GK) * 128 : 0;
+        }
         pair = p;
         left = in.kp / GK - kk;
     }
@@ -126,7 +187,7 @@ struct Gemm {
         const int ks = in.kp / GK;
         steps = last - first;
         bytes_a = span(in.lda, m, in.m, BM);
-        bytes_b = span(in.ldb, n, in.n, BN);
+        if constexpr (!TB) bytes_b = span(in.ldb, n, in.n, BN);
         seek(in, m, n, first / ks, first % ks);
         issue(in, m, n, true, l0);
         issue(in, m, n, steps > 1, l1);
@@ -159,7 +220,10 @@ struct Gemm {
                 fa[x] = *(const V8*)(da + at((wm * TM + x) * 16 + i, 4 * c + h));
 #pragma unroll
             for (int y = 0; y < TN; ++y)
-                fb[y] = *(const V8*)(db + at((wn * TN + y) * 16 + i, 4 * c + h));
+                if constexpr (TB)
+                    fb[y] = read_across<V8>(db, wn * TN + y, c, h, i);
+                else
+                    fb[y] = *(const V8*)(db + at((wn * TN + y) * 16 + i, 4 * c + h));
         };
         auto multiply = [&](const V8(&fa)[TM], const V8(&fb)[TN]) {
 #pragma unroll
@@ -169,16 +233,20 @@ struct Gemm {
         };
         // the order of a half: its copies and LDS reads one by one between the products
         auto spread = [&](const int copies) {
+            auto put_copies = [&]() {
 #pragma unroll
-            for (int g = 0; g < copies; ++g) {
-                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // matrix product
-                __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // memory read
-            }
+                for (int g = 0; g < copies; ++g) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // matrix product
+                    __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // memory read
+                }
+            };
+            if constexpr (!TB) put_copies();
 #pragma unroll
-            for (int g = 0; g < TM + TN; ++g) {
+            for (int g = 0; g < TM + (TB ? 2 : 1) * TN; ++g) {
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
                 __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
             }
+            if constexpr (TB) put_copies();
             __builtin_amdgcn_sched_group_barrier(0x8, TM * TN, 0);
         };
         // the first step's copies have landed; the second's may be in flight
@@ -200,8 +268,11 @@ struct Gemm {
             __builtin_amdgcn_s_waitcnt(0);
             __syncthreads();  // ... and every wave's
             __builtin_amdgcn_sched_barrier(0);
-            issue(in, m, n, togo > 2, cur);
+            // the transposing loads wait for every copy in flight (the compiler does
+            // not tell their buffers apart): they go first
+            if constexpr (!TB) issue(in, m, n, togo > 2, cur);
             read(fa[0], fb[0], other, 0);
+            if constexpr (TB) issue(in, m, n, togo > 2, cur);
             multiply(fa[1], fb[1]);
             spread(COPIES);
             __builtin_amdgcn_sched_barrier(0);

@@ -9,10 +9,15 @@
 // fp32 logits into the workspace and scored from there.
 // Gradient: the logits' tiles are computed again, and the epilogue turns them
 // into dx = scale (g_lp ([v = t] - p) - g_H p (log p + H)), written for a chunk of
-// rows in both orders (n x v and v x n), from which two more products make
-// dh = dx W and dW = dx^T h. For bf16 data dx is rounded to bf16, the type of
-// the matrix units' operands; for fp32 data it is kept in three planes like
-// the operands.
+// rows, from which two more products make dh = dx W and dW = dx^T h (the latter
+// reads dx across, see gmm_gemm.h). For fp32 data dx is cut into three planes like the
+// operands. For bf16 data dx is rounded to fp16, whose 11 bits leave an eighth
+// of bf16's error at the same rate; W and h (8 bits each) go into fp16
+// unrounded. fp16's short range is met by powers of two taken out of the sums
+// again: W and h are multiplied to a largest value in [2^14, 2^15), dx's rows by
+// their own bounds (a row of small gradients keeps its digits); for dW, h's rows
+// are divided by the same, relative to the row of the largest bound. What then
+// lies below 2^-29 of the largest value loses digits, and below 2^-39 is dropped.
 //
 // Orientation: the tiles' rows are the axis that the outputs are contiguous in
 // (codes for logits, dims for the gradients), their columns the rows of h (or
@@ -37,7 +42,7 @@ constexpr int32_t HEAD_MAX_CODES = 1 << 22;
 constexpr int64_t HEAD_MAX_LD = (int64_t)1 << 22;  // 256 rows span at most 2^31 bytes
 constexpr size_t HEAD_LOGIT_BYTES = (size_t)256 << 20;  // fp32 logits of one chunk of rows
 constexpr size_t HEAD_PART_BYTES = (size_t)64 << 20;    // tile statistics of one chunk
-constexpr size_t HEAD_DX_BYTES = (size_t)1 << 30;       // dx of one chunk, both orders
+constexpr size_t HEAD_DX_BYTES = (size_t)512 << 20;       // dx of one chunk
 constexpr size_t HEAD_SPLIT_BYTES = (size_t)128 << 20;  // partial sums of a split product
 constexpr int HEAD_MAX_SPLIT = 16;
 
@@ -125,7 +130,8 @@ __global__ __launch_bounds__(256) void k_planes(LayoutPair p, int kp) {
 constexpr int RANGE_BLOCKS = 1024;
 
 // The exponent e for which a value with these magnitude bits, times 2^e, lies in
-// [2^14, 2^15); 0 for zero and for what is not finite.
+// [2^14, 2^15); 0 for zero and for what is not finite. 2^e may lie outside fp32's
+// range: it is applied with ldexpf.
 __device__ __forceinline__ int range_of(uint32_t bits) {
     if (bits == 0 || bits >= 0x7f800000u) return 0;
     int e;
@@ -154,14 +160,22 @@ __device__ __forceinline__ int range_exp(const uint32_t* part) {
 __device__ __forceinline__ uint32_t rows_range(const uint16_t* x, int64_t rows, int d, int64_t ld) {
     uint32_t m = 0;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < rows; r += RANGE_BLOCKS * 4)
+    constexpr int U = 4;  // rows in flight
+    for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < rows; r += U * RANGE_BLOCKS * 4)
         for (int c = lane * 8; c < d; c += 512) {
-            const Raw16 v = load_vec(x + r * ld, c, (int64_t)d);
+            Raw16 v[U];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t b = __float_as_uint(Vec<uint16_t>::get(v, k)) & 0x7fffffffu;
-                if (b < 0x7f800000u && b > m) m = b;
+            for (int u = 0; u < U; ++u) {
+                const int64_t q = r + u * RANGE_BLOCKS * 4;
+                v[u] = load_zero(x + (q < rows ? q : r) * ld, c, (int64_t)d);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t b = __float_as_uint(Vec<uint16_t>::get(v[u], k)) & 0x7fffffffu;
+                    if (b < 0x7f800000u && b > m) m = b;
+                }
         }
     return m;
 }
@@ -218,43 +232,60 @@ __device__ __forceinline__ uint16_t f32_to_f16(float f) {
 
 // The planes of x^T: d rows of x's rows, padded with 0 to a multiple of 64: 64 x 64 tiles
 // turned through LDS. bf16 values become fp16 times the power of two of `range`
-// (W's and h's).
+// (W's and h's); h's rows (row_exp) also times 2^(e - row_exp), e the exponent of
+// dx's largest bound: what dx's rows were multiplied by, relative to that row.
 template <typename T>
-__global__ __launch_bounds__(256) void k_planes_t(LayoutPair p, const uint32_t* range) {
+__global__ __launch_bounds__(256) void k_planes_t(LayoutPair p, const uint32_t* range,
+                                                  const int32_t* row_exp) {
     constexpr int P = Planes<T>::P;
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
-    __shared__ uint16_t tile[P][64][66];
+    constexpr int VE = Vec<T>::VE, PER_ROW = 64 / VE;  // vectors of a tile's row
+    __shared__ __align__(16) uint16_t tile[P][64][72];
     const Layout o = p.o[blockIdx.y];
     const int ct = (p.d + 63) / 64;
     const int64_t rp = (o.rows + 63) / 64 * 64, total = ct * (rp / 64), plane = p.d * rp;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    const float up = F16 ? ldexpf(1.f, range_exp(range + blockIdx.y * RANGE_BLOCKS)) : 1.f;
+    const int tid = threadIdx.x;
+    const int up = F16 ? range_exp(range + blockIdx.y * RANGE_BLOCKS) : 0;
+    const int e = F16 && blockIdx.y == 1 ? range_exp(range + 2 * RANGE_BLOCKS) : 0;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int64_t r0 = b / ct * 64;
         const int c0 = (int)(b % ct) * 64;
-        float y[16];  // all of a thread's loads in flight
+        constexpr int N = 64 * PER_ROW / 256;  // vectors per thread
+        Raw16 v[N];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int r = ty + 4 * k;
-            const bool in = r0 + r < o.rows && c0 + tx < p.d;
-            y[k] = in ? Vec<T>::one((const T*)o.x + (r0 + r) * o.ld + c0 + tx) : 0.f;
+        for (int k = 0; k < N; ++k) {
+            const int r = (k * 256 + tid) / PER_ROW, c = (k * 256 + tid) % PER_ROW * VE;
+            v[k] = r0 + r < o.rows ? load_zero((const T*)o.x + (r0 + r) * o.ld, c0 + c, (int64_t)p.d)
+                                   : Raw16{{0u, 0u, 0u, 0u}};
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            uint16_t cut[P];
-            if (F16)
-                cut[0] = f32_to_f16(y[k] * up);
-            else
-                Planes<T>::cut(y[k], cut);
+        for (int k = 0; k < N; ++k) {
+            const int r = (k * 256 + tid) / PER_ROW, c = (k * 256 + tid) % PER_ROW * VE;
+            int by = up;
+            // a row without gradient has exponent 0: its dx is 0
+            if (F16 && blockIdx.y == 1 && r0 + r < o.rows) by += min(e - row_exp[r0 + r], 0);
 #pragma unroll
-            for (int q = 0; q < P; ++q) tile[q][tx][ty + 4 * k] = cut[q];
+            for (int u = 0; u < VE; ++u) {
+                uint16_t cut[P];
+                const float y = Vec<T>::get(v[k], u);
+                if (F16)
+                    cut[0] = f32_to_f16(ldexpf(y, by));
+                else
+                    Planes<T>::cut(y, cut);
+#pragma unroll
+                for (int q = 0; q < P; ++q) tile[q][c + u][r] = cut[q];
+            }
         }
         __syncthreads();
-        for (int c = ty; c < 64; c += 4)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = (k * 256 + tid) / 8, r = (k * 256 + tid) % 8 * 8;
             if (c0 + c < p.d)
 #pragma unroll
                 for (int q = 0; q < P; ++q)
-                    o.out[q * plane + panel_at(p.d, c0 + c, r0 + tx)] = tile[q][c][tx];
+                    *(uint4*)(o.out + q * plane + panel_at(p.d, c0 + c, r0 + r)) =
+                        *(const uint4*)&tile[q][c][r];
+        }
         __syncthreads();
     }
 }
@@ -269,10 +300,9 @@ struct HeadArgs {
     float* x;            // logits or target logits of the chunk
     ScorePart* part;     // [rows][mt]
     const float *norm, *entropy, *g_logprob, *g_entropy;
-    uint16_t *dx, *dxt;  // planes of rows x vp and v x np, in panels
-    int64_t plane_dx, plane_dxt;
-    int32_t vp, np;
-    const uint32_t* range;   // of dx over all rows
+    uint16_t* dx;        // planes of rows x vp, in panels
+    int64_t plane_dx;
+    int32_t vp;
     const int32_t* row_exp;  // of dx's rows
 };
 
@@ -430,88 +460,47 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_logits(HeadArgs p) {
     }
 }
 
-// dx of a chunk of rows, in both orders; 0 in the padding. The order with rows
-// contiguous is turned in LDS, 16 codes of each wave row at a time through two
-// buffers (a code's rows in 32-byte pieces rotated by four codes, so that the four
-// codes that a wave writes at once lie in different banks).
+// dx of a chunk of rows; 0 in the padding.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
     using G = Gemm<BM, BN, WM, WN, std::is_same<T, uint16_t>::value>;
     constexpr int P = Planes<T>::P;
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
-    constexpr int NT = G::NT, TURN = WM * 16 * BN * 2;
-    __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE], turns[2 * TURN];
-    const int tid = threadIdx.x;
-    const float up_all = F16 ? ldexpf(1.f, range_exp(p.range)) : 1.f;
+    __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
     gemm_walk<bf16x8, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
-        GradRow k[G::TN];
-        float up[G::TN], base[G::TN];
 #pragma unroll
         for (int y = 0; y < G::TN; ++y) {
             const int r = n0 + G::col(y);
-            k[y] = GradRow{};
-            up[y] = 1.f;
-            if (r < p.in.n) {
-                k[y] = grad_row(grad_args(p), r);
-                if (F16) up[y] = ldexpf(1.f, p.row_exp[r]);
-            }
-            base[y] = fmaf(k[y].gh, k[y].h, k[y].glp);
-        }
+            if (r >= p.in.n) continue;
+            const GradRow k = grad_row(grad_args(p), r);
+            const int up = F16 ? p.row_exp[r] : 0;
+            const float base = fmaf(k.gh, k.h, k.glp);
 #pragma unroll
-        for (int x = 0; x < G::TM; ++x) {
-            const int c = m0 + G::row(x);
-            uint16_t ot[P][G::TN][4];  // for the turned order
-#pragma unroll
-            for (int y = 0; y < G::TN; ++y) {
-                const int r = n0 + G::col(y);
-                const bool there = r < p.in.n;
+            for (int x = 0; x < G::TM; ++x) {
+                const int c = m0 + G::row(x);
                 uint16_t o[P][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float lp = fmaf(g.acc[x][y][q], k[y].scale, -k[y].m) - k[y].logs;
+                    const float lp = fmaf(g.acc[x][y][q], k.scale, -k.m) - k.logs;
                     const float pr = exp_neg(lp);
-                    const float hot = c + q == k[y].t ? k[y].glp : 0.f;
-                    float v = k[y].scale * fmaf(-pr, fmaf(k[y].gh, lp, base[y]), hot);
-                    if (!there || c + q >= p.in.m) v = 0.f;
+                    const float hot = c + q == k.t ? k.glp : 0.f;
+                    float v = k.scale * fmaf(-pr, fmaf(k.gh, lp, base), hot);
+                    if (c + q >= p.in.m) v = 0.f;
                     if (F16) {
-                        o[0][q] = f32_to_f16(v * up[y]);
-                        ot[0][y][q] = f32_to_f16(v * up_all);
+                        o[0][q] = f32_to_f16(ldexpf(v, up));
                     } else {
                         uint16_t cut[P];
                         Planes<T>::cut(v, cut);
 #pragma unroll
-                        for (int j = 0; j < P; ++j) o[j][q] = ot[j][y][q] = cut[j];
+                        for (int j = 0; j < P; ++j) o[j][q] = cut[j];
                     }
                 }
-                if (there && c < p.vp)  // vp is a multiple of 64: whole fours
+                if (c < p.vp)  // vp is a multiple of 64: whole fours
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         *(uint2*)(p.dx + j * p.plane_dx + panel_at(p.in.n, r, c)) =
                             uint2{(uint32_t)o[j][0] | ((uint32_t)o[j][1] << 16),
                                   (uint32_t)o[j][2] | ((uint32_t)o[j][3] << 16)};
-            }
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                unsigned char* turn = turns + ((x * P + j) & 1) * TURN;
-#pragma unroll
-                for (int y = 0; y < G::TN; ++y)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        // code of the 16 WM: wave row, 4 h + q
-                        const int e = (tid >> 6) / WN * 16 + 4 * ((tid & 63) >> 4) + q;
-                        *(uint16_t*)(turn + e * BN * 2 + ((G::col(y) * 2) ^ ((e & 12) << 3))) =
-                            ot[j][y][q];
-                    }
-                __syncthreads();
-                // 8 rows of a code per lane, 64 rows of each code after another
-#pragma unroll
-                for (int u = tid; u < WM * 16 * (BN / 8); u += NT) {
-                    const int e = u / 8 % (WM * 16), r = u / 8 / (WM * 16) * 64 + u % 8 * 8;
-                    const int code = m0 + e / 16 * (BM / WM) + x * 16 + e % 16;
-                    if (code < p.in.m && n0 + r < p.np)  // np is a multiple of 64
-                        *(uint4*)(p.dxt + j * p.plane_dxt + panel_at(p.in.m, code, n0 + r)) =
-                            *(const uint4*)(turn + e * BN * 2 + ((r * 2) ^ ((e & 12) << 3)));
-                }
             }
         }
     });
@@ -575,9 +564,9 @@ __device__ __forceinline__ int grad_back(const GradOut& p) {
     return -range_exp(p.range_a) - (p.row_exp ? 0 : range_exp(p.range_b));
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, bool TB, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
-    using G = Gemm<BM, BN, WM, WN, std::is_same<T, uint16_t>::value>;
+    using G = Gemm<BM, BN, WM, WN, std::is_same<T, uint16_t>::value, TB>;
     __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
     int tm, tn;
     if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
@@ -714,7 +703,7 @@ struct HeadPlan {
     int planes, pairs, dp, vp, np;
     int64_t chunk;      // rows per chunk, a multiple of 256
     bool pack_h, pack_w;
-    size_t o_w, o_h, o_x, o_part, o_wt, o_ht, o_dx, o_dxt, o_sum, o_split, o_score, o_range, o_exp, bytes;
+    size_t o_w, o_h, o_x, o_part, o_wt, o_ht, o_dx, o_sum, o_split, o_score, o_range, o_exp, bytes;
 };
 
 static bool direct(const void* p, int32_t d, int64_t ld, int dtype) {
@@ -736,7 +725,7 @@ static HeadPlan head_plan(int64_t n, int32_t d, int32_t v, int dtype, int32_t m,
     const int64_t tiles = (v + 63) / 64;
     size_t row, most;
     if (grad) {
-        row = (size_t)q.planes * q.vp * 4;
+        row = (size_t)q.planes * q.vp * 2;
         most = HEAD_DX_BYTES;
     } else if (m > 0) {
         row = (size_t)v * 4;
@@ -766,7 +755,6 @@ static HeadPlan head_plan(int64_t n, int32_t d, int32_t v, int dtype, int32_t m,
     q.o_wt = take(grad ? ps * d * q.vp : 0);
     q.o_ht = take(grad ? ps * d * q.np : 0);
     q.o_dx = take(grad ? ps * c * q.vp : 0);
-    q.o_dxt = take(grad ? ps * v * q.np : 0);
     q.o_sum = take(grad && q.chunk < n ? (size_t)v * d * 4 : 0);
     const size_t most_out = (size_t)(q.chunk > v ? q.chunk : v) * d * 4 * HEAD_MAX_SPLIT;
     q.o_split = take(grad ? (most_out < HEAD_SPLIT_BYTES ? most_out : HEAD_SPLIT_BYTES) : 0);
@@ -790,11 +778,13 @@ static void planes(const LayoutPair& p, int kp, hipStream_t st) {
     if (grid) hipLaunchKernelGGL((k_planes<T>), dim3(grid, 2), dim3(256), 0, st, p, kp);
 }
 template <typename T>
-static void planes_t(const LayoutPair& p, const uint32_t* range, hipStream_t st) {
+static void planes_t(const LayoutPair& p, const uint32_t* range, const int32_t* row_exp,
+                     hipStream_t st) {
     const int64_t rows = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
     const int64_t work = (int64_t)((p.d + 63) / 64) * ((rows + 63) / 64);
     const unsigned grid = (unsigned)(work < 65536 ? work : 65536);
-    if (grid) hipLaunchKernelGGL((k_planes_t<T>), dim3(grid, 2), dim3(256), 0, st, p, range);
+    if (grid) hipLaunchKernelGGL((k_planes_t<T>), dim3(grid, 2), dim3(256), 0, st, p, range,
+                                 row_exp);
 }
 
 static unsigned tile_grid(int mt, int nt) {
@@ -813,7 +803,7 @@ static void launch_tiles(K kernel, A& a, int split, bool walk, hipStream_t st) {
 }
 
 // out = the product of o.in, with the tile and split that suit it.
-template <typename T>
+template <typename T, bool TB>
 static void launch_grad(GradOut& o, float* part, hipStream_t st) {
     const Choice c = choose_tile(o.in.m, o.in.n, (int64_t)o.in.kp / GK * o.in.pairs, HEAD_MAX_SPLIT);
     o.split = c.split;
@@ -822,7 +812,7 @@ static void launch_grad(GradOut& o, float* part, hipStream_t st) {
     with_tile(c.tile, [&](auto b) {
         constexpr int B = decltype(b)::value;
         using C = Tile<B>;
-        launch_tiles<B>(k_head_grad<T, C::BM, C::BN, C::WM, C::WN>, o, c.split, false, st);
+        launch_tiles<B>(k_head_grad<T, TB, C::BM, C::BN, C::WM, C::WN>, o, c.split, false, st);
     });
     if (c.split > 1) {
         const int64_t work = ((int64_t)o.in.n * ((o.in.m + 3) / 4) + 255) / 256;
@@ -941,18 +931,14 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         r.row_exp = row_exp;
         hipLaunchKernelGGL(k_head_range, dim3(RANGE_BLOCKS), dim3(256), 0, st, r);
     }
-    a.range = range + 2 * RANGE_BLOCKS;
     a.dx = (uint16_t*)(ws + q.o_dx);
-    a.dxt = (uint16_t*)(ws + q.o_dxt);
     a.vp = q.vp;
     const HeadArgs all = a;
     for (int64_t r0 = 0; r0 < x.n; r0 += q.chunk) {
         const int64_t rows = x.n - r0 < q.chunk ? x.n - r0 : q.chunk;
         head_rows<T>(x, q, ws, r0, rows, &a, st);
-        a.np = pad(rows);
         a.row_exp = row_exp + r0;
         a.plane_dx = rows * q.vp;
-        a.plane_dxt = (int64_t)x.v * a.np;
         a.s.targets = all.s.targets ? all.s.targets + r0 : nullptr;
         a.norm = all.norm + 2 * r0;
         a.entropy = all.entropy ? all.entropy + r0 : nullptr;
@@ -968,7 +954,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         turned.d = x.d;
         if (dh && r0 == 0) turned.o[0] = Layout{x.w, x.v, x.ldw, wt};
         if (dw) turned.o[1] = Layout{(const T*)x.h + r0 * x.ldh, rows, x.ldh, ht};
-        planes_t<T>(turned, range, st);
+        planes_t<T>(turned, range, a.row_exp, st);
         if (dh) {
             GradOut o{};
             o.in = GemmIn{wt, a.dx, GK, GK, (int64_t)x.d * GK, rows * GK, (int64_t)x.d * q.vp, a.plane_dx,
@@ -977,12 +963,14 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
             o.ldo = lddh;
             o.range_a = range;
             o.row_exp = row_exp + r0;
-            launch_grad<T>(o, part, st);
+            launch_grad<T, false>(o, part, st);
         }
         if (dw) {
             GradOut o{};
-            o.in = GemmIn{ht, a.dxt, GK, GK, (int64_t)x.d * GK, (int64_t)x.v * GK, (int64_t)x.d * a.np,
-                          a.plane_dxt, x.d, x.v, a.np, q.pairs};
+            // dx read across: panels of 64 codes, rows * 64 values each
+            const int np = pad(rows);
+            o.in = GemmIn{ht, a.dx, GK, rows, (int64_t)x.d * GK, GK * GK, (int64_t)x.d * np,
+                          a.plane_dx, x.d, x.v, np, q.pairs, (int32_t)rows};
             float* sum = (float*)(ws + q.o_sum);
             o.add = r0 > 0 ? sum : nullptr;
             o.sum = r0 + q.chunk < x.n ? sum : nullptr;
@@ -990,7 +978,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
             o.ldo = lddw;
             o.range_a = range + RANGE_BLOCKS;
             o.range_b = range + 2 * RANGE_BLOCKS;
-            launch_grad<T>(o, part, st);
+            launch_grad<T, true>(o, part, st);
         }
     }
     return hipGetLastError();

@@ -53,18 +53,6 @@ struct MoeArgs {
     void* y;
 };
 
-// 16 bytes of a row, 0 at or past `end`.
-template <typename T>
-__device__ __forceinline__ Raw16 load_zero(const T* p, int64_t i, int64_t end) {
-    constexpr int VE = Vec<T>::VE;
-    if (i + VE <= end) return *reinterpret_cast<const Raw16*>(p + i);
-    Raw16 r = {{0u, 0u, 0u, 0u}};
-#pragma unroll
-    for (int k = 0; k < VE; ++k)
-        if (i + k < end) Vec<T>::set(r, k, Vec<T>::one(p + i + k));
-    return r;
-}
-
 // c += the 16 x 16 product of 4 VE contracted values: lane 16 h + i holds
 // values VE h .. VE h + VE of row i of both operands.
 __device__ __forceinline__ f32x4 mfma_raw(const Raw16& a, const Raw16& b, f32x4 c, uint16_t) {

@@ -76,6 +76,18 @@ __device__ __forceinline__ Raw16 load_vec(const T* p, int64_t i, int64_t end) {
     return r;
 }
 
+// 16 bytes of a row, 0 at or past `end`.
+template <typename T>
+__device__ __forceinline__ Raw16 load_zero(const T* p, int64_t i, int64_t end) {
+    constexpr int VE = Vec<T>::VE;
+    if (i + VE <= end) return *reinterpret_cast<const Raw16*>(p + i);
+    Raw16 r = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+    for (int k = 0; k < VE; ++k)
+        if (i + k < end) Vec<T>::set(r, k, Vec<T>::one(p + i + k));
+    return r;
+}
+
 // ---- wave-wide reductions on the data-parallel lanes (no LDS)
 
 // v of another lane: 0x120 + N rotates each group of 16 lanes by N, 0x138

@@ -298,8 +298,11 @@ int gmm_head_score(const void* hidden, int64_t n, int32_t d, int64_t ldh, const 
  * in the operands' type, rounded once from fp32 sums (leading dimensions lddh,
  * lddw >= d). Either may be NULL (not computed), not both. They must not overlap
  * hidden or weight. dx is computed a chunk of rows at a time into the
- * workspace: in bf16 for bf16 operands, exactly for fp32. n = 0 sets d_weight to
- * 0. Sizes as for gmm_head_score. */
+ * workspace: exactly for fp32 operands; for bf16 in fp16, scaled by a power of two for
+ * each row (d_hidden) or for all rows (d_weight), with 11 significant bits
+ * down to 2^-29 of what a row's (all rows') dx can reach and nothing below 2^-39.
+ * n = 0 sets d_weight to 0. Sizes as for gmm_head_score; the workspace grows with n by 4
+ * bytes a row for bf16. */
 size_t gmm_head_score_backward_workspace_bytes(int64_t n, int32_t d, int32_t v, int32_t dtype);
 int gmm_head_score_backward(const void* hidden, int64_t n, int32_t d, int64_t ldh,
                             const void* weight, int32_t v, int64_t ldw, int32_t dtype,

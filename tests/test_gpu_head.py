@@ -172,7 +172,7 @@ def test_gradient(ops, n, d, v, dtype):
 
 
 def test_gradient_of_several_chunks(ops):
-    # 1 GiB of dx: 4,096 rows of 65,536 codes in bf16, 1,280 in fp32
+    # 512 MiB of dx: 4,096 rows of 65,536 codes in bf16, 1,280 in fp32
     h, w, t = _inputs(4500, 64, 65_536, torch.bfloat16, 8)
     _grad(ops, h, w, t, 1.0)
     h, w, t = _inputs(1500, 32, 65_536, torch.float32, 9)
@@ -195,6 +195,27 @@ def test_gradient_of_far_apart_magnitudes(ops):
     tw = 2.0 ** -10 * (dx.abs().t() @ h.double().abs()) + 2.0 ** -8 * ww.abs()
     # what is dropped: 2^-39 of the largest dx, times h, in each of 60 rows
     tw += 60 * 2.0 ** -39 * float(dx.abs().max()) * float(h.abs().max())
+    assert bool(((dw.double() - ww).abs() <= 1.1 * tw).all())
+
+
+@pytest.mark.parametrize("e", [-115, 115])
+def test_gradient_of_tiny_and_huge_operands(ops, e):
+    # operands at the ends of the range whose products are ordinary; some codes and
+    # rows are 0 (0 times the largest power of two stays 0)
+    h, w, t = _inputs(33, 64, 100, torch.bfloat16, 15)
+    t.clamp_(min=0)
+    h, w = h * 2.0 ** e, w * 2.0 ** -e
+    h[3], w[7] = 0.0, 0.0
+    gl = torch.linspace(-1, 1, 33, device=DEV)
+    gl[5] = 0.0
+    s = ops.head_score(h, w, t)
+    dh, dw = ops.head_score_backward(h, w, t, s.norm, s.entropy, gl)
+    dx = ref.dlogits(h.double() @ w.double().t(), t, gl, torch.zeros_like(gl), 1.0)
+    wh, ww = dx @ w.double(), dx.t() @ h.double()
+    th = 2.0 ** -10 * (dx.abs() @ w.double().abs()) + 2.0 ** -8 * wh.abs()
+    tw = 2.0 ** -10 * (dx.abs().t() @ h.double().abs()) + 2.0 ** -8 * ww.abs()
+    assert dh[5].eq(0).all()
+    assert bool(((dh.double() - wh).abs() <= 1.1 * th).all())
     assert bool(((dw.double() - ww).abs() <= 1.1 * tw).all())
 
 
