@@ -468,32 +468,48 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
     __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
     gemm_walk<bf16x8, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
+        const bool edge = m0 + BM > p.in.m;  // some of the tile's codes are not there
 #pragma unroll
         for (int y = 0; y < G::TN; ++y) {
             const int r = n0 + G::col(y);
             if (r >= p.in.n) continue;
-            const GradRow k = grad_row(grad_args(p), r);
+            GradRow k = grad_row(grad_args(p), r);
+            if (k.m == INFINITY) k.m = 3.0e38f;  // nothing left in the row: p = 0, log p finite
+            // the scale and the row's power of two go into the gradients
             const int up = F16 ? p.row_exp[r] : 0;
-            const float base = fmaf(k.gh, k.h, k.glp);
+            const float gh = -ldexpf(k.scale * k.gh, up);
+            const float base = -ldexpf(k.scale * fmaf(k.gh, k.h, k.glp), up);
+            const float hot = ldexpf(k.scale * k.glp, up);
+            const int t4 = k.t & ~3;  // the four that the target is among
 #pragma unroll
             for (int x = 0; x < G::TM; ++x) {
                 const int c = m0 + G::row(x);
-                uint16_t o[P][4];
+                float v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float lp = fmaf(g.acc[x][y][q], k.scale, -k.m) - k.logs;
-                    const float pr = exp_neg(lp);
-                    const float hot = c + q == k.t ? k.glp : 0.f;
-                    float v = k.scale * fmaf(-pr, fmaf(k.gh, lp, base), hot);
-                    if (c + q >= p.in.m) v = 0.f;
-                    if (F16) {
-                        o[0][q] = f32_to_f16(ldexpf(v, up));
-                    } else {
-                        uint16_t cut[P];
-                        Planes<T>::cut(v, cut);
+                    v[q] = exp_neg(lp) * fmaf(gh, lp, base);
+                }
+                if (c == t4) {
 #pragma unroll
-                        for (int j = 0; j < P; ++j) o[j][q] = cut[j];
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        if (c + q == k.t) v[q] += hot;
+                }
+                if (edge) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (c + q >= p.in.m) v[q] = 0.f;
+                }
+                uint16_t o[P][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint16_t cut[P];
+                    if (F16)
+                        cut[0] = f32_to_f16(v[q]);
+                    else
+                        Planes<T>::cut(v[q], cut);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) o[j][q] = cut[j];
                 }
                 if (c < p.vp)  // vp is a multiple of 64: whole fours
 #pragma unroll

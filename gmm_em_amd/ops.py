@@ -279,6 +279,10 @@ def _rows2(t, name):
     return dt, max(t.stride(0), t.shape[1])
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _row(t, n, name, dtype, device):
     """Address of a contiguous per-row vector, or None."""
     if t is None:
@@ -350,8 +354,8 @@ def logits_score(logits, targets=None, m: int = 0, scale: float = 1.0, ws=None) 
     ws, nb = _scratch(lib.gmm_logits_score_workspace_bytes(n, v, m), ws, dev)
     out = _score_outputs(n, m, targets, dev)
     with _On(dev) as stream:
-        _check(lib.gmm_logits_score(logits.data_ptr(), n, v, ldl, dt, t, m, scale, _ptr(out[0]),
-                                    _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(out[4]),
+        _check(lib.gmm_logits_score(logits.data_ptr(), n, v, ldl, dt, t, m, scale, _addr(out[0]),
+                                    _addr(out[1]), _addr(out[2]), _addr(out[3]), _addr(out[4]),
                                     ws.data_ptr(), nb, stream))
     return out
 
@@ -402,8 +406,8 @@ def head_score(hidden, weight, targets=None, m: int = 0, scale: float = 1.0, ws=
     out = _score_outputs(n, m, targets, dev)
     with _On(dev) as stream:
         _check(lib.gmm_head_score(hidden.data_ptr(), n, d, ldh, weight.data_ptr(), v, ldw, dt, t, m,
-                                  scale, _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]),
-                                  _ptr(out[4]), ws.data_ptr(), nb, stream))
+                                  scale, _addr(out[0]), _addr(out[1]), _addr(out[2]), _addr(out[3]),
+                                  _addr(out[4]), ws.data_ptr(), nb, stream))
     return out
 
 
@@ -463,7 +467,7 @@ def moe_layer(x, w_in, w_out, gate=None, m: int = 2, share_all: bool = False, id
         resp = torch.empty((n, m), dtype=torch.float32, device=dev)
     y = torch.empty((n, d), dtype=x.dtype, device=dev)
     with _On(dev) as stream:
-        _check(lib.gmm_moe_layer(x.data_ptr(), n, d, ldx, _ptr(gate), e, w_in.data_ptr(),
+        _check(lib.gmm_moe_layer(x.data_ptr(), n, d, ldx, _addr(gate), e, w_in.data_ptr(),
                                  w_out.data_ptr(), f, dt, m, int(share_all), idx.data_ptr(),
                                  resp.data_ptr(), y.data_ptr(), d, ws.data_ptr(), nb, stream))
     return y, idx, resp

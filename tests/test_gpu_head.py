@@ -179,6 +179,22 @@ def test_gradient_of_several_chunks(ops):
     _grad(ops, h, w, t, 1.0)
 
 
+def test_gradient_of_rows_with_nothing_left(ops):
+    # a row whose norm says that nothing is left has no gradient, whatever arrives
+    for dtype in (torch.float32, torch.bfloat16):
+        h, w, t = _inputs(6, 64, 90, dtype, 16)
+        t.clamp_(min=0)
+        s = ops.head_score(h, w, t)
+        g = torch.ones(6, device=DEV)
+        a = ops.head_score_backward(h[:5], w, t[:5].contiguous(), s.norm[:5], s.entropy[:5].contiguous(),
+                                    g[:5].contiguous(), g[:5].contiguous())
+        s.norm[5, 0], s.norm[5, 1], s.entropy[5] = -INF, 0.0, 0.0
+        dh, dw = ops.head_score_backward(h, w, t, s.norm, s.entropy, g, g)
+        assert dh[5].eq(0).all() and torch.equal(dh[:5], a[0])
+        # its row adds nothing to dw (the sums may be cut elsewhere: 2^-7 of the largest)
+        assert (dw.float() - a[1].float()).abs().max() <= 2.0 ** -7 * a[1].float().abs().max()
+
+
 def test_gradient_of_far_apart_magnitudes(ops):
     # rows whose gradients differ by 2^40, operands by 2^30: small rows of dh keep
     # their digits, and what dw loses is small beside its largest contributions
