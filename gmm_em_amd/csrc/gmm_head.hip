@@ -18,6 +18,10 @@
 // their own bounds (a row of small gradients keeps its digits); for dW, h's rows
 // are divided by the same, relative to the row of the largest bound. What then
 // lies below 2^-29 of the largest value loses digits, and below 2^-39 is dropped.
+// Measured, bf16, 8192 x 768 x 16384: scores 188 us (the product without epilogue 148, the
+// softmax of an accumulator is 7 operations and an exponential); gradient 690 us: dx 240,
+// dh 205 + 16 for its split, dW 212, ranges 13, turned operands 19. Bound by the
+// matrix products (1000 to 1400 TFLOP/s in them).
 //
 // Orientation: the tiles' rows are the axis that the outputs are contiguous in
 // (codes for logits, dims for the gradients), their columns the rows of h (or

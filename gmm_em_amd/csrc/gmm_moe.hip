@@ -12,10 +12,13 @@
 //   k_moe_in:    (expert, 16 features of a and of b): the contracted axis is
 //                split over the waves and joined in LDS; silu(a) b goes to the
 //                workspace, as two bf16 parts for bf16 data (16 bits of it).
-//   k_moe_out:   (expert, 16 features of y): as before; r_j times it goes to
-//                the workspace.
+//   k_moe_out:   (expert, 32 or 16 features of y): as before; r_j times it goes to
+//                the workspace. One or two rows: k_moe_out_row instead of both.
 //   k_moe_join:  y = the sum over j in order, rounded once.
 // Every sum is fp32 in a fixed order.
+// Measured, bf16: 64 rows of 2048, f = 1408, 4 of 64 experts (1.09 GB of weights):
+// k_moe_in 145 us (5.0 TB/s), k_moe_out 88 us (4.2 TB/s), route 9, join 5; one row of 768,
+// f = 2048, 2 of 64: 5 + 5 + 9 us, bound by latency and the three launches.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
