@@ -333,15 +333,14 @@ __device__ __forceinline__ float sum4(float v) {
 }
 
 // Statistics of each row over the tile's codes, and the targets' logits. Sums
-// are of 2^(c (x - max)) with c = scale log2 e: the exponential's argument in
-// one step from the accumulator; a is put back to base e at the end.
+// are of exp(l - max), the maximum subtracted before the exponential's factor log2 e.
 template <bool ONE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
     using G = Gemm<BM, BN, WM, WN, ONE>;
     __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
     __shared__ float sh[WM * BN * 3];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const float c2 = p.s.scale * 1.44269504088896341f;
+    const float scale = p.s.scale;
     gemm_walk<bf16x8, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
         const bool edge = m0 + BM > p.in.m;  // some of the tile's codes are not there
         const int code0 = m0 + G::row(0);
@@ -361,6 +360,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mx = fmaxf(mx, g.acc[x][y][q]);
             mx = max4(mx);
+            const float m = mx * scale;
             float s = 0.f, a = 0.f;
             if (edge || mx < -1e30f) {
                 // masked codes: 0 * -inf stays 0
@@ -368,28 +368,28 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
                 for (int x = 0; x < G::TM; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float d = fmaxf((g.acc[x][y][q] - mx) * c2, -1000.f);
-                        const float e = g.acc[x][y][q] != g.acc[x][y][q] ? NAN : __builtin_amdgcn_exp2f(d);
+                        const float l = g.acc[x][y][q];
+                        const float d = fmaxf(fmaf(l, scale, -m), -1000.f);
+                        const float e = l != l ? NAN : exp_neg(d);
                         s += e;
                         a = fmaf(e, d, a);
                     }
             } else {
-                const float mc = mx * c2;
 #pragma unroll
                 for (int x = 0; x < G::TM; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float d = fmaf(g.acc[x][y][q], c2, -mc);
-                        const float e = __builtin_amdgcn_exp2f(d);
+                        const float d = fmaf(g.acc[x][y][q], scale, -m);
+                        const float e = exp_neg(d);
                         s += e;
                         a = fmaf(e, d, a);
                     }
             }
             s = sum4(s);
-            a = sum4(a) * 0.693147180559945309f;
+            a = sum4(a);
             if (lane < 16) {
                 float* o = sh + (wave / WN * BN + G::col(y)) * 3;
-                o[0] = mx * p.s.scale;
+                o[0] = m;
                 o[1] = s;
                 o[2] = a;
             }

@@ -81,7 +81,6 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
     __shared__ float sst[NW][3], gmax[64], cv[SC_CAND], best_v;
     __shared__ int ci[SC_CAND], hot[NT], hots, count, best_i;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const float c2 = p.scale * 1.44269504088896341f;
     for (int64_t item = blockIdx.x; item < p.n * p.parts; item += gridDim.x) {
         const int64_t row = item / p.parts;
         const int part = (int)(item - row * p.parts);
@@ -106,29 +105,20 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
                 for (int k = 0; k < VE; ++k) xm = fmaxf(xm, Vec<T>::get(raw[u], k));
             cm = fmaxf(cm, xm * p.scale);
             st.raise(fmaxf(st.m, xm * p.scale));
-            if (__builtin_amdgcn_ballot_w64(fabsf(st.m) > 1e30f)) {
-                // far out: the scaled maximum times log2 e would pass the range
+            // l - m before the exponential's factor log2 e: the rounding of m log2 e would
+            // stay in every term
+            float s = 0.f, a = 0.f;
 #pragma unroll
-                for (int u = 0; u < SC_U; ++u)
+            for (int u = 0; u < SC_U; ++u)
 #pragma unroll
-                    for (int k = 0; k < VE; ++k)
-                        st.add(fmaf(Vec<T>::get(raw[u], k), p.scale, -st.m));
-            } else {
-                // 2^(c2 x - m log2 e): one step to the exponential's argument; a in base 2
-                const float mc = st.m * 1.44269504088896341f;
-                float s = 0.f, a = 0.f;
-#pragma unroll
-                for (int u = 0; u < SC_U; ++u)
-#pragma unroll
-                    for (int k = 0; k < VE; ++k) {
-                        const float d = fmaf(Vec<T>::get(raw[u], k), c2, -mc);
-                        const float e = __builtin_amdgcn_exp2f(d);
-                        s += e;
-                        a = fmaf(e, fmaxf(d, -1000.f), a);
-                    }
-                st.s += s;
-                st.a = fmaf(a, 0.693147180559945309f, st.a);
-            }
+                for (int k = 0; k < VE; ++k) {
+                    const float d = fmaf(Vec<T>::get(raw[u], k), p.scale, -st.m);
+                    const float e = exp_neg(d);
+                    s += e;
+                    a = fmaf(e, fmaxf(d, -1000.f), a);
+                }
+            st.s += s;
+            st.a += a;
         }
         st.wave_join();
         float gm = TOP ? group_max<G>(cm) : 0.f;

@@ -156,12 +156,6 @@ struct Stats {
         s *= e;
         m = mn;
     }
-    // adds one value: d = l - m
-    __device__ __forceinline__ void add(float d) {
-        const float e = exp_neg(d);
-        s += e;
-        a = fmaf(e, fmaxf(d, -1000.f), a);
-    }
     __device__ __forceinline__ void join(float m2, float s2, float a2) {
         const float mn = fmaxf(m, m2);
         Stats o{m2, s2, a2};
