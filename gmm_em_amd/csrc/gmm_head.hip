@@ -360,7 +360,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mx = fmaxf(mx, g.acc[x][y][q]);
             mx = max4(mx);
-            const float m = mx * scale;
+            const float m = fmaxf(scaled(mx, scale), -3.402823466e38f);  // finite where all are masked
             float s = 0.f, a = 0.f;
             if (edge || mx < -1e30f) {
                 // masked codes: 0 * -inf stays 0
@@ -368,18 +368,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
                 for (int x = 0; x < G::TM; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float l = g.acc[x][y][q];
-                        const float d = fmaxf(fmaf(l, scale, -m), -1000.f);
-                        const float e = l != l ? NAN : exp_neg(d);
+                        const float d = scaled(g.acc[x][y][q], scale) - m;
+                        const float e = exp_neg(d);
                         s += e;
-                        a = fmaf(e, d, a);
+                        a = fmaf(e, fmaxf(d, -1000.f), a);
                     }
             } else {
 #pragma unroll
                 for (int x = 0; x < G::TM; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float d = fmaf(g.acc[x][y][q], scale, -m);
+                        const float d = scaled(g.acc[x][y][q], scale) - m;
                         const float e = exp_neg(d);
                         s += e;
                         a = fmaf(e, d, a);
@@ -491,7 +490,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
                 float v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float lp = fmaf(g.acc[x][y][q], k.scale, -k.m) - k.logs;
+                    const float lp = (scaled(g.acc[x][y][q], k.scale) - k.m) - k.logs;
                     v[q] = exp_neg(lp) * fmaf(gh, lp, base);
                 }
                 if (c == t4) {

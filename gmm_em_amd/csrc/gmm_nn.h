@@ -55,7 +55,7 @@ __device__ __forceinline__ void score_out(const ScoreArgs& p, int64_t row, const
             if (t >= p.v)
                 lp = NAN;
             else if (t >= 0)
-                lp = none ? -INFINITY : fmaf(xt, p.scale, -st.m) - logs;
+                lp = none ? -INFINITY : (scaled(xt, p.scale) - st.m) - logs;
             p.logprob[row] = lp;
         }
     }
@@ -92,7 +92,7 @@ struct GradRow {
     int t;
     // dl of logit x at code i; a code of probability 0 has no entropy term
     __device__ __forceinline__ float at(float x, int i) const {
-        const float lp = fmaf(x, scale, -m) - logs;
+        const float lp = (scaled(x, scale) - m) - logs;
         const float p = exp_neg(lp);
         const float hot = i == t ? glp : 0.f;
         // lp is cut at -1000, where p is 0: 0 * lp stays 0 for a masked logit

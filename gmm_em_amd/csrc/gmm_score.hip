@@ -2,7 +2,7 @@
 // logits, and their gradient (gmm_logits_score, gmm_logits_score_backward,
 // declared in include/gmm_em.h).
 //
-// Scores: with l = scale * x, one pass over a row keeps, per thread, the maximum m,
+// Scores: with l = scale * x (rounded once, see scaled()), one pass over a row keeps, per thread, the maximum m,
 // s = sum exp(l - m) and a = sum exp(l - m)(l - m) (restated when m rises), so that
 //   log p_t = (l_t - m) - log s      entropy = log s - a / s
 // with nothing of the row stored; the threads' sums are joined over the lanes and
@@ -103,8 +103,9 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
             for (int u = 0; u < SC_U; ++u)
 #pragma unroll
                 for (int k = 0; k < VE; ++k) xm = fmaxf(xm, Vec<T>::get(raw[u], k));
-            cm = fmaxf(cm, xm * p.scale);
-            st.raise(fmaxf(st.m, xm * p.scale));
+            const float lm = scaled(xm, p.scale);
+            cm = fmaxf(cm, lm);
+            st.raise(fmaxf(st.m, lm));
             // l - m before the exponential's factor log2 e: the rounding of m log2 e would
             // stay in every term
             float s = 0.f, a = 0.f;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
             for (int u = 0; u < SC_U; ++u)
 #pragma unroll
                 for (int k = 0; k < VE; ++k) {
-                    const float d = fmaf(Vec<T>::get(raw[u], k), p.scale, -st.m);
+                    const float d = scaled(Vec<T>::get(raw[u], k), p.scale) - st.m;
                     const float e = exp_neg(d);
                     s += e;
                     a = fmaf(e, fmaxf(d, -1000.f), a);
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
                 const int u = j / VE, k = j % VE;
                 const int at = u / SC_U * CHUNK + (u % SC_U * NT + hot[h]) * VE + k;
                 if (at < x.len) {
-                    const float l = Vec<T>::one(x.x + at) * p.scale;
+                    const float l = scaled(Vec<T>::one(x.x + at), p.scale);
                     if (in(l)) {
                         const int to = atomicAdd(&count, 1);
                         if (to < SC_CAND) {
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
                         const Raw16 r = load_vec(x.x, (int64_t)at, (int64_t)x.len);
 #pragma unroll
                         for (int k = 0; k < VE; ++k) {
-                            const float l = Vec<T>::get(r, k) * p.scale;
+                            const float l = scaled(Vec<T>::get(r, k), p.scale);
                             const int i = (int)i0 + at + k;
                             if (top_before(lv, li, l, i) && top_before(l, i, bv, bi)) {
                                 bv = l;

@@ -15,6 +15,14 @@ __device__ __forceinline__ float exp_neg(float d) {
     return __builtin_amdgcn_exp2f(d * 1.44269504088896341f);
 }
 
+// A logit l = scale x, rounded to fp32 on its own. Every use of it sees this number: a
+// product fused into l - max would leave the maximum's own rounding in the difference,
+// 2^-24 of a logit of any size (the contraction is off for that).
+__device__ __forceinline__ float scaled(float x, float scale) {
+#pragma clang fp contract(off)
+    return x * scale;
+}
+
 // 16 bytes of a row at any element alignment (the hardware's global accesses
 // need no alignment, so rows of any stride take the same path).
 struct __attribute__((packed, aligned(2))) Raw16 {

@@ -229,7 +229,7 @@ int gmm_kmeans_fit(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t x_d
 
 /* Scores of given codes under a softmax over v codes, from its logits.
  * The log-likelihood of a learned softmax over components in place of a
- * mixture's: with l = scale * x for row x of the logits,
+ * mixture's: with l = scale * x (rounded to fp32) for row x of the logits,
  *   norm[2r], norm[2r+1] = max l, log sum exp(l - max l)
  *   logprob[r]  = l[t] - norm[2r] - norm[2r+1]        for t = targets[r]
  *   entropy[r]  = -sum p log p                         with p = softmax(l)
@@ -245,9 +245,9 @@ int gmm_kmeans_fit(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t x_d
  * exponentials of top_logprob is what gmm_ivf_build reads.
  * Masks: a logit of -inf (or one whose l is) has probability 0 and is never an
  * alternative: places left over hold -1 and -inf. A row with nothing left has
- * norm (-inf, 0), entropy 0 and logprob -inf. A row with a NaN or +inf has NaN
- * in logprob, entropy and norm; NaN is never an alternative. Rows whose
- * largest logit is the type's lowest finite value are ordinary rows.
+ * norm (-inf, 0), entropy 0 and logprob -inf. A row with a NaN or +inf (or one
+ * whose l is) has NaN in logprob, entropy and norm; NaN is never an alternative.
+ * Rows whose largest l is the lowest finite value are ordinary rows.
  * Sums are fp32 in a fixed order (bitwise reproducible). n may be 0; n <= 2^40,
  * v <= 2^30. The workspace (device, 256-byte aligned) has
  * gmm_logits_score_workspace_bytes(n, v, m) bytes (0: invalid sizes). */
