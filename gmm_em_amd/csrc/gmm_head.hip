@@ -52,14 +52,15 @@ constexpr int HEAD_MAX_SPLIT = 16;
 
 // ---- operand planes
 
-// Cuts a finite fp32 value into three bf16 values that add up to it exactly;
-// infinities and NaN go whole into the first.
+// Cuts a finite fp32 value into three bf16 values that add up to it exactly. An infinity
+// becomes NaN: its product with another operand's planes is NaN where one of those is 0,
+// and would be infinite elsewhere.
 __device__ __forceinline__ void cut3(float x, uint16_t* p) {
     const uint32_t u = __float_as_uint(x);
     p[0] = (uint16_t)(u >> 16);
     p[1] = p[2] = 0;
     if ((u & 0x7f800000u) == 0x7f800000u) {
-        if (u & 0x007fffffu) p[0] |= 0x40;  // NaN whose payload was cut off
+        p[0] = 0x7fc0;
         return;
     }
     const float r = x - __uint_as_float(u & 0xffff0000u);
@@ -362,26 +363,25 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_stats(HeadArgs p) {
             mx = max4(mx);
             const float m = fmaxf(scaled(mx, scale), -3.402823466e38f);  // finite where all are masked
             float s = 0.f, a = 0.f;
-            if (edge || mx < -1e30f) {
-                // masked codes: 0 * -inf stays 0
+#pragma unroll
+            for (int x = 0; x < G::TM; ++x)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float d = scaled(g.acc[x][y][q], scale) - m;
+                    const float e = exp_neg(d);
+                    s += e;
+                    a = fmaf(e, d, a);
+                }
+            if (a != a) {
+                // a masked code's 0 * -inf: once more with the difference cut (the cut in
+                // every sum costs 4 of 196 us at 8192 x 768 x 16384)
+                a = 0.f;
 #pragma unroll
                 for (int x = 0; x < G::TM; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float d = scaled(g.acc[x][y][q], scale) - m;
-                        const float e = exp_neg(d);
-                        s += e;
-                        a = fmaf(e, fmaxf(d, -1000.f), a);
-                    }
-            } else {
-#pragma unroll
-                for (int x = 0; x < G::TM; ++x)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float d = scaled(g.acc[x][y][q], scale) - m;
-                        const float e = exp_neg(d);
-                        s += e;
-                        a = fmaf(e, d, a);
+                        a = fmaf(exp_neg(d), fmaxf(d, -1000.f), a);
                     }
             }
             s = sum4(s);
@@ -476,8 +476,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
         for (int y = 0; y < G::TN; ++y) {
             const int r = n0 + G::col(y);
             if (r >= p.in.n) continue;
-            GradRow k = grad_row(grad_args(p), r);
-            if (k.m == INFINITY) k.m = 3.0e38f;  // nothing left in the row: p = 0, log p finite
+            const GradRow k = grad_row(grad_args(p), r);
             // the scale and the row's power of two go into the gradients
             const int up = F16 ? p.row_exp[r] : 0;
             const float gh = -ldexpf(k.scale * k.gh, up);
@@ -491,7 +490,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(HeadArgs p) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float lp = (scaled(g.acc[x][y][q], k.scale) - k.m) - k.logs;
-                    v[q] = exp_neg(lp) * fmaf(gh, lp, base);
+                    v[q] = exp_neg(lp) * fmaf(gh, fmaxf(lp, -1000.f), base);  // 0 for a masked code
                 }
                 if (c == t4) {
 #pragma unroll
