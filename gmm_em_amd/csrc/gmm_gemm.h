@@ -3,9 +3,9 @@
 // contracted axis contiguous.
 //
 // fp32 operands come as three bf16 planes whose sum is the fp32 value bit for
-// bit (24 bits in three cuts of 8): the product is then the sum of the six
-// plane products that reach 2^-24 of it, smallest first, in the same fp32
-// accumulators. bf16 and fp16 operands have one plane.
+// bit (24 bits in three parts of 8, rounded to nearest): the product is then the sum
+// of six plane products, smallest first, in the same fp32 accumulators; the three that are
+// left out are below 2^-24 of it together, of either sign. bf16 and fp16 operands have one plane.
 //
 // B may also lie with the contracted axis across (TB): panels of 64 of its rows,
 // [n / 64][k][64], as the product before wrote them with those rows contiguous. Its

@@ -52,21 +52,26 @@ constexpr int HEAD_MAX_SPLIT = 16;
 
 // ---- operand planes
 
-// Cuts a finite fp32 value into three bf16 values that add up to it exactly. An infinity
-// becomes NaN: its product with another operand's planes is NaN where one of those is 0,
-// and would be infinite elsewhere.
+// Cuts a finite fp32 value into three bf16 values that add up to it exactly (where the third
+// stays in bf16's range, above 2^-110). The upper two are rounded to nearest, so that the rest
+// is at most 2^-8 and 2^-17 of a value in [1, 2), of either sign: cut off instead, 2^-7 and
+// 2^-15 of the value's sign, and the products left out add up. An infinity becomes NaN: its
+// product with another operand's planes is NaN where one of those is 0, and would be infinite
+// elsewhere.
 __device__ __forceinline__ void cut3(float x, uint16_t* p) {
     const uint32_t u = __float_as_uint(x);
-    p[0] = (uint16_t)(u >> 16);
     p[1] = p[2] = 0;
     if ((u & 0x7f800000u) == 0x7f800000u) {
         p[0] = 0x7fc0;
         return;
     }
-    const float r = x - __uint_as_float(u & 0xffff0000u);
-    p[1] = (uint16_t)(__float_as_uint(r) >> 16);
-    const float r2 = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
-    p[2] = (uint16_t)(__float_as_uint(r2) >> 16);
+    uint32_t hi = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    if ((hi & 0x7f80u) == 0x7f80u) hi = u >> 16;  // would round to infinity
+    const float r = x - bf16_to_f32(hi);
+    const uint32_t mid = f32_to_bf16(r);
+    p[0] = (uint16_t)hi;
+    p[1] = (uint16_t)mid;
+    p[2] = (uint16_t)(__float_as_uint(r - bf16_to_f32(mid)) >> 16);
 }
 
 template <typename T>

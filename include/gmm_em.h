@@ -282,8 +282,8 @@ int gmm_logits_score_backward(const void* logits, int64_t n, int32_t v, int64_t 
  * added in fp32; fp32 operands are cut into three bf16 planes and multiplied to
  * 2^-24 of each product, so both types give fp32 logits. A logit of -inf (of a
  * bf16 weight of -inf, or of a product beyond fp32) is a masked code, one of +inf or
- * NaN gives its row NaN; an infinity in an fp32 operand counts as NaN. 1 <= d <= 2^20,
- * v <= 2^22 (GMM_E_UNSUPPORTED beyond). The workspace (device, 256-byte aligned)
+ * NaN gives its row NaN; an infinity in an fp32 operand counts as NaN, and a product of
+ * fp32 operands beyond 2^135 may. 1 <= d <= 2^20, v <= 2^22 (GMM_E_UNSUPPORTED beyond). The workspace (device, 256-byte aligned)
  * has gmm_head_score_workspace_bytes bytes (0: invalid or unsupported sizes); it
  * is bounded in n. Rows of bf16 that are 16-byte aligned with d a multiple of 64
  * are read in place, others are laid out in the workspace first. */
