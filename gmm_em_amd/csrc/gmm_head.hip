@@ -14,10 +14,11 @@
 // operands. For bf16 data dx is rounded to fp16, whose 11 bits leave an eighth
 // of bf16's error at the same rate; W and h (8 bits each) go into fp16
 // unrounded. fp16's short range is met by powers of two taken out of the sums
-// again: W and h are multiplied to a largest value in [2^14, 2^15), dx's rows by
-// their own bounds (a row of small gradients keeps its digits); for dW, h's rows
-// are divided by the same, relative to the row of the largest bound. What then
-// lies below 2^-29 of the largest value loses digits, and below 2^-39 is dropped.
+// again: dx's rows are multiplied by their own bounds' (a row of small gradients keeps its
+// digits); W by one for each dim, to a largest value in [2^14, 2^15); h by one for each dim
+// too, after its rows are divided by what dx's were multiplied by (so that rows count by
+// what they can add to dW, and those without a gradient not at all). What then lies
+// below 2^-29 of the largest of its dim or row loses digits, and below 2^-39 is dropped.
 // Measured, bf16, 8192 x 768 x 16384: scores 188 us (the product without epilogue 148, the
 // softmax of an accumulator is 7 operations and an exponential); gradient 690 us: dx 240,
 // dh 205 + 16 for its split, dW 212, ranges 13, turned operands 19. Bound by the
@@ -137,8 +138,6 @@ __global__ __launch_bounds__(256) void k_planes(LayoutPair p, int kp) {
 
 // ---- fp16's powers of two
 
-constexpr int RANGE_BLOCKS = 1024;
-
 // The exponent e for which a value with these magnitude bits, times 2^e, lies in
 // [2^14, 2^15); 0 for zero and for what is not finite. 2^e may lie outside fp32's
 // range: it is applied with ldexpf.
@@ -149,88 +148,109 @@ __device__ __forceinline__ int range_of(uint32_t bits) {
     return 15 - e;
 }
 
-// The exponent of the largest of the blocks' magnitudes (every lane of a wave).
-__device__ __forceinline__ int range_exp(const uint32_t* part) {
-    const int lane = threadIdx.x & 63;
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < RANGE_BLOCKS / 64; ++k) {
-        const uint32_t o = part[k * 64 + lane];
-        m = m > o ? m : o;
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)m, off);
-        m = m > o ? m : o;
-    }
-    return range_of(m);
-}
+constexpr int ROW_NONE = -(1 << 20);    // power of two of a row whose dx is 0
+constexpr int KEY_NONE = -(1 << 30);    // of a dim without a finite value other than 0
+constexpr int RANGE_COLS = 2048;        // dims of a workgroup: 8 per thread
 
-// Largest finite magnitude of each block's rows of bf16 values, by magnitude bits.
-__device__ __forceinline__ uint32_t rows_range(const uint16_t* x, int64_t rows, int d, int64_t ld) {
-    uint32_t m = 0;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    constexpr int U = 4;  // rows in flight
-    for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < rows; r += U * RANGE_BLOCKS * 4)
-        for (int c = lane * 8; c < d; c += 512) {
-            Raw16 v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t q = r + u * RANGE_BLOCKS * 4;
-                v[u] = load_zero(x + (q < rows ? q : r) * ld, c, (int64_t)d);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t b = __float_as_uint(Vec<uint16_t>::get(v[u], k)) & 0x7fffffffu;
-                    if (b < 0x7f800000u && b > m) m = b;
-                }
-        }
-    return m;
+// Row parts that the dims' ranges are made in: up to 512 workgroups for each of W and h, with 8
+// rows or more of the longer of them.
+inline int range_parts(int64_t n, int32_t v, int dp) {
+    const int chunks = (dp + RANGE_COLS - 1) / RANGE_COLS;
+    const int64_t most = chunks < 512 ? 512 / chunks : 1, rows = (n > v ? n : v) / 8;
+    return (int)(rows < 1 ? 1 : rows < most ? rows : most);
 }
 
 struct RangeArgs {
     const uint16_t *h, *w;
     int64_t n, ldh, ldw;
-    int32_t d, v;
+    int32_t d, dp, v;
     ScoreGradArgs g;
-    uint32_t* part;    // [3][RANGE_BLOCKS]: W, h, dx
+    int32_t* part;     // [parts][2][dp]: W's and h's largest exponents
     int32_t* row_exp;  // [n]: dx's power of two for each row
 };
 
 // What dx's row can reach: |g_lp| + |g_H| max p |log p + H|, with p |log p| < 0.37.
 __device__ __forceinline__ float grad_bound(const GradRow& g) {
     const float b = g.scale * (fabsf(g.glp) + fabsf(g.gh) * (0.375f + fabsf(g.h)));
-    return b < 3.0e38f ? b : 0.f;  // not finite: no power of two helps
+    return fminf(b, 3.402823466e38f);  // NaN: any power of two leaves it so
 }
 
-__global__ __launch_bounds__(256) void k_head_range(RangeArgs p) {
-    __shared__ uint32_t sh[4][3];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t m[3];
-    m[0] = rows_range(p.w, p.v, p.d, p.ldw);
-    m[1] = rows_range(p.h, p.n, p.d, p.ldh);
-    m[2] = 0;
-    for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < p.n; r += RANGE_BLOCKS * 256) {
-        const uint32_t b = __float_as_uint(grad_bound(grad_row(p.g, r)));
-        p.row_exp[r] = range_of(b);
-        m[2] = m[2] > b ? m[2] : b;
-    }
+// m[k]: the largest e with a value of the 8 dims below 2^e (row_exp: times 2^-row_exp[r]) over
+// rows r, r + step, ... < end.
+template <bool H>
+__device__ __forceinline__ void dims_range(const uint16_t* x, int64_t ld, int c, int d, int64_t r,
+                                           int64_t end, int step, const int32_t* row_exp, int* m) {
+    constexpr int U = 4;  // rows in flight
+    for (; r < end; r += U * step) {
+        Raw16 v[U];
+        int e[U];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const uint32_t o = (uint32_t)__shfl_xor((int)m[k], off);
-            m[k] = m[k] > o ? m[k] : o;
+        for (int u = 0; u < U; ++u) {
+            const int64_t q = r + u * step < end ? r + u * step : r;
+            v[u] = load_zero(x + q * ld, c, (int64_t)d);
+            e[u] = H ? row_exp[q] : 0;
         }
-        if (lane == 0) sh[wave][k] = m[k];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (H && e[u] == ROW_NONE) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int b = (int)((v[u].w[k >> 1] >> (k & 1 ? 16 : 0)) & 0x7fffu);
+                const int key = max(b >> 7, 1) - 126 - e[u];
+                if (b != 0 && b < 0x7f80) m[k] = max(m[k], key);
+            }
+        }
     }
+}
+
+// The powers of two of dx's rows, and the largest exponents of W's and h's dims over a part
+// of their rows. Reads W and h once: 38 MB (8192 x 768 x 16384) in RANGE_US us.
+__global__ __launch_bounds__(256) void k_head_range(RangeArgs p) {
+    __shared__ __align__(16) int sh[256][8];
+    const int tid = threadIdx.x;
+    const int c0 = blockIdx.y * RANGE_COLS;
+    const int left = (p.dp - c0) / 8, cols = left < 256 ? left : 256;  // vectors of a row
+    const int per = 256 / cols, row = tid / cols, c = c0 + (tid - row * cols) * 8;
+    const int64_t parts = gridDim.x, b = blockIdx.x;
+    int m[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m[k] = KEY_NONE;
+    if (blockIdx.z == 0) {
+        if (row < per)
+            dims_range<false>(p.w, p.ldw, c, p.d, p.v * b / parts + row, p.v * (b + 1) / parts, per, nullptr, m);
+    } else {
+        const int64_t r0 = p.n * b / parts, r1 = p.n * (b + 1) / parts;
+        for (int64_t r = r0 + tid; r < r1; r += 256) {
+            const float most = grad_bound(grad_row(p.g, r));
+            p.row_exp[r] = most == 0.f ? ROW_NONE : range_of(__float_as_uint(most));
+        }
+        __syncthreads();
+        if (row < per) dims_range<true>(p.h, p.ldh, c, p.d, r0 + row, r1, per, p.row_exp, m);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sh[tid][k] = m[k];
     __syncthreads();
-    if (threadIdx.x < 3) {
-        uint32_t o = 0;
-        for (int w = 0; w < 4; ++w) o = o > sh[w][threadIdx.x] ? o : sh[w][threadIdx.x];
-        p.part[threadIdx.x * RANGE_BLOCKS + blockIdx.x] = o;
+    for (int j = tid; j < cols * 8; j += 256) {
+        int o = KEY_NONE;
+        for (int q = 0; q < per; ++q) o = max(o, sh[q * cols + j / 8][j % 8]);
+        p.part[(b * 2 + blockIdx.z) * p.dp + c0 + j] = o;
+    }
+}
+
+// The powers of two of W's dims (blockIdx.y 0) and of h's: 15 - the largest exponent.
+__global__ __launch_bounds__(1024) void k_head_dims(const int32_t* part, int parts, int dp, int32_t* out) {
+    __shared__ int sh[16][64];
+    const int tid = threadIdx.x, c = blockIdx.x * 64 + (tid & 63);
+    int m = KEY_NONE;
+#pragma unroll 8
+    for (int b = tid >> 6; b < parts; b += 16)
+        m = max(m, part[((int64_t)b * 2 + blockIdx.y) * dp + c]);
+    sh[tid >> 6][tid & 63] = m;
+    __syncthreads();
+    if (tid < 64) {
+#pragma unroll
+        for (int q = 1; q < 16; ++q) m = max(m, sh[q][tid]);
+        out[(int64_t)blockIdx.y * dp + c] = m == KEY_NONE ? 0 : 15 - m;
     }
 }
 
@@ -241,11 +261,10 @@ __device__ __forceinline__ uint16_t f32_to_f16(float f) {
 // ---- transposed operands
 
 // The planes of x^T: d rows of x's rows, padded with 0 to a multiple of 64: 64 x 64 tiles
-// turned through LDS. bf16 values become fp16 times the power of two of `range`
-// (W's and h's); h's rows (row_exp) also times 2^(e - row_exp), e the exponent of
-// dx's largest bound: what dx's rows were multiplied by, relative to that row.
+// turned through LDS. bf16 values become fp16 times the power of two of their dim
+// (dim_exp: W's dims, then h's), h's rows divided by dx's (row_exp).
 template <typename T>
-__global__ __launch_bounds__(256) void k_planes_t(LayoutPair p, const uint32_t* range,
+__global__ __launch_bounds__(256) void k_planes_t(LayoutPair p, const int32_t* dim_exp,
                                                   const int32_t* row_exp) {
     constexpr int P = Planes<T>::P;
     constexpr bool F16 = std::is_same<T, uint16_t>::value;
@@ -255,8 +274,7 @@ __global__ __launch_bounds__(256) void k_planes_t(LayoutPair p, const uint32_t* 
     const int ct = (p.d + 63) / 64;
     const int64_t rp = (o.rows + 63) / 64 * 64, total = ct * (rp / 64), plane = p.d * rp;
     const int tid = threadIdx.x;
-    const int up = F16 ? range_exp(range + blockIdx.y * RANGE_BLOCKS) : 0;
-    const int e = F16 && blockIdx.y == 1 ? range_exp(range + 2 * RANGE_BLOCKS) : 0;
+    const int32_t* exps = dim_exp + (int64_t)blockIdx.y * (ct * 64);
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int64_t r0 = b / ct * 64;
         const int c0 = (int)(b % ct) * 64;
@@ -271,17 +289,18 @@ __global__ __launch_bounds__(256) void k_planes_t(LayoutPair p, const uint32_t* 
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int r = (k * 256 + tid) / PER_ROW, c = (k * 256 + tid) % PER_ROW * VE;
-            int by = up;
-            // a row without gradient has exponent 0: its dx is 0
-            if (F16 && blockIdx.y == 1 && r0 + r < o.rows) by += min(e - row_exp[r0 + r], 0);
+            const int down = F16 && blockIdx.y == 1 && r0 + r < o.rows ? row_exp[r0 + r] : 0;
 #pragma unroll
             for (int u = 0; u < VE; ++u) {
                 uint16_t cut[P];
-                const float y = Vec<T>::get(v[k], u);
-                if (F16)
-                    cut[0] = f32_to_f16(ldexpf(y, by));
-                else
+                float y = Vec<T>::get(v[k], u);
+                if constexpr (F16) {
+                    // a row without gradient adds 0, whatever finite values it has
+                    if (down == ROW_NONE && fabsf(y) < INFINITY) y = 0.f;
+                    cut[0] = f32_to_f16(ldexpf(y, exps[c0 + c + u] - down));
+                } else {
                     Planes<T>::cut(y, cut);
+                }
 #pragma unroll
                 for (int q = 0; q < P; ++q) tile[q][c + u][r] = cut[q];
             }
@@ -539,20 +558,26 @@ struct GradOut {
     void* out;
     int64_t ldo;
     int32_t fours;     // wide stores: see grad_store
-    // fp16 operands: the powers of two that they were multiplied by, b's for
-    // each row where row_exp is given
-    const uint32_t *range_a, *range_b;
-    const int32_t* row_exp;
+    // fp16 operands: the powers of two of the dims and, where they are given, of the rows
+    const int32_t *dim_exp, *row_exp;
 };
 
-// Four neighbouring values of row r from dim c on, summed over the split already.
+// The powers of two of four neighbouring dims, c a multiple of 4 (dim_exp is padded to 64).
+template <typename T>
+__device__ __forceinline__ int4 grad_dims(const GradOut& p, int c) {
+    if (std::is_same<T, uint16_t>::value) return *(const int4*)(p.dim_exp + c);
+    return int4{0, 0, 0, 0};
+}
+
+// Four neighbouring values of row r from dim c on (dim: grad_dims), summed over the split already.
 // p.fours: every row starts at a multiple of four values, m is one too.
 template <typename T>
-__device__ __forceinline__ void grad_store(const GradOut& p, int64_t r, int c, f32x4 v, int back) {
+__device__ __forceinline__ void grad_store(const GradOut& p, int64_t r, int c, f32x4 v, int4 dim) {
     if (std::is_same<T, uint16_t>::value) {
-        const int e = p.row_exp ? back - p.row_exp[r] : back;
+        const int row = p.row_exp ? p.row_exp[r] : 0;
+        const int by[4] = {dim.x + row, dim.y + row, dim.z + row, dim.w + row};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = ldexpf(v[q], e);
+        for (int q = 0; q < 4; ++q) v[q] = ldexpf(v[q], -by[q]);
     }
     const int64_t at = r * p.in.m + c;
     if (p.fours) {
@@ -580,13 +605,6 @@ __device__ __forceinline__ void grad_store(const GradOut& p, int64_t r, int c, f
     }
 }
 
-// the power of two to take out of a's and b's sums
-template <typename T>
-__device__ __forceinline__ int grad_back(const GradOut& p) {
-    if (!std::is_same<T, uint16_t>::value) return 0;
-    return -range_exp(p.range_a) - (p.row_exp ? 0 : range_exp(p.range_b));
-}
-
 template <typename T, bool TB, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
     using G = Gemm<BM, BN, WM, WN, std::is_same<T, uint16_t>::value, TB>;
@@ -600,8 +618,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
     G g;
     g.begin(p.in, m0, n0, (int)((int64_t)steps * z / p.split),
             (int)((int64_t)steps * (z + 1) / p.split), l0, l1);
-    const int back = p.split > 1 ? 0 : grad_back<T>(p);
     g.template finish<std::conditional_t<F16, f16x8, bf16x8>>(p.in, m0, n0, l0, l1);
+    int4 dim[G::TM];
+#pragma unroll
+    for (int x = 0; x < G::TM; ++x) {
+        const int c = m0 + G::row(x);
+        dim[x] = p.split > 1 || c >= p.in.m ? int4{0, 0, 0, 0} : grad_dims<T>(p, c);
+    }
 #pragma unroll
     for (int y = 0; y < G::TN; ++y) {
         const int r = n0 + G::col(y);
@@ -620,7 +643,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
                         if (c + q < p.in.m) o[q] = g.acc[x][y][q];
                 }
             } else {
-                grad_store<T>(p, r, c, g.acc[x][y], back);
+                grad_store<T>(p, r, c, g.acc[x][y], dim[x]);
             }
         }
     }
@@ -629,7 +652,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_grad(GradOut p) {
 // The sum over a split product's parts, in order.
 template <typename T>
 __global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
-    const int back = grad_back<T>(p);
     const int per = (p.in.m + 3) / 4;
     const int64_t total = (int64_t)p.in.n * per;
     for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total;
@@ -648,7 +670,7 @@ __global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
                     if (c + q < p.in.m) v[q] += o[q];
             }
         }
-        grad_store<T>(p, r, c, v, back);
+        grad_store<T>(p, r, c, v, grad_dims<T>(p, c));
     }
 }
 
@@ -726,7 +748,7 @@ struct HeadPlan {
     int planes, pairs, dp, vp, np;
     int64_t chunk;      // rows per chunk, a multiple of 256
     bool pack_h, pack_w;
-    size_t o_w, o_h, o_x, o_part, o_wt, o_ht, o_dx, o_sum, o_split, o_score, o_range, o_exp, bytes;
+    size_t o_w, o_h, o_x, o_part, o_wt, o_ht, o_dx, o_sum, o_split, o_score, o_range, o_dims, o_exp, bytes;
 };
 
 static bool direct(const void* p, int32_t d, int64_t ld, int dtype) {
@@ -782,7 +804,8 @@ static HeadPlan head_plan(int64_t n, int32_t d, int32_t v, int dtype, int32_t m,
     const size_t most_out = (size_t)(q.chunk > v ? q.chunk : v) * d * 4 * HEAD_MAX_SPLIT;
     q.o_split = take(grad ? (most_out < HEAD_SPLIT_BYTES ? most_out : HEAD_SPLIT_BYTES) : 0);
     const bool f16 = grad && dtype == GMM_BF16;
-    q.o_range = take(f16 ? 3 * RANGE_BLOCKS * sizeof(uint32_t) : 0);
+    q.o_range = take(f16 ? (size_t)range_parts(n, v, q.dp) * 2 * q.dp * sizeof(int32_t) : 0);
+    q.o_dims = take(f16 ? (size_t)2 * q.dp * sizeof(int32_t) : 0);
     q.o_exp = take(f16 ? (size_t)n * sizeof(int32_t) : 0);
     q.bytes = off < 256 ? 256 : off;
     return q;
@@ -801,12 +824,12 @@ static void planes(const LayoutPair& p, int kp, hipStream_t st) {
     if (grid) hipLaunchKernelGGL((k_planes<T>), dim3(grid, 2), dim3(256), 0, st, p, kp);
 }
 template <typename T>
-static void planes_t(const LayoutPair& p, const uint32_t* range, const int32_t* row_exp,
+static void planes_t(const LayoutPair& p, const int32_t* dim_exp, const int32_t* row_exp,
                      hipStream_t st) {
     const int64_t rows = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
     const int64_t work = (int64_t)((p.d + 63) / 64) * ((rows + 63) / 64);
     const unsigned grid = (unsigned)(work < 65536 ? work : 65536);
-    if (grid) hipLaunchKernelGGL((k_planes_t<T>), dim3(grid, 2), dim3(256), 0, st, p, range,
+    if (grid) hipLaunchKernelGGL((k_planes_t<T>), dim3(grid, 2), dim3(256), 0, st, p, dim_exp,
                                  row_exp);
 }
 
@@ -937,7 +960,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
                             void* dw, int64_t lddw, char* ws, hipStream_t st) {
     uint16_t* wt = (uint16_t*)(ws + q.o_wt);
     uint16_t* ht = (uint16_t*)(ws + q.o_ht);
-    uint32_t* range = (uint32_t*)(ws + q.o_range);  // W, h, dx
+    int32_t* dim_exp = (int32_t*)(ws + q.o_dims);  // W's, h's
     int32_t* row_exp = (int32_t*)(ws + q.o_exp);
     float* part = (float*)(ws + q.o_split);
     if (std::is_same<T, uint16_t>::value) {
@@ -948,11 +971,15 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         r.ldh = x.ldh;
         r.ldw = x.ldw;
         r.d = x.d;
+        r.dp = q.dp;
         r.v = x.v;
         r.g = grad_args(a);
-        r.part = range;
+        r.part = (int32_t*)(ws + q.o_range);
         r.row_exp = row_exp;
-        hipLaunchKernelGGL(k_head_range, dim3(RANGE_BLOCKS), dim3(256), 0, st, r);
+        const int parts = range_parts(x.n, x.v, q.dp);
+        hipLaunchKernelGGL(k_head_range, dim3(parts, (q.dp + RANGE_COLS - 1) / RANGE_COLS, 2), dim3(256),
+                           0, st, r);
+        hipLaunchKernelGGL(k_head_dims, dim3(q.dp / 64, 2), dim3(1024), 0, st, r.part, parts, q.dp, dim_exp);
     }
     a.dx = (uint16_t*)(ws + q.o_dx);
     a.vp = q.vp;
@@ -977,14 +1004,14 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         turned.d = x.d;
         if (dh && r0 == 0) turned.o[0] = Layout{x.w, x.v, x.ldw, wt};
         if (dw) turned.o[1] = Layout{(const T*)x.h + r0 * x.ldh, rows, x.ldh, ht};
-        planes_t<T>(turned, range, a.row_exp, st);
+        planes_t<T>(turned, dim_exp, a.row_exp, st);
         if (dh) {
             GradOut o{};
             o.in = GemmIn{wt, a.dx, GK, GK, (int64_t)x.d * GK, rows * GK, (int64_t)x.d * q.vp, a.plane_dx,
                           x.d, (int32_t)rows, q.vp, q.pairs};
             o.out = (T*)dh + r0 * lddh;
             o.ldo = lddh;
-            o.range_a = range;
+            o.dim_exp = dim_exp;
             o.row_exp = row_exp + r0;
             launch_grad<T, false>(o, part, st);
         }
@@ -999,8 +1026,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
             o.sum = r0 + q.chunk < x.n ? sum : nullptr;
             o.out = dw;
             o.ldo = lddw;
-            o.range_a = range + RANGE_BLOCKS;
-            o.range_b = range + 2 * RANGE_BLOCKS;
+            o.dim_exp = dim_exp + q.dp;
             launch_grad<T, true>(o, part, st);
         }
     }

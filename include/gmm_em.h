@@ -299,9 +299,14 @@ int gmm_head_score(const void* hidden, int64_t n, int32_t d, int64_t ldh, const 
  * in the operands' type, rounded once from fp32 sums (leading dimensions lddh,
  * lddw >= d). Either may be NULL (not computed), not both. They must not overlap
  * hidden or weight. dx is computed a chunk of rows at a time into the
- * workspace: exactly for fp32 operands; for bf16 in fp16, scaled by a power of two for
- * each row (d_hidden) or for all rows (d_weight), with 11 significant bits
- * down to 2^-29 of what a row's (all rows') dx can reach and nothing below 2^-39.
+ * workspace: exactly for fp32 operands. For bf16 the two products have fp16 operands,
+ * each multiplied by a power of two that is taken out of the sums again: dx by one for
+ * each row, W by one for each dim, and for d_weight h by one for each dim after its rows
+ * are divided by dx's. They have 11 significant bits (all of W's and h's 8) down to
+ * 2^-29 of the most that a row's dx can reach, of a dim's largest |W| and of a dim's
+ * largest |h| times what its row's dx can reach, and nothing below 2^-39 of it. Rows
+ * without a gradient add 0 whatever finite values they hold; an infinity or NaN in W or
+ * h gives NaN in its dim of d_hidden or d_weight.
  * n = 0 sets d_weight to 0. Sizes as for gmm_head_score; the workspace grows with n by 4
  * bytes a row for bf16. */
 size_t gmm_head_score_backward_workspace_bytes(int64_t n, int32_t d, int32_t v, int32_t dtype);
