@@ -109,9 +109,10 @@ __global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
         for (int j = 0; j < RT_U; ++j) {
             const float t = wave_sum(s[j]);
             if (lane == 0 && e0 + j < p.e) {
+                // -inf and NaN have the lowest number's key and rank after it by their ids
                 z[e0 + j] = t;
-                key[e0 + j] = t > -3.402823466e38f ? t : -3.402823466e38f;  // NaN ranks last
-                id[e0 + j] = e0 + j;
+                key[e0 + j] = t > -3.402823466e38f ? t : -3.402823466e38f;
+                id[e0 + j] = e0 + j + (t != t ? 2 : t == -INFINITY ? 1 : 0) * MOE_MAX_EXPERTS;
             }
         }
     }
@@ -123,17 +124,20 @@ __global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
             int ci[C];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                ci[c] = c * 64 + lane;
-                cv[c] = ci[c] < p.e ? key[ci[c]] : -INFINITY;
+                const int i = c * 64 + lane;
+                ci[c] = i < p.e ? id[i] : i;
+                cv[c] = i < p.e ? key[i] : -INFINITY;
             }
             const TopList t = top_pick<C>(cv, ci, p.m, lane);
             if (lane < p.m) {
                 ov[lane] = t.v;
-                oi[lane] = t.i;
+                oi[lane] = t.i % MOE_MAX_EXPERTS;
             }
         }
     } else {
         top_rank(key, id, p.e, p.m, ov, oi, tid, RT_NT);
+        __syncthreads();
+        if (tid < p.m) oi[tid] %= MOE_MAX_EXPERTS;
     }
     __syncthreads();
     const float top = ov[0];
