@@ -279,6 +279,13 @@ def _rows2(t, name):
     return dt, max(t.stride(0), t.shape[1])
 
 
+def _int32(*sizes):
+    """Refuses sizes that the int32 arguments of the C ABI would cut to their low bits."""
+    for s in sizes:
+        if not 0 <= s <= 0x7fffffff:
+            raise GmmError(GMM_E_INVALID)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -349,6 +356,7 @@ def logits_score(logits, targets=None, m: int = 0, scale: float = 1.0, ws=None) 
     """
     dt, ldl = _rows2(logits, "logits")
     n, v = logits.shape
+    _int32(v, m)
     dev = logits.device
     t = _row(targets, n, "targets", torch.int32, dev)
     ws, nb = _scratch(lib.gmm_logits_score_workspace_bytes(n, v, m), ws, dev)
@@ -369,6 +377,7 @@ def logits_score_backward(logits, targets, norm, entropy=None, g_logprob=None, g
     """
     dt, ldl = _rows2(logits, "logits")
     n, v = logits.shape
+    _int32(v)
     dev = logits.device
     _norm(norm, n, dev)
     if out is None:
@@ -391,6 +400,7 @@ def _head(hidden, weight):
     dt2, ldw = _rows2(weight, "weight")
     if dt != dt2 or hidden.shape[1] != weight.shape[1] or hidden.device != weight.device:
         raise ValueError("hidden (N, D) and weight (V, D) must agree in D, type and device")
+    _int32(*weight.shape)
     return dt, ldh, ldw, hidden.shape[0], hidden.shape[1], weight.shape[0], hidden.device
 
 
@@ -401,6 +411,7 @@ def head_score(hidden, weight, targets=None, m: int = 0, scale: float = 1.0, ws=
     in ``include/gmm_em.h``.
     """
     dt, ldh, ldw, n, d, v, dev = _head(hidden, weight)
+    _int32(m)
     t = _row(targets, n, "targets", torch.int32, dev)
     ws, nb = _scratch(lib.gmm_head_score_workspace_bytes(n, d, v, dt, m), ws, dev)
     out = _score_outputs(n, m, targets, dev)
@@ -461,6 +472,7 @@ def moe_layer(x, w_in, w_out, gate=None, m: int = 2, share_all: bool = False, id
         for t, nm, ty in ((idx, "idx", torch.int32), (resp, "resp", torch.float32)):
             if t.dtype != ty or tuple(t.shape) != (n, m) or not t.is_contiguous() or t.device != dev:
                 raise ValueError(f"{nm} must be a contiguous (N, m) tensor of {ty} on x's device")
+    _int32(d, f, e, m)
     ws, nb = _scratch(lib.gmm_moe_layer_workspace_bytes(n, d, f, e, dt, m), ws, dev)
     if gate is not None:
         idx = torch.empty((n, m), dtype=torch.int32, device=dev)
