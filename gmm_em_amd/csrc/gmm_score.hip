@@ -308,14 +308,15 @@ __global__ __launch_bounds__(SG_NT) void k_score_grad(ScoreGradArgs p) {
 ScorePlan score_plan(int64_t n, int32_t v, int32_t m) {
     ScorePlan q;
     q.parts = 1;
-    // few long rows: parts of at least 32768 values until 256 blocks run
-    if (n < 128) {
-        const int64_t most = v / 32768;
-        int64_t want = n > 0 ? 256 / n : 1;
-        if (want > most) want = most;
-        if (want > SC_MAX_PARTS) want = SC_MAX_PARTS;
-        if (want > 1) q.parts = (int)want;
-    }
+    // few long rows: parts of at least 32768 values until 256 workgroups run, where that makes
+    // three or more. fp32, m = 4, cut against whole rows: 1 x 131072 12.1 us (14.7), 1 x 524288
+    // 12.3 (43.3), 64 x 262144 20.7 (26.5), 80 x 180000 18.7 (20.8); two parts lose to the join's
+    // launch: 1 x 80000 13.4 us (11.0), 100 x 131072 18.0 (16.2), 127 x 262144 29.9 (27.6).
+    int64_t want = n > 0 ? 256 / n : 1;
+    const int64_t most = v / 32768;
+    if (want > most) want = most;
+    if (want > SC_MAX_PARTS) want = SC_MAX_PARTS;
+    if (want > 2) q.parts = (int)want;
     q.part_len = ((v + q.parts - 1) / q.parts + 7) / 8 * 8;
     q.parts = (v + q.part_len - 1) / q.part_len;
     if (q.parts < 1) q.parts = 1;
