@@ -341,12 +341,13 @@ static void launch_score_nt(const ScoreArgs& a, hipStream_t st) {
 }
 
 // Threads per (row, part): one wave where it has at most 8 chunks to go through (8192
-// rows of 5000 bf16 values, m = 8: 37 us, with 256 threads 47), else 256; as many as
-// there can be where there are few rows for the chip.
+// rows of 5000 bf16 values, m = 8: 37 us, with 256 threads 47), else 256; 1024 while every
+// workgroup has a CU of its own (fp32, m = 4: 256 rows of 40000 11.7 us, with 256 threads 13.8;
+// 257 rows 18.5 against 14.1).
 template <typename T>
 static void launch_score_t(const ScoreArgs& a, hipStream_t st) {
     constexpr int64_t PER = SC_U * Vec<T>::VE;
-    const bool few = a.n * a.parts < 512;
+    const bool few = a.n * a.parts <= 256;
     if (a.part_len <= 64 * PER || (!few && a.part_len <= 8 * 64 * PER))
         launch_score_nt<T, 64>(a, st);
     else if (!few)
