@@ -490,9 +490,13 @@ static hipError_t launch_moe(const MoeArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((k_moe_out_row<T>), dim3(dt, a.n), dim3(64 * MOE_ROW_W), 0, st, a);
         return hipGetLastError();
     }
-    // enough tiles: 32 features share the loads of act (64 rows of 2048 x 1408, 64 experts:
-    // the layer in 249 us, with 64 features 255); few: 16 waves share a tile
-    if ((int64_t)dt * a.slots >= 4096)
+    // bf16, the layer with 32 features sharing the loads of act / 16 features in 4 waves / in 16:
+    // 8192 tiles of 16 (64 rows of 2048 x 1408, 4 of 64 experts) 248 / 271 / 344 us, 4096 (8
+    // rows) 122 / 132 / 156, 1024 (64 rows of 2048 x 1408, 4 of 8) 61 / 73 / 83, 1024 (64 rows of
+    // 1024 x 1024, 2 of 16) 35.2 / 34.7 / 43.3; 768 (64 rows of 768 x 1024, 2 of 16) 32.6 / 30.8 /
+    // 36.8, 512 (12 rows of 1024 x 2048, 2 of 8) 36.9 / 35.8 / 36.1; 256 (300 rows of 512 x 512, 2 of
+    // 8) 37.8 / 39.6 / 34.6
+    if ((int64_t)dt * a.slots >= 1024)
         hipLaunchKernelGGL((k_moe_out<T, 2, 4>), dim3((dt + 1) / 2, a.slots), dim3(256), 0, st, a);
     else if ((int64_t)dt * a.slots >= 512)
         hipLaunchKernelGGL((k_moe_out<T, 1, 4>), dim3(dt, a.slots), dim3(256), 0, st, a);
