@@ -38,8 +38,6 @@ constexpr int32_t MOE_MAX_DIM = 1 << 20;
 constexpr int MOE_FEW_ROWS = 2;          // rows whose second product is made row by row
 constexpr int MOE_WIN = 2048;            // pairs looked through at a time
 
-// Where the picks of one call fit a wave (pairs <= 64), every wave finds its
-// workgroup's expert and rows from one load and a ballot.
 struct MoeArgs {
     const void *x, *gate, *w_in, *w_out;
     int64_t ldx, ldy;
@@ -159,7 +157,8 @@ __global__ __launch_bounds__(RT_NT) void k_moe_route(MoeArgs p) {
 }
 
 // The pairs of window [w0, w0 + MOE_WIN) that picked expert e, in order.
-// Returns their count; all W waves call it.
+// Returns their count; all W waves call it. Where the picks of one call fit a wave
+// (pairs <= 64), every wave finds them from one load and a ballot, here and in moe_expert.
 template <int W>
 __device__ __forceinline__ int moe_list(const MoeArgs& p, int e, int w0, int* list, int* cnt) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -461,16 +460,17 @@ struct MoePlan {
     size_t o_act, o_part, bytes;
 };
 
-static bool moe_plan(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype, int32_t m, MoePlan* q) {
+static MoePlan moe_plan(int64_t n, int32_t d, int32_t f, int32_t m) {
     auto align = [](size_t b) { return (b + 255) & ~(size_t)255; };
     const size_t pairs = (size_t)n * m;
-    q->fp = (f + 15) / 16 * 16;
-    q->o_act = 0;
+    MoePlan q;
+    q.fp = (f + 15) / 16 * 16;
+    q.o_act = 0;
     // fp32, or two parts of bf16
-    q->o_part = align(pairs * q->fp * 4);
-    q->bytes = q->o_part + align(pairs * d * 4);
-    if (q->bytes < 256) q->bytes = 256;
-    return true;
+    q.o_part = align(pairs * q.fp * 4);
+    q.bytes = q.o_part + align(pairs * d * 4);
+    if (q.bytes < 256) q.bytes = 256;
+    return q;
 }
 
 static int moe_check(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype, int32_t m) {
@@ -516,9 +516,7 @@ extern "C" {
 
 size_t gmm_moe_layer_workspace_bytes(int64_t n, int32_t d, int32_t f, int32_t e, int32_t dtype,
                                      int32_t m) {
-    MoePlan q;
-    if (moe_check(n, d, f, e, dtype, m) != GMM_OK) return 0;
-    return moe_plan(n, d, f, e, dtype, m, &q) ? q.bytes : 0;
+    return moe_check(n, d, f, e, dtype, m) == GMM_OK ? moe_plan(n, d, f, m).bytes : 0;
 }
 
 int gmm_moe_layer(const void* x, int64_t n, int32_t d, int64_t ldx, const void* gate, int32_t e,
@@ -529,8 +527,7 @@ int gmm_moe_layer(const void* x, int64_t n, int32_t d, int64_t ldx, const void* 
     if (rc != GMM_OK) return rc;
     if (ldx < d || ldy < d) return GMM_E_INVALID;
     if (n > 0 && (!x || !w_in || !w_out || !idx || !resp || !y)) return GMM_E_INVALID;
-    MoePlan q;
-    moe_plan(n, d, f, e, dtype, m, &q);
+    const MoePlan q = moe_plan(n, d, f, m);
     if (!workspace || workspace_bytes < q.bytes || (uintptr_t)workspace % 256 != 0)
         return GMM_E_WORKSPACE;
     if (n == 0) return GMM_OK;

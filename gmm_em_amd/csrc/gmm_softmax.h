@@ -98,8 +98,8 @@ __device__ __forceinline__ Raw16 load_zero(const T* p, int64_t i, int64_t end) {
 
 // ---- wave-wide reductions on the data-parallel lanes (no LDS)
 
-// v of another lane: 0x120 + N rotates each group of 16 lanes by N, 0x138
-// shifts the wave up by one lane (lane 0 keeps its own).
+// v of another lane: 0x120 + N rotates each group of 16 lanes by N, 0x140 and 0x141 mirror
+// groups of 16 and of 8, 0xb1 and 0x4e swap neighbours and pairs within each four.
 template <int CTRL>
 __device__ __forceinline__ float lane_move(float v) {
     const int u = (int)__float_as_uint(v);
