@@ -19,10 +19,10 @@
 // too, after its rows are divided by what dx's were multiplied by (so that rows count by
 // what they can add to dW, and those without a gradient not at all). What then lies
 // below 2^-29 of the largest of its dim or row loses digits, and below 2^-39 is dropped.
-// Measured, bf16, 8192 x 768 x 16384: scores 188 us (the product without epilogue 148, the
-// softmax of an accumulator is 7 operations and an exponential); gradient 690 us: dx 240,
-// dh 205 + 16 for its split, dW 212, ranges 13, turned operands 19. Bound by the
-// matrix products (1000 to 1400 TFLOP/s in them).
+// Measured, bf16, 8192 x 768 x 16384 (medians of one trace): scores 197 us: tiles 192 (the
+// product without epilogue 148; the softmax of an accumulator is 8 operations and an
+// exponential), join 5; gradient 705 us: ranges 14 + 5, dx 233, turned operands 16, dh 208 + 14
+// for its split, dW 215. Bound by the matrix products (950 to 1400 TFLOP/s in them).
 //
 // Orientation: the tiles' rows are the axis that the outputs are contiguous in
 // (codes for logits, dims for the gradients), their columns the rows of h (or
@@ -701,7 +701,13 @@ struct Tile<3> {
 // The tile and the split of the contracted axis that take least time by a
 // model of it: rounds of workgroups over the chip, each of a fixed part and a
 // part per step, and the writing and reading of a split's partial sums.
-// per_step: measured over long products, per workgroup with the chip full.
+// per_step: measured over long products of bf16 rows read in place, per workgroup with the chip
+// full; the gradients' operands take longer (a step of 192 x 256 1.6 us), all tiles alike.
+// What it picks against the best of the four tiles with splits of 1, 2, 4, 8 and 16 (microseconds of
+// a call for dh, for dW; in those dx has the tile too), bf16: 8192 x 768 x 16384 469 and 461 (469,
+// 474), 4096 x 1024 x 8192 179 and 155 (167, 167), 2048 x 512 x 32768 188 and 170 (206, 170), 1024 x
+// 768 x 4096 50 and 44 (49, 44), 300 x 256 x 5000 37 and 26 (36, 26); fp32: 2048 x 768 x 8192 315 and
+// 309 (323, 326), 777 x 100 x 1001 35 and 34 (34, 32).
 struct TileCost {
     int bm, bn, at_once;  // workgroups on the chip
     float per_step, fixed;  // microseconds

@@ -73,7 +73,7 @@ struct RowPart {
 // NT threads per (row, part). parts == 1: writes the results; else the part's
 // statistics and list go to the workspace for k_score_join.
 // Bound by its reads: 4096 rows of 32768 bf16 values in 51 us without alternatives
-// (5.3 TB/s), 57 us with 4; the insertion of every value above a wave's own m-th best
+// (5.3 TB/s), 58 us with 4; the insertion of every value above a wave's own m-th best
 // into its sorted list took 73.
 template <typename T, int NT, bool TOP>
 __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(64) void k_score_join(ScoreArgs p) {
 }
 
 // One block per (row, segment). Bound by its traffic: 4096 x 32768 bf16 (537 MB) in
-// 100 us, 5.4 TB/s.
+// 101 us, 5.3 TB/s.
 constexpr int SG_NT = 256, SG_U = 4;
 template <typename T>
 __global__ __launch_bounds__(SG_NT) void k_score_grad(ScoreGradArgs p) {
