@@ -215,7 +215,7 @@ def run(state):
             return [ops.embed_backward(s["x"], s["codes"], s["case"]["v"], s["scale"])]
         if op == "int8":
             q, scale = ops.quantize_rows(s["x"])
-            return [ops.int8_product(q, scale, s["w"], s["w_scale"], s["x"].dtype), scale]
+            return [ops.quantized_product(q, scale, s["w"], s["w_scale"], s["x"].dtype), scale]
         if op == "balance":
             r = ops.balance_loss(s["z"], s["idx"])
             dz = ops.balance_loss_backward(s["z"], r.counts, r.totals, r.norm, s["g"])
