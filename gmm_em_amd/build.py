@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgmm_em.so")
 SOURCES = ["gmm_api.hip", "gmm_kernels.hip", "gmm_wide.hip", "gmm_ivf.hip", "gmm_i8.hip",
            "gmm_b16.hip", "gmm_score.hip", "gmm_head.hip",
-           "gmm_moe.hip"]
+           "gmm_moe.hip", "gmm_embed.hip", "gmm_quant.hip", "gmm_beam.hip",
+           "gmm_balance.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,353 @@
+// gmm_balance.hip - the balance loss of a router and its gradient (gmm_balance_loss,
+// gmm_balance_loss_backward, declared in include/gmm_em.h). With p = softmax(z) of a row's
+// gate logits, f_c = picks of expert c / all picks, P_c = the rows' mean of p_c:
+//   loss = E sum_c f_c P_c        dz_c = g E / rows p_c (f_c - sum_c' f_c' p_c')
+// (f is constant for the gradient: picks have none).
+//
+// One pass over the logits: 16, 32 or 64 lanes hold a row, so that a wave has up to four
+// rows at once and a lane always the same experts: their sums of p stay in its registers. A
+// workgroup leaves its sums and counts in the workspace and k_balance_join adds them in order.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "gmm_em.h"
+#include "gmm_nn.h"
+#include "gmm_softmax.h"
+
+namespace gmm {
+
+constexpr int BAL_MAX_EXPERTS = 4096;  // as the layer's
+constexpr int BAL_NT = 256, BAL_W = BAL_NT / 64;
+constexpr int BAL_PARTS = 256;         // workgroups of the pass over the rows
+
+struct BalanceArgs {
+    const void* z;
+    void* dz;
+    const int32_t* idx;
+    int64_t n, ldz, lddz;
+    int32_t e, m, parts;
+    float *norm, *loss, *prob;
+    int32_t* counts;
+    int64_t* totals;
+    const float* g_loss;
+    float* part_p;      // [parts][e]
+    int32_t* part_c;    // [parts][e + 1]: counts, then rows
+};
+
+// over groups of LPR lanes
+template <int LPR>
+__device__ __forceinline__ float group_reduce_max(float v) {
+    v = max16(v);
+    if (LPR > 16) v = fmaxf(v, __shfl_xor(v, 16));
+    if (LPR > 32) v = fmaxf(v, __shfl_xor(v, 32));
+    return v;
+}
+template <int LPR>
+__device__ __forceinline__ float group_reduce_sum(float v) {
+    v = sum16(v);
+    if (LPR > 16) v += __shfl_xor(v, 16);
+    if (LPR > 32) v += __shfl_xor(v, 32);
+    return v;
+}
+
+// The values of a row that a lane holds: vectors at gl VE, gl VE + LPR VE, ...
+template <typename T, int LPR, int CV>
+struct RouterRow {
+    static constexpr int VE = Vec<T>::VE, C = CV * VE;
+    static __device__ __forceinline__ int at(int gl, int j) { return (j / VE * LPR + gl) * VE + j % VE; }
+    float v[C];
+    __device__ __forceinline__ void load(const T* z, int e, int gl) {
+#pragma unroll
+        for (int q = 0; q < CV; ++q) {
+            const Raw16 r = load_vec(z, (int64_t)(q * LPR + gl) * VE, (int64_t)e);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) v[q * VE + k] = Vec<T>::get(r, k);
+        }
+    }
+};
+
+template <typename T, int LPR, int CV>
+__global__ __launch_bounds__(BAL_NT) void k_balance_rows(BalanceArgs p) {
+    using Row = RouterRow<T, LPR, CV>;
+    constexpr int C = Row::C, RPW = 64 / LPR;
+    extern __shared__ float sums[];  // [e], then counts [e + 1]
+    int* cnt = (int*)(sums + p.e);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int gl = lane % LPR, grp = lane / LPR;
+    for (int c = tid; c <= p.e; c += BAL_NT) cnt[c] = 0;
+    __syncthreads();
+    float acc[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[j] = 0.f;
+    const int64_t step = (int64_t)p.parts * BAL_W * RPW;
+    for (int64_t r0 = ((int64_t)blockIdx.x * BAL_W + wave) * RPW; r0 < p.n; r0 += step) {
+        const int64_t row = r0 + grp;
+        const bool in = row < p.n;
+        int pick = -1;
+        if (in && gl < p.m) pick = p.idx[row * p.m + gl];
+        const bool picked = pick >= 0 && pick < p.e;
+        const uint64_t mine = ((LPR == 64 ? ~uint64_t(0) : (uint64_t(1) << (LPR & 63)) - 1)) << (grp * LPR);
+        const bool live = (__builtin_amdgcn_ballot_w64(picked) & mine) != 0;
+        if (picked) atomicAdd(&cnt[pick], 1);
+        if (gl == 0 && live) atomicAdd(&cnt[p.e], 1);
+        Row x;
+        x.load((const T*)p.z + (in ? row : 0) * p.ldz, p.e, gl);
+        float m = -3.402823466e38f, s = 0.f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) m = fmaxf(m, x.v[j]);
+        m = group_reduce_max<LPR>(m);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            x.v[j] = exp_neg(x.v[j] - m);
+            s += x.v[j];
+        }
+        s = group_reduce_sum<LPR>(s);
+        const bool none = s == 0.f;  // every logit -inf
+        if (live) {
+            const float inv = none ? 0.f : 1.f / s;
+#pragma unroll
+            for (int j = 0; j < C; ++j) acc[j] = fmaf(x.v[j], inv, acc[j]);
+        }
+        if (gl == 0 && in) {
+            p.norm[2 * row] = !live ? INFINITY : none ? -INFINITY : (s == s ? m : NAN);
+            p.norm[2 * row + 1] = !live || none ? 0.f : logf(s);
+        }
+    }
+    // the rows of a wave, then its workgroup's waves in order
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        if (LPR < 32) acc[j] += __shfl_xor(acc[j], 16);
+        if (LPR < 64) acc[j] += __shfl_xor(acc[j], 32);
+    }
+    for (int w = 0; w < BAL_W; ++w) {
+        if (w == wave && grp == 0) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                const int c = Row::at(gl, j);
+                if (c < p.e) sums[c] = w == 0 ? acc[j] : sums[c] + acc[j];
+            }
+        }
+        __syncthreads();
+    }
+    for (int c = tid; c < p.e; c += BAL_NT) p.part_p[(int64_t)blockIdx.x * p.e + c] = sums[c];
+    for (int c = tid; c <= p.e; c += BAL_NT) p.part_c[(int64_t)blockIdx.x * (p.e + 1) + c] = cnt[c];
+}
+
+// One workgroup adds the parts: 16 groups of them side by side, then those in order.
+constexpr int BJ_NT = 1024, BJ_G = 16, BJ_C = BJ_NT / BJ_G;
+__global__ __launch_bounds__(BJ_NT) void k_balance_join(BalanceArgs p) {
+    __shared__ float sp[BJ_G][BJ_C];
+    __shared__ int sc[BJ_G][BJ_C];
+    const int tid = threadIdx.x, col = tid % BJ_C, g = tid / BJ_C;  // a group is a wave
+    const int a = p.parts * g / BJ_G, z = p.parts * (g + 1) / BJ_G;
+    int rows = 0;
+    for (int t = col; t < p.parts; t += BJ_C) rows += p.part_c[(int64_t)t * (p.e + 1) + p.e];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) rows += __shfl_xor(rows, o);
+    float dot = 0.f;         // sum of picks * mass over this thread's experts
+    long long total = 0;
+    for (int c0 = 0; c0 < p.e; c0 += BJ_C) {
+        const int c = c0 + col;
+        float s = 0.f;
+        int n = 0;
+        if (c < p.e) {
+#pragma unroll 8
+            for (int t = a; t < z; ++t) {
+                s += p.part_p[(int64_t)t * p.e + c];
+                n += p.part_c[(int64_t)t * (p.e + 1) + c];
+            }
+        }
+        sp[g][col] = s;
+        sc[g][col] = n;
+        __syncthreads();
+        if (g == 0 && c < p.e) {
+            for (int q = 1; q < BJ_G; ++q) {
+                s += sp[q][col];
+                n += sc[q][col];
+            }
+            p.counts[c] = n;
+            p.prob[c] = s / (float)(rows > 0 ? rows : 1);
+            total += n;
+            dot = fmaf((float)n, s, dot);
+        }
+        __syncthreads();
+    }
+    if (g == 0) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
+        dot = wave_sum(dot);
+        if (col == 0) {
+            p.totals[0] = rows;
+            p.totals[1] = total;
+            p.loss[0] = rows > 0 ? (float)p.e * (dot / (float)total / (float)rows) : 0.f;
+        }
+    }
+}
+
+template <typename T, int LPR, int CV>
+__global__ __launch_bounds__(BAL_NT) void k_balance_grad(BalanceArgs p) {
+    using Row = RouterRow<T, LPR, CV>;
+    constexpr int C = Row::C, RPW = 64 / LPR, VE = Vec<T>::VE;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int gl = lane % LPR, grp = lane / LPR;
+    const float rows = (float)p.totals[0], picks = (float)p.totals[1];
+    const float by = (p.g_loss ? p.g_loss[0] : 1.f) * ((float)p.e / fmaxf(rows, 1.f));
+    float f[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        const int c = Row::at(gl, j);
+        f[j] = c < p.e ? (float)p.counts[c] / fmaxf(picks, 1.f) : 0.f;
+    }
+    for (int64_t r0 = ((int64_t)blockIdx.x * BAL_W + wave) * RPW; r0 < p.n;
+         r0 += (int64_t)gridDim.x * BAL_W * RPW) {
+        const int64_t row = r0 + grp;
+        const bool in = row < p.n;
+        const float m = in ? p.norm[2 * row] : INFINITY, logs = in ? p.norm[2 * row + 1] : 0.f;
+        Row x;
+        x.load((const T*)p.z + (in ? row : 0) * p.ldz, p.e, gl);
+        const bool off = m == INFINITY || m == -INFINITY;  // left out, or no logit above -inf
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            x.v[j] = off ? 0.f : exp_neg((x.v[j] - m) - logs);
+            s = fmaf(f[j], x.v[j], s);
+        }
+        s = group_reduce_sum<LPR>(s);
+        if (!in) continue;
+        T* out = (T*)p.dz + row * p.lddz;
+#pragma unroll
+        for (int q = 0; q < CV; ++q) {
+            const int64_t i = (int64_t)(q * LPR + gl) * VE;
+            Raw16 o = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                const int j = q * VE + k;
+                Vec<T>::set(o, k, off ? 0.f : by * (x.v[j] * (f[j] - s)));
+            }
+            if (i + VE <= p.e) {
+                *reinterpret_cast<Raw16*>(out + i) = o;
+            } else {
+#pragma unroll
+                for (int k = 0; k < VE; ++k)
+                    if (i + k < p.e) out[i + k] = Vec<T>::store(Vec<T>::get(o, k));
+            }
+        }
+    }
+}
+
+static size_t bal_up(size_t b) { return (b + 255) & ~(size_t)255; }
+static int balance_parts(int64_t n) {
+    const int64_t want = (n + 15) / 16;
+    return (int)(want < 1 ? 1 : want < BAL_PARTS ? want : BAL_PARTS);
+}
+static bool balance_ok(int64_t n, int32_t e, int32_t m) {
+    return n >= 0 && e >= 1 && m >= 1 && m <= TOP_MAX;
+}
+static bool balance_fits(int64_t n, int32_t e, int32_t m) {
+    return e <= BAL_MAX_EXPERTS && n <= 0x7fffffff / m;  // counts are 32-bit
+}
+
+// Lanes of a row and vectors of a lane: as few lanes as hold the row in one vector each.
+template <typename T, typename F>
+static void with_row(int e, F f) {
+    constexpr int VE = Vec<T>::VE;
+    using std::integral_constant;
+    if (e <= 16 * VE) f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    else if (e <= 32 * VE) f(integral_constant<int, 32>(), integral_constant<int, 1>());
+    else if (e <= 64 * VE) f(integral_constant<int, 64>(), integral_constant<int, 1>());
+    else if (e <= 256 * VE) f(integral_constant<int, 64>(), integral_constant<int, 4>());
+    else f(integral_constant<int, 64>(), integral_constant<int, BAL_MAX_EXPERTS / 64 / VE>());
+}
+
+template <typename T>
+static hipError_t balance(const BalanceArgs& a, hipStream_t st) {
+    with_row<T>(a.e, [&](auto l, auto c) {
+        constexpr int LPR = decltype(l)::value, CV = decltype(c)::value;
+        const size_t lds = (size_t)(2 * a.e + 1) * 4;
+        hipLaunchKernelGGL((k_balance_rows<T, LPR, CV>), dim3(a.parts), dim3(BAL_NT), lds, st, a);
+    });
+    hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(BJ_NT), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t balance_grad(const BalanceArgs& a, hipStream_t st) {
+    with_row<T>(a.e, [&](auto l, auto c) {
+        constexpr int LPR = decltype(l)::value, CV = decltype(c)::value;
+        const int64_t per = BAL_W * (64 / LPR), blocks = (a.n + per - 1) / per;
+        hipLaunchKernelGGL((k_balance_grad<T, LPR, CV>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)),
+                           dim3(BAL_NT), 0, st, a);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace gmm
+
+using namespace gmm;
+
+extern "C" {
+
+size_t gmm_balance_loss_workspace_bytes(int64_t n, int32_t e, int32_t m) {
+    if (!balance_ok(n, e, m) || !balance_fits(n, e, m)) return 0;
+    const size_t parts = balance_parts(n);
+    return bal_up(parts * e * 4) + bal_up(parts * (e + 1) * 4);
+}
+
+int gmm_balance_loss(const void* logits, int64_t n, int32_t e, int64_t ldz, int32_t dtype,
+                     const int32_t* idx, int32_t m, float* loss, int32_t* counts, int64_t* totals,
+                     float* prob, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dtype != GMM_F32 && dtype != GMM_BF16) return GMM_E_DTYPE;
+    if (!balance_ok(n, e, m) || ldz < e || !loss || !counts || !totals || !prob) return GMM_E_INVALID;
+    if (n > 0 && (!logits || !idx || !norm)) return GMM_E_INVALID;
+    if (!balance_fits(n, e, m)) return GMM_E_UNSUPPORTED;
+    if (!workspace || workspace_bytes < gmm_balance_loss_workspace_bytes(n, e, m) ||
+        (uintptr_t)workspace % 256 != 0)
+        return GMM_E_WORKSPACE;
+    BalanceArgs a{};
+    a.z = logits;
+    a.idx = idx;
+    a.n = n;
+    a.ldz = ldz;
+    a.e = e;
+    a.m = m;
+    a.parts = balance_parts(n);
+    a.norm = norm;
+    a.loss = loss;
+    a.prob = prob;
+    a.counts = counts;
+    a.totals = totals;
+    a.part_p = (float*)workspace;
+    a.part_c = (int32_t*)((char*)workspace + bal_up((size_t)a.parts * e * 4));
+    const hipError_t err = dtype == GMM_F32 ? balance<float>(a, (hipStream_t)stream)
+                                            : balance<uint16_t>(a, (hipStream_t)stream);
+    return err == hipSuccess ? GMM_OK : GMM_E_HIP;
+}
+
+int gmm_balance_loss_backward(const void* logits, int64_t n, int32_t e, int64_t ldz, int32_t dtype,
+                              const int32_t* counts, const int64_t* totals, const float* norm,
+                              const float* g_loss, void* dlogits, int64_t lddz, void* stream) {
+    if (dtype != GMM_F32 && dtype != GMM_BF16) return GMM_E_DTYPE;
+    if (!balance_ok(n, e, 1) || ldz < e || lddz < e) return GMM_E_INVALID;
+    if (!balance_fits(n, e, 1)) return GMM_E_UNSUPPORTED;
+    if (n > 0 && (!logits || !counts || !totals || !norm || !dlogits)) return GMM_E_INVALID;
+    if (n == 0) return GMM_OK;
+    BalanceArgs a{};
+    a.z = logits;
+    a.dz = dlogits;
+    a.n = n;
+    a.ldz = ldz;
+    a.lddz = lddz;
+    a.e = e;
+    a.counts = (int32_t*)counts;
+    a.totals = (int64_t*)totals;
+    a.norm = (float*)norm;
+    a.g_loss = g_loss;
+    const hipError_t err = dtype == GMM_F32 ? balance_grad<float>(a, (hipStream_t)stream)
+                                            : balance_grad<uint16_t>(a, (hipStream_t)stream);
+    return err == hipSuccess ? GMM_OK : GMM_E_HIP;
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
 // gmm_nn.h - arguments and launchers shared by the softmax-over-codes
-// operators (gmm_score.hip, gmm_head.hip, gmm_moe.hip).
+// operators (gmm_score.hip, gmm_head.hip, gmm_moe.hip) and those for sequences of codes
+// (gmm_beam.hip, gmm_embed.hip, gmm_quant.hip, gmm_balance.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -35,7 +36,19 @@ struct ScoreArgs {
     ScorePart* part;
     float* part_v;
     int32_t* part_i;
+    // beam search: rows that have no continuations of their own are not read
+    const float* beam_score;
+    const int32_t* beam_last;
+    int32_t beam_end;
 };
+
+// A beam goes on with the codes of its row: its score is finite and its last code is not the end.
+__device__ __forceinline__ bool beam_alive(const float* score, int64_t row) {
+    return fabsf(score[row]) < INFINITY;
+}
+__device__ __forceinline__ bool beam_ended(const int32_t* last, int32_t end, int64_t row) {
+    return last && end >= 0 && last[row] == end;
+}
 
 // Writes a row's results from its statistics and its target's logit xt
 // (thread 0) and its sorted alternatives (thread j < m holds entry j).

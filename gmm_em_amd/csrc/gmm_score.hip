@@ -75,7 +75,8 @@ struct RowPart {
 // Bound by its reads: 4096 rows of 32768 bf16 values in 51 us without alternatives
 // (5.3 TB/s), 58 us with 4; the insertion of every value above a wave's own m-th best
 // into its sorted list took 73.
-template <typename T, int NT, bool TOP>
+// BEAM: rows of beams that are dead or have ended are left out, their results unwritten.
+template <typename T, int NT, bool TOP, bool BEAM = false>
 __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
     constexpr int VE = Vec<T>::VE, NW = NT / 64, G = NT / 64, CHUNK = NT * VE * SC_U;
     __shared__ float sst[NW][3], gmax[64], cv[SC_CAND], best_v;
@@ -83,6 +84,7 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int64_t item = blockIdx.x; item < p.n * p.parts; item += gridDim.x) {
         const int64_t row = item / p.parts;
+        if (BEAM && (!beam_alive(p.beam_score, row) || beam_ended(p.beam_last, p.beam_end, row))) continue;
         const int part = (int)(item - row * p.parts);
         const int64_t i0 = (int64_t)part * p.part_len;
         const RowPart<T> x{(const T*)p.x + row * p.ldl + i0,
@@ -334,7 +336,9 @@ static void launch_score_nt(const ScoreArgs& a, hipStream_t st) {
     const int64_t items = a.n * a.parts;
     const int64_t most = (int64_t)1 << 20;  // grid threads stay below 2^32
     const dim3 grid((unsigned)(items < most ? items : most));
-    if (a.m > 0)
+    if (a.beam_score)
+        hipLaunchKernelGGL((k_score<T, NT, true, true>), grid, dim3(NT), 0, st, a);
+    else if (a.m > 0)
         hipLaunchKernelGGL((k_score<T, NT, true>), grid, dim3(NT), 0, st, a);
     else
         hipLaunchKernelGGL((k_score<T, NT, false>), grid, dim3(NT), 0, st, a);

@@ -53,6 +53,25 @@ lib.gmm_moe_layer_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32
 lib.gmm_moe_layer_workspace_bytes.restype = _sz
 lib.gmm_moe_layer.argtypes = [_vp, _i64, _i32, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
                               _vp, _vp, _i64, _vp, _sz, _vp]
+lib.gmm_embed.argtypes = [_vp, _i32, _i32, _i64, _i32, _vp, _i64, _f32, _vp, _i64, _vp]
+lib.gmm_embed_backward_workspace_bytes.argtypes = [_i64, _i32, _i32]
+lib.gmm_embed_backward_workspace_bytes.restype = _sz
+lib.gmm_embed_backward.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i32, _f32, _vp, _i64, _vp, _sz, _vp]
+lib.gmm_quantize_rows.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _vp]
+lib.gmm_quantized_product_workspace_bytes.argtypes = [_i64, _i32, _i32]
+lib.gmm_quantized_product_workspace_bytes.restype = _sz
+lib.gmm_quantized_product.argtypes = [_vp, _i64, _i32, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _i32,
+                                      _vp, _sz, _vp]
+lib.gmm_beam_step_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32]
+lib.gmm_beam_step_workspace_bytes.restype = _sz
+lib.gmm_beam_step.argtypes = [_vp, _i64, _i32, _i32, _i64, _i32, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp,
+                              _vp, _sz, _vp]
+lib.gmm_beam_reorder.argtypes = [_vp, _i64, _i64, _i64, _i32, _i64, _i64, _vp, _i32, _vp, _i64, _i64, _vp]
+lib.gmm_balance_loss_workspace_bytes.argtypes = [_i64, _i32, _i32]
+lib.gmm_balance_loss_workspace_bytes.restype = _sz
+lib.gmm_balance_loss.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                 _vp]
+lib.gmm_balance_loss_backward.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
 lib.gmm_device_status.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.argtypes = [_vp, _vp]
 lib.gmm_estep_arithmetic.restype = ctypes.c_int
@@ -64,7 +83,9 @@ lib.gmm_profile_end.argtypes = [ctypes.POINTER(_f64), ctypes.POINTER(_i32), ctyp
                                 ctypes.POINTER(_i32)]
 for _f in (lib.gmm_em_step, lib.gmm_fit, lib.gmm_loglik, lib.gmm_assign_topm, lib.gmm_kmeans_step,
            lib.gmm_kmeans_fit, lib.gmm_ivf_build, lib.gmm_logits_score, lib.gmm_logits_score_backward,
-           lib.gmm_head_score, lib.gmm_head_score_backward, lib.gmm_moe_layer, lib.gmm_device_status, lib.gmm_profile_begin, lib.gmm_profile_end):
+           lib.gmm_head_score, lib.gmm_head_score_backward, lib.gmm_moe_layer, lib.gmm_embed, lib.gmm_embed_backward,
+           lib.gmm_quantize_rows, lib.gmm_quantized_product, lib.gmm_beam_step, lib.gmm_beam_reorder,
+           lib.gmm_balance_loss, lib.gmm_balance_loss_backward, lib.gmm_device_status, lib.gmm_profile_begin, lib.gmm_profile_end):
     _f.restype = ctypes.c_int
 
 (GMM_OK, GMM_E_INVALID, GMM_E_DTYPE, GMM_E_WORKSPACE, GMM_E_PARAMS, GMM_E_HIP,
@@ -483,6 +504,274 @@ def moe_layer(x, w_in, w_out, gate=None, m: int = 2, share_all: bool = False, id
                                  w_out.data_ptr(), f, dt, m, int(share_all), idx.data_ptr(),
                                  resp.data_ptr(), y.data_ptr(), d, ws.data_ptr(), nb, stream))
     return y, idx, resp
+
+
+def _new_like_rows(out, n, d, x, name="out"):
+    """(tensor, leading dimension) of an (n, d) result in x's type: the caller's, or a new one."""
+    if out is None:
+        out = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    elif tuple(out.shape) != (n, d) or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError(f"{name} must be an ({n}, {d}) tensor of the operand's type and device")
+    return out, _rows2(out, name)[1]
+
+
+def embed(table, codes, scale: float = 1.0, out=None):
+    """Rows scale * table[codes] (N, D), in the table's type.
+
+    table (V, D) float32 or bfloat16, rows of any stride; codes int32 (N,): a negative
+    one gives a row of 0, one of V or more a row of NaN. See gmm_embed in ``include/gmm_em.h``.
+    """
+    dt, ldt = _rows2(table, "table")
+    v, d = table.shape
+    _int32(v, d)
+    dev = table.device
+    n = codes.numel()
+    c = _row(codes, n, "codes", torch.int32, dev)
+    out, ldo = _new_like_rows(out, n, d, table)
+    with _On(dev) as stream:
+        _check(lib.gmm_embed(table.data_ptr(), v, d, ldt, dt, c, n, scale, out.data_ptr(), ldo, stream))
+    return out
+
+
+def embed_backward(grad, codes, v: int, scale: float = 1.0, out=None, ws=None):
+    """Gradient (V, D) of :func:`embed` with respect to its table, in the type of grad (N, D).
+
+    Sums in float32 in a fixed order. See gmm_embed_backward in ``include/gmm_em.h``.
+    """
+    dt, ldg = _rows2(grad, "grad")
+    n, d = grad.shape
+    _int32(d, v)
+    dev = grad.device
+    c = _row(codes, n, "codes", torch.int32, dev)
+    ws, nb = _scratch(lib.gmm_embed_backward_workspace_bytes(n, d, v), ws, dev)
+    out, ldt = _new_like_rows(out, v, d, grad)
+    with _On(dev) as stream:
+        _check(lib.gmm_embed_backward(grad.data_ptr(), n, d, ldg, dt, c, v, scale, out.data_ptr(), ldt,
+                                      ws.data_ptr(), nb, stream))
+    return out
+
+
+def _bytes2(t, name):
+    """Leading dimension of a 2-D row-major int8 device tensor."""
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit stride along columns")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return max(t.stride(0), t.shape[1])
+
+
+def quantize_rows(x):
+    """Rows in 8-bit integers: (q int8 (N, D), scale float32 (N,)) with x close to q * scale[:, None].
+
+    scale = max |x| / 127 of the row. See gmm_quantize_rows in ``include/gmm_em.h``.
+    """
+    dt, ldx = _rows2(x, "x")
+    n, d = x.shape
+    _int32(d)
+    q = torch.empty((n, d), dtype=torch.int8, device=x.device)
+    scale = torch.empty(n, dtype=torch.float32, device=x.device)
+    with _On(x.device) as stream:
+        _check(lib.gmm_quantize_rows(x.data_ptr(), n, d, ldx, dt, q.data_ptr(), d, scale.data_ptr(), stream))
+    return q, scale
+
+
+def quantized_product(q, q_scale, weight, weight_scale, dtype=torch.bfloat16, out=None, ws=None):
+    """(q * q_scale[:, None]) @ (weight * weight_scale[:, None]).T (N, V) of int8 rows, in ``dtype``.
+
+    q (N, D) and weight (V, D) int8, rows of any stride, with float32 scales of their rows, as
+    :func:`quantize_rows` returns them. Sums are exact. See gmm_quantized_product in
+    ``include/gmm_em.h``.
+    """
+    ldq, ldw = _bytes2(q, "q"), _bytes2(weight, "weight")
+    n, d = q.shape
+    v = weight.shape[0]
+    if weight.shape[1] != d or weight.device != q.device:
+        raise ValueError("q (N, D) and weight (V, D) must agree in D and device")
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dtype must be float32 or bfloat16")
+    _int32(d, v)
+    dev = q.device
+    qs = _row(q_scale, n, "q_scale", torch.float32, dev)
+    wsc = _row(weight_scale, v, "weight_scale", torch.float32, dev)
+    ws, nb = _scratch(lib.gmm_quantized_product_workspace_bytes(n, d, v), ws, dev)
+    if out is None:
+        out = torch.empty((n, v), dtype=dtype, device=dev)
+    elif tuple(out.shape) != (n, v) or out.dtype != dtype or out.device != dev:
+        raise ValueError(f"out must be an ({n}, {v}) tensor of dtype on q's device")
+    dt, ldy = _rows2(out, "out")
+    with _On(dev) as stream:
+        _check(lib.gmm_quantized_product(q.data_ptr(), n, d, ldq, qs, weight.data_ptr(), v, ldw, wsc,
+                                         out.data_ptr(), ldy, dt, ws.data_ptr(), nb, stream))
+    return out
+
+
+class Beams(NamedTuple):
+    """What :func:`beam_step` returns, best beam first; places without a beam hold -1, -1 and -inf."""
+
+    parent: torch.Tensor  # (B, m) int32: the beam that is continued
+    code: torch.Tensor    # (B, m) int32: its next code
+    score: torch.Tensor   # (B, m) float32
+
+
+def _grid2(t, shape, name, dtype, device):
+    """Address of a contiguous 2-D tensor of a given shape."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on the operand's device")
+    return t.data_ptr()
+
+
+def beam_step(logits, scores, last=None, end: int = -1, m: Optional[int] = None, scale: float = 1.0,
+              ws=None) -> Beams:
+    """The m best continuations of each search's beams (m = W unless given).
+
+    logits (B * W, V) float32 or bfloat16; scores float32 (B, W), the beams' log-probabilities so
+    far (not finite: no beam); last int32 (B, W), their last codes: a beam whose last code is
+    ``end`` (not negative) goes on as itself. See gmm_beam_step in ``include/gmm_em.h``.
+    """
+    dt, ldl = _rows2(logits, "logits")
+    dev = logits.device
+    if scores.dim() != 2:
+        raise ValueError("scores must be a (B, W) tensor")
+    b, w = scores.shape
+    m = w if m is None else m
+    n, v = logits.shape
+    if n != b * w:
+        raise ValueError("logits must have B * W rows")
+    _int32(v, w, m)
+    if not -0x80000000 <= end <= 0x7fffffff:
+        raise GmmError(GMM_E_INVALID)
+    sc = _grid2(scores, (b, w), "scores", torch.float32, dev)
+    la = None if last is None else _grid2(last, (b, w), "last", torch.int32, dev)
+    ws, nb = _scratch(lib.gmm_beam_step_workspace_bytes(b, w, v, m), ws, dev)
+    i32 = torch.int32
+    out = Beams(torch.empty((b, m), dtype=i32, device=dev), torch.empty((b, m), dtype=i32, device=dev),
+                torch.empty((b, m), dtype=torch.float32, device=dev))
+    with _On(dev) as stream:
+        _check(lib.gmm_beam_step(logits.data_ptr(), b, w, v, ldl, dt, sc, la, end, m, scale,
+                                 out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), nb,
+                                 stream))
+    return out
+
+
+def _state(t, dim, name):
+    """(outer, outer stride, row stride, row bytes) of a tensor as rows along ``dim``, in bytes."""
+    size, stride, es = list(t.shape), list(t.stride()), t.element_size()
+    inner = 1
+    for k in range(t.dim() - 1, dim, -1):
+        if size[k] != 1:
+            if stride[k] != inner:
+                raise ValueError(f"the dims of {name} behind dim must be contiguous")
+            inner *= size[k]
+    outer, step = 1, 0
+    for k in range(dim - 1, -1, -1):
+        if size[k] != 1:
+            if outer == 1:
+                step = stride[k]
+            elif stride[k] != step * outer:
+                raise ValueError(f"the dims of {name} before dim must form one")
+            outer *= size[k]
+    return outer, step * es, stride[dim] * es if size[dim] > 1 else inner * es, inner * es
+
+
+def beam_reorder(state, parent, w: int, dim: int = 0, out=None):
+    """The states of the beams that :func:`beam_step` chose, for states of any type.
+
+    state's dim ``dim`` holds the B * w beams before the step (as one row of logits each), the
+    result's the B * m after it; parent int32 (B, m). A place without a parent gets 0. out may be
+    the state itself (m = w): rows that stay are then not touched. See gmm_beam_reorder in
+    ``include/gmm_em.h``.
+    """
+    if not state.is_cuda:
+        raise ValueError("state must be a device tensor")
+    if state.is_complex() or state.is_quantized or state.layout != torch.strided:
+        raise TypeError("state must be a plain strided tensor")
+    if not -state.dim() <= dim < state.dim():
+        raise ValueError("dim must be a dim of state")
+    dim %= state.dim()
+    if parent.dim() != 2:
+        raise ValueError("parent must be a (B, m) tensor")
+    dev = state.device
+    b, m = parent.shape
+    pa = _grid2(parent, (b, m), "parent", torch.int32, dev)
+    if state.shape[dim] != b * w:
+        raise ValueError("state must have B * w rows along dim")
+    _int32(w, m)
+    shape = (*state.shape[:dim], b * m, *state.shape[dim + 1:])
+    if out is None:
+        out = torch.empty(shape, dtype=state.dtype, device=dev)
+    elif tuple(out.shape) != shape or out.dtype != state.dtype or out.device != dev:
+        raise ValueError("out must have state's shape with B * m rows, its type and device")
+    if out.numel() == 0:
+        return out
+    outer, so, sr, nb = _state(state, dim, "state")
+    outer2, oo, orow, _ = _state(out, dim, "out")
+    with _On(dev) as stream:
+        _check(lib.gmm_beam_reorder(state.data_ptr(), outer, so, b, w, sr, nb, pa, m, out.data_ptr(), oo, orow,
+                                    stream))
+    return out
+
+
+class Balance(NamedTuple):
+    """What :func:`balance_loss` returns."""
+
+    loss: torch.Tensor    # () float32
+    counts: torch.Tensor  # (E,) int32: picks of each expert
+    totals: torch.Tensor  # (2,) int64: rows with a pick, picks
+    prob: torch.Tensor    # (E,) float32: mean probability over those rows
+    norm: torch.Tensor    # (N, 2) float32, for the gradient
+
+
+def balance_loss(logits, idx, ws=None) -> Balance:
+    """Balance loss E * sum(share of the picks * mean probability) of a router, and what it is made of.
+
+    logits (N, E) float32 or bfloat16; idx int32 (N, m), the picks, as :func:`moe_layer` and
+    :func:`assign_topm` return them; those outside [0, E) are none and a row without any is left
+    out. See gmm_balance_loss in ``include/gmm_em.h``.
+    """
+    dt, ldz = _rows2(logits, "logits")
+    n, e = logits.shape
+    dev = logits.device
+    if idx.dim() != 2:
+        raise ValueError("idx must be an (N, m) tensor")
+    m = idx.shape[1]
+    ix = _grid2(idx, (n, m), "idx", torch.int32, dev)
+    _int32(e, m)
+    ws, nb = _scratch(lib.gmm_balance_loss_workspace_bytes(n, e, m), ws, dev)
+    f32 = torch.float32
+    out = Balance(torch.empty((), dtype=f32, device=dev), torch.empty(e, dtype=torch.int32, device=dev),
+                  torch.empty(2, dtype=torch.int64, device=dev), torch.empty(e, dtype=f32, device=dev),
+                  torch.empty((n, 2), dtype=f32, device=dev))
+    with _On(dev) as stream:
+        _check(lib.gmm_balance_loss(logits.data_ptr(), n, e, ldz, dt, ix, m, out[0].data_ptr(),
+                                    out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                                    out[4].data_ptr(), ws.data_ptr(), nb, stream))
+    return out
+
+
+def balance_loss_backward(logits, counts, totals, norm, g_loss=None, out=None):
+    """Gradient of :func:`balance_loss`'s loss with respect to the logits, in their type.
+
+    counts, totals and norm are what the forward call returned; g_loss a float32 device tensor
+    of one value, None for 1. out may be the logits themselves.
+    """
+    dt, ldz = _rows2(logits, "logits")
+    n, e = logits.shape
+    dev = logits.device
+    _int32(e)
+    _norm(norm, n, dev)
+    c = _row(counts, e, "counts", torch.int32, dev)
+    t = _row(totals, 2, "totals", torch.int64, dev)
+    if g_loss is not None and (g_loss.dtype != torch.float32 or g_loss.numel() != 1 or g_loss.device != dev):
+        raise ValueError("g_loss must be a float32 tensor of one value on the device of the logits")
+    out, ldo = _new_like_rows(out, n, e, logits)
+    with _On(dev) as stream:
+        _check(lib.gmm_balance_loss_backward(logits.data_ptr(), n, e, ldz, dt, c, t, norm.data_ptr(),
+                                             _addr(g_loss), out.data_ptr(), ldo, stream))
+    return out
 
 
 def device_status(ws, device="cuda") -> int:

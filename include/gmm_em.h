@@ -346,6 +346,113 @@ int gmm_moe_layer(const void* x, int64_t n, int32_t d, int64_t ldx, const void* 
                   int32_t share_all, int32_t* idx, float* resp, void* y, int64_t ldy,
                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* Embedding of codes: out[r] = scale * table[codes[r]], rounded once to the table's type. The
+ * input end of a model over codes, as gmm_head_score is its output end. table (device): v rows of d
+ * values with leading dimension ldt >= d, fp32 or bf16; codes (device, n int32): a negative one is
+ * no code and gives a row of 0, one of v or more a row of NaN. out (n x d, type of the table, leading
+ * dimension ldo >= d) must not overlap the table. Any alignment of an element; offsets are 64-bit.
+ * scale must be finite. n may be 0; n <= 2^40, d <= 2^20, v <= 2^22 (GMM_E_UNSUPPORTED beyond
+ * for d and v). Needs no workspace. */
+int gmm_embed(const void* table, int32_t v, int32_t d, int64_t ldt, int32_t dtype,
+              const int32_t* codes, int64_t n, float scale, void* out, int64_t ldo, void* stream);
+
+/* Gradient of gmm_embed with respect to its table: for the gradient grad (device, n x d, leading
+ * dimension ldg >= d) that arrives at out,
+ *   d_table[c] = scale * sum of grad[r] over the rows r with codes[r] = c
+ * in grad's type, rounded once from fp32 sums; a code that no row has gets 0, rows whose code is
+ * not in [0, v) add nothing. The rows are sorted by code, so every sum has one order (bitwise
+ * reproducible) and a code that most rows have costs no more than others. d_table (v x d, leading
+ * dimension ldt >= d) must not overlap grad. n = 0 sets d_table to 0. n < 2^31, d and v as for
+ * gmm_embed (GMM_E_UNSUPPORTED beyond). The workspace (device, 256-byte aligned) has
+ * gmm_embed_backward_workspace_bytes(n, d, v) bytes (0: invalid or unsupported sizes). */
+size_t gmm_embed_backward_workspace_bytes(int64_t n, int32_t d, int32_t v);
+int gmm_embed_backward(const void* grad, int64_t n, int32_t d, int64_t ldg, int32_t dtype,
+                       const int32_t* codes, int32_t v, float scale, void* d_table, int64_t ldt,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rows in 8-bit integers: for each row of x (device, n rows of d values, leading dimension
+ * ldx >= d, fp32 or bf16)
+ *   scale[r] = max |x_r| / 127 (rounded to fp32),  q[r][k] = the integer nearest x_r[k] / scale[r]
+ * (ties to the even one, within +-127). A row of zeros (or one whose scale is below fp32's smallest
+ * value) has scale 0 and q 0; a row with an infinity or NaN has scale NaN and q 0, so that its
+ * products are NaN. q: n x d with leading dimension ldq >= d (values between d and ldq are left as
+ * they are). n may be 0; n <= 2^40, d < 2^17 (GMM_E_UNSUPPORTED beyond). Needs no workspace. */
+int gmm_quantize_rows(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t dtype, int8_t* q,
+                      int64_t ldq, float* scale, void* stream);
+
+/* Product of rows in 8-bit integers with a scale for each row and each code (or output channel):
+ *   y[r][c] = (sum_k q[r][k] w[c][k]) * q_scale[r] * w_scale[c]
+ * q: n x d (leading dimension ldq >= d), w: v x d (ldw >= d), as gmm_quantize_rows writes them (all
+ * 256 values are allowed); q_scale n floats, w_scale v floats. The sums are exact; the sum, its
+ * product with q_scale and then with w_scale are rounded to fp32 and y (n x v, ldy >= v) to dtype
+ * (fp32 or bf16). y must not overlap the operands. With w the codes' quantised rows this is the
+ * head's logits in 8 bits, read by gmm_logits_score and gmm_beam_step. Any alignment; offsets are
+ * 64-bit. n may be 0; n <= 2^40, d < 2^17, v <= 2^22 (GMM_E_UNSUPPORTED beyond). The workspace
+ * (device, 256-byte aligned) has gmm_quantized_product_workspace_bytes bytes (0: invalid or
+ * unsupported sizes). */
+size_t gmm_quantized_product_workspace_bytes(int64_t n, int32_t d, int32_t v);
+int gmm_quantized_product(const int8_t* q, int64_t n, int32_t d, int64_t ldq, const float* q_scale,
+                          const int8_t* w, int32_t v, int64_t ldw, const float* w_scale, void* y,
+                          int64_t ldy, int32_t dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* A step of beam search over the logits of b searches with w beams each (device, b w rows of v
+ * values, leading dimension ldl >= v, fp32 or bf16; row s w + k is beam k of search s). With
+ * l = scale * x as in gmm_logits_score, the continuations of a search are
+ *   score(k, c) = scores[s][k] + ((l_c - max l) - log sum exp(l - max l))
+ * and the m best, best first, go to parent[s][j] = k, code[s][j] = c and score[s][j] (b x m each).
+ * Equal scores: the smaller k first, then the larger l, then the smaller c. A beam whose last code
+ * (last, b x w int32, may be NULL) equals end >= 0 has ended: its one continuation is itself, with
+ * code end and its score unchanged. A beam whose score is not finite is dead and has none; the
+ * rows of ended and dead beams are not read. A code whose logit is -inf or NaN, or whose score is -inf
+ * or NaN (every code of a row with a NaN or +inf), is no continuation; places left over hold
+ * -1, -1 and -inf. 1 <= w, m <= GMM_TOP_MAX, which may differ (a first step has w = 1); v <= 2^30.
+ * b may be 0. parent, code and score must not overlap scores and last. The workspace (device,
+ * 256-byte aligned) has gmm_beam_step_workspace_bytes bytes (0: invalid sizes). */
+size_t gmm_beam_step_workspace_bytes(int64_t b, int32_t w, int32_t v, int32_t m);
+int gmm_beam_step(const void* logits, int64_t b, int32_t w, int32_t v, int64_t ldl, int32_t dtype,
+                  const float* scores, const int32_t* last, int32_t end, int32_t m, float scale,
+                  int32_t* parent, int32_t* code, float* score, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Moves the states that belong to beams after gmm_beam_step: for o < outer (layers, for example),
+ *   out[o][s m + j] = state[o][s w + parent[s][j]]      (0 where parent is not in [0, w))
+ * with rows of row_bytes bytes (of any type and alignment), strides in bytes: out's rows must not
+ * overlap, state's may be the same row (stride 0). out may be state itself (w = m, the same
+ * strides): then rows that stay are not touched and each other one is read and written once; else it
+ * must not overlap state. parent: b x m int32. outer and b may be 0. */
+int gmm_beam_reorder(const void* state, int64_t outer, int64_t stride_outer, int64_t b, int32_t w,
+                     int64_t stride_row, int64_t row_bytes, const int32_t* parent, int32_t m,
+                     void* out, int64_t out_stride_outer, int64_t out_stride_row, void* stream);
+
+/* Balance of a router over e experts (or of the codes of an assignment over their lists). For gate
+ * logits (device, n rows of e values, leading dimension ldz >= e, fp32 or bf16), p = softmax of a
+ * row, and picks idx (n x m int32, as gmm_moe_layer and gmm_assign_topm write them):
+ *   counts[c] = picks of c,  totals[0] = rows with a pick,  totals[1] = picks
+ *   prob[c] = the mean of p_c over the rows with a pick
+ *   loss = e * sum_c counts[c] / totals[1] * prob[c]        (1 when balanced)
+ * Picks outside [0, e) are none; a row without a pick (padding) is left out altogether. No such row:
+ * loss and prob 0. norm[r] = (max z, log sum exp(z - max z)) for the gradient: (+inf, 0) for a row
+ * left out, (-inf, 0) for a row whose logits are all -inf (its p counts as 0), NaN for a row with a
+ * NaN or +inf, which makes loss and prob NaN. Sums are fp32 in a fixed order (bitwise reproducible).
+ * 1 <= m <= GMM_TOP_MAX; n may be 0; e <= 4096 and n m < 2^31 (GMM_E_UNSUPPORTED beyond). The
+ * workspace (device, 256-byte aligned) has gmm_balance_loss_workspace_bytes bytes (0: invalid
+ * or unsupported sizes). */
+size_t gmm_balance_loss_workspace_bytes(int64_t n, int32_t e, int32_t m);
+int gmm_balance_loss(const void* logits, int64_t n, int32_t e, int64_t ldz, int32_t dtype,
+                     const int32_t* idx, int32_t m, float* loss, int32_t* counts, int64_t* totals,
+                     float* prob, float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of gmm_balance_loss's loss with respect to the logits (counts have none), in their type:
+ *   dlogits[r][c] = g e / totals[0] * p_c (f_c - sum_c' f_c' p_c'),  f_c = counts[c] / totals[1]
+ * counts, totals and norm are what gmm_balance_loss wrote; g_loss (device, 1 float, may be NULL: 1)
+ * is the gradient that arrives at loss. Rows left out or with no logit above -inf get 0, rows with
+ * a NaN or +inf NaN. dlogits (leading dimension lddz >= e) may be the logits themselves with the same
+ * leading dimension. Needs no workspace. */
+int gmm_balance_loss_backward(const void* logits, int64_t n, int32_t e, int64_t ldz, int32_t dtype,
+                              const int32_t* counts, const int64_t* totals, const float* norm,
+                              const float* g_loss, void* dlogits, int64_t lddz, void* stream);
+
 /* Synchronises the stream and returns GMM_E_PARAMS if the last call that used
  * this workspace found invalid parameter values, GMM_OK otherwise, or
  * GMM_E_HIP if the synchronisation failed. */
