@@ -20,8 +20,18 @@
 namespace gmm {
 
 constexpr int BAL_MAX_EXPERTS = 4096;  // as the layer's
-constexpr int BAL_NT = 256, BAL_W = BAL_NT / 64;
-constexpr int BAL_PARTS = 256;         // workgroups of the pass over the rows
+constexpr int BAL_PARTS = 256;         // workgroups of the pass over the rows, at most
+
+struct BalancePart {
+    float mass;     // sum of p
+    int32_t picks;
+};
+
+// A join workgroup's share of the loss.
+struct BalanceSum {
+    float dot;      // sum of picks * mass over its experts
+    int32_t picks;
+};
 
 struct BalanceArgs {
     const void* z;
@@ -33,8 +43,10 @@ struct BalanceArgs {
     int32_t* counts;
     int64_t* totals;
     const float* g_loss;
-    float* part_p;      // [parts][e]
-    int32_t* part_c;    // [parts][e + 1]: counts, then rows
+    BalancePart* part;   // [parts][e]
+    int32_t* part_rows;  // [parts]
+    BalanceSum* sum;     // [join workgroups]
+    int32_t* done;       // join workgroups that have written theirs
 };
 
 // over groups of LPR lanes
@@ -59,42 +71,59 @@ struct RouterRow {
     static constexpr int VE = Vec<T>::VE, C = CV * VE;
     static __device__ __forceinline__ int at(int gl, int j) { return (j / VE * LPR + gl) * VE + j % VE; }
     float v[C];
-    __device__ __forceinline__ void load(const T* z, int e, int gl) {
+    static __device__ __forceinline__ void fetch(const T* z, int e, int gl, Raw16* r) {
 #pragma unroll
-        for (int q = 0; q < CV; ++q) {
-            const Raw16 r = load_vec(z, (int64_t)(q * LPR + gl) * VE, (int64_t)e);
+        for (int q = 0; q < CV; ++q) r[q] = load_vec(z, (int64_t)(q * LPR + gl) * VE, (int64_t)e);
+    }
+    __device__ __forceinline__ void take(const Raw16* r) {
 #pragma unroll
-            for (int k = 0; k < VE; ++k) v[q * VE + k] = Vec<T>::get(r, k);
-        }
+        for (int q = 0; q < CV; ++q)
+#pragma unroll
+            for (int k = 0; k < VE; ++k) v[q * VE + k] = Vec<T>::get(r[q], k);
     }
 };
 
-template <typename T, int LPR, int CV>
-__global__ __launch_bounds__(BAL_NT) void k_balance_rows(BalanceArgs p) {
+template <typename T, int LPR, int CV, int NT>
+__global__ __launch_bounds__(NT) void k_balance_rows(BalanceArgs p) {
     using Row = RouterRow<T, LPR, CV>;
-    constexpr int C = Row::C, RPW = 64 / LPR;
+    constexpr int C = Row::C, RPW = 64 / LPR, W = NT / 64;
     extern __shared__ float sums[];  // [e], then counts [e + 1]
     int* cnt = (int*)(sums + p.e);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int gl = lane % LPR, grp = lane / LPR;
-    for (int c = tid; c <= p.e; c += BAL_NT) cnt[c] = 0;
+    if (blockIdx.x == 0 && tid == 0) *p.done = 0;  // for the kernel after this one
+    for (int c = tid; c <= p.e; c += NT) cnt[c] = 0;
     __syncthreads();
     float acc[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) acc[j] = 0.f;
-    const int64_t step = (int64_t)p.parts * BAL_W * RPW;
-    for (int64_t r0 = ((int64_t)blockIdx.x * BAL_W + wave) * RPW; r0 < p.n; r0 += step) {
+    const int64_t step = (int64_t)p.parts * W * RPW;
+    const uint64_t mine = (LPR == 64 ? ~uint64_t(0) : (uint64_t(1) << (LPR & 63)) - 1) << (grp * LPR);
+    struct Next {
+        Raw16 z[CV];
+        int pick;
+    };
+    auto fetch = [&](int64_t r0) {
+        const int64_t row = r0 + grp < p.n ? r0 + grp : p.n - 1;
+        Next x;
+        x.pick = gl < p.m ? p.idx[row * p.m + gl] : -1;
+        Row::fetch((const T*)p.z + row * p.ldz, p.e, gl, x.z);
+        return x;
+    };
+    int64_t r0 = ((int64_t)blockIdx.x * W + wave) * RPW;
+    Next next;
+    if (r0 < p.n) next = fetch(r0);
+    for (; r0 < p.n; r0 += step) {
         const int64_t row = r0 + grp;
         const bool in = row < p.n;
-        int pick = -1;
-        if (in && gl < p.m) pick = p.idx[row * p.m + gl];
+        Row x;
+        x.take(next.z);
+        const int pick = in ? next.pick : -1;
+        if (r0 + step < p.n) next = fetch(r0 + step);
         const bool picked = pick >= 0 && pick < p.e;
-        const uint64_t mine = ((LPR == 64 ? ~uint64_t(0) : (uint64_t(1) << (LPR & 63)) - 1)) << (grp * LPR);
         const bool live = (__builtin_amdgcn_ballot_w64(picked) & mine) != 0;
         if (picked) atomicAdd(&cnt[pick], 1);
         if (gl == 0 && live) atomicAdd(&cnt[p.e], 1);
-        Row x;
-        x.load((const T*)p.z + (in ? row : 0) * p.ldz, p.e, gl);
         float m = -3.402823466e38f, s = 0.f;
 #pragma unroll
         for (int j = 0; j < C; ++j) m = fmaxf(m, x.v[j]);
@@ -122,7 +151,7 @@ __global__ __launch_bounds__(BAL_NT) void k_balance_rows(BalanceArgs p) {
         if (LPR < 32) acc[j] += __shfl_xor(acc[j], 16);
         if (LPR < 64) acc[j] += __shfl_xor(acc[j], 32);
     }
-    for (int w = 0; w < BAL_W; ++w) {
+    for (int w = 0; w < W; ++w) {
         if (w == wave && grp == 0) {
 #pragma unroll
             for (int j = 0; j < C; ++j) {
@@ -132,82 +161,116 @@ __global__ __launch_bounds__(BAL_NT) void k_balance_rows(BalanceArgs p) {
         }
         __syncthreads();
     }
-    for (int c = tid; c < p.e; c += BAL_NT) p.part_p[(int64_t)blockIdx.x * p.e + c] = sums[c];
-    for (int c = tid; c <= p.e; c += BAL_NT) p.part_c[(int64_t)blockIdx.x * (p.e + 1) + c] = cnt[c];
+    for (int c = tid; c < p.e; c += NT)
+        p.part[(int64_t)blockIdx.x * p.e + c] = BalancePart{sums[c], cnt[c]};
+    if (tid == 0) p.part_rows[blockIdx.x] = cnt[p.e];
 }
 
-// One workgroup adds the parts: 16 groups of them side by side, then those in order.
-constexpr int BJ_NT = 1024, BJ_G = 16, BJ_C = BJ_NT / BJ_G;
+// A workgroup adds the parts of 64 experts, 16 groups of parts side by side, then the groups in
+// order. The one that comes last adds the workgroups' shares of the loss, in their order.
+constexpr int BJ_G = 16, BJ_NT = 64 * BJ_G;
 __global__ __launch_bounds__(BJ_NT) void k_balance_join(BalanceArgs p) {
-    __shared__ float sp[BJ_G][BJ_C];
-    __shared__ int sc[BJ_G][BJ_C];
-    const int tid = threadIdx.x, col = tid % BJ_C, g = tid / BJ_C;  // a group is a wave
+    __shared__ BalancePart sh[BJ_G][64];
+    const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
     const int a = p.parts * g / BJ_G, z = p.parts * (g + 1) / BJ_G;
-    int rows = 0;
-    for (int t = col; t < p.parts; t += BJ_C) rows += p.part_c[(int64_t)t * (p.e + 1) + p.e];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) rows += __shfl_xor(rows, o);
-    float dot = 0.f;         // sum of picks * mass over this thread's experts
-    long long total = 0;
-    for (int c0 = 0; c0 < p.e; c0 += BJ_C) {
-        const int c = c0 + col;
-        float s = 0.f;
-        int n = 0;
-        if (c < p.e) {
-#pragma unroll 8
-            for (int t = a; t < z; ++t) {
-                s += p.part_p[(int64_t)t * p.e + c];
-                n += p.part_c[(int64_t)t * (p.e + 1) + c];
-            }
+    float s = 0.f;
+    int n = 0, rows = 0;
+    if (c < p.e) {
+#pragma unroll 16
+        for (int t = a; t < z; ++t) {
+            const BalancePart q = p.part[(int64_t)t * p.e + c];
+            s += q.mass;
+            n += q.picks;
         }
-        sp[g][col] = s;
-        sc[g][col] = n;
-        __syncthreads();
-        if (g == 0 && c < p.e) {
-            for (int q = 1; q < BJ_G; ++q) {
-                s += sp[q][col];
-                n += sc[q][col];
-            }
-            p.counts[c] = n;
-            p.prob[c] = s / (float)(rows > 0 ? rows : 1);
-            total += n;
-            dot = fmaf((float)n, s, dot);
-        }
-        __syncthreads();
     }
     if (g == 0) {
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
-        dot = wave_sum(dot);
-        if (col == 0) {
-            p.totals[0] = rows;
-            p.totals[1] = total;
-            p.loss[0] = rows > 0 ? (float)p.e * (dot / (float)total / (float)rows) : 0.f;
+        for (int t = lane; t < BAL_PARTS; t += 64) rows += t < p.parts ? p.part_rows[t] : 0;
+    }
+    sh[g][lane] = BalancePart{s, n};
+    __syncthreads();
+    if (g != 0) return;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) rows += __shfl_xor(rows, o);
+#pragma unroll
+    for (int q = 1; q < BJ_G; ++q) {
+        s += sh[q][lane].mass;
+        n += sh[q][lane].picks;
+    }
+    if (c < p.e) {
+        p.counts[c] = n;
+        p.prob[c] = s / (float)(rows > 0 ? rows : 1);
+    }
+    float dot = wave_sum(c < p.e ? (float)n * s : 0.f);
+    int total = n;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
+    if (gridDim.x > 1) {
+        int before = 0;
+        if (lane == 0) {
+            BalanceSum* mine = p.sum + blockIdx.x;
+            __hip_atomic_store(&mine->dot, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&mine->picks, total, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            before = __hip_atomic_fetch_add(p.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
         }
+        if (__builtin_amdgcn_readfirstlane(before) + 1 != (int)gridDim.x) return;
+        dot = 0.f;
+        total = 0;
+        if (lane < (int)gridDim.x) {  // at most 64 workgroups
+            BalanceSum* theirs = p.sum + lane;
+            dot = __hip_atomic_load(&theirs->dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            total = __hip_atomic_load(&theirs->picks, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        dot = wave_sum(dot);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
+    }
+    if (lane == 0) {
+        p.totals[0] = rows;
+        p.totals[1] = total;  // below 2^31, as n m is
+        p.loss[0] = rows > 0 ? (float)p.e * (dot / (float)total / (float)rows) : 0.f;
     }
 }
 
+constexpr int BG_W = 4;
 template <typename T, int LPR, int CV>
-__global__ __launch_bounds__(BAL_NT) void k_balance_grad(BalanceArgs p) {
+__global__ __launch_bounds__(64 * BG_W) void k_balance_grad(BalanceArgs p) {
     using Row = RouterRow<T, LPR, CV>;
     constexpr int C = Row::C, RPW = 64 / LPR, VE = Vec<T>::VE;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int gl = lane % LPR, grp = lane / LPR;
-    const float rows = (float)p.totals[0], picks = (float)p.totals[1];
+    const float rows = (float)p.totals[0], inv = 1.f / fmaxf((float)p.totals[1], 1.f);
     const float by = (p.g_loss ? p.g_loss[0] : 1.f) * ((float)p.e / fmaxf(rows, 1.f));
     float f[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
         const int c = Row::at(gl, j);
-        f[j] = c < p.e ? (float)p.counts[c] / fmaxf(picks, 1.f) : 0.f;
+        f[j] = c < p.e ? (float)p.counts[c] * inv : 0.f;
     }
-    for (int64_t r0 = ((int64_t)blockIdx.x * BAL_W + wave) * RPW; r0 < p.n;
-         r0 += (int64_t)gridDim.x * BAL_W * RPW) {
+    struct Next {
+        Raw16 z[CV];
+        float m, logs;
+    };
+    auto fetch = [&](int64_t r0) {
+        const int64_t row = r0 + grp < p.n ? r0 + grp : p.n - 1;
+        Next x;
+        x.m = p.norm[2 * row];
+        x.logs = p.norm[2 * row + 1];
+        Row::fetch((const T*)p.z + row * p.ldz, p.e, gl, x.z);
+        return x;
+    };
+    // p.dz may be p.z: the rows fetched ahead are other ones than those written
+    const int64_t step = (int64_t)gridDim.x * BG_W * RPW;
+    int64_t r0 = ((int64_t)blockIdx.x * BG_W + wave) * RPW;
+    Next next;
+    if (r0 < p.n) next = fetch(r0);
+    for (; r0 < p.n; r0 += step) {
         const int64_t row = r0 + grp;
-        const bool in = row < p.n;
-        const float m = in ? p.norm[2 * row] : INFINITY, logs = in ? p.norm[2 * row + 1] : 0.f;
         Row x;
-        x.load((const T*)p.z + (in ? row : 0) * p.ldz, p.e, gl);
+        x.take(next.z);
+        const float m = next.m, logs = next.logs;
+        if (r0 + step < p.n) next = fetch(r0 + step);
         const bool off = m == INFINITY || m == -INFINITY;  // left out, or no logit above -inf
         float s = 0.f;
 #pragma unroll
@@ -216,17 +279,18 @@ __global__ __launch_bounds__(BAL_NT) void k_balance_grad(BalanceArgs p) {
             s = fmaf(f[j], x.v[j], s);
         }
         s = group_reduce_sum<LPR>(s);
-        if (!in) continue;
+        if (row >= p.n) continue;
         T* out = (T*)p.dz + row * p.lddz;
 #pragma unroll
         for (int q = 0; q < CV; ++q) {
             const int64_t i = (int64_t)(q * LPR + gl) * VE;
-            Raw16 o = {{0u, 0u, 0u, 0u}};
+            float w[VE];
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
                 const int j = q * VE + k;
-                Vec<T>::set(o, k, off ? 0.f : by * (x.v[j] * (f[j] - s)));
+                w[k] = off ? 0.f : by * (x.v[j] * (f[j] - s));
             }
+            const Raw16 o = pack16<T>(w);
             if (i + VE <= p.e) {
                 *reinterpret_cast<Raw16*>(out + i) = o;
             } else {
@@ -267,9 +331,11 @@ static hipError_t balance(const BalanceArgs& a, hipStream_t st) {
     with_row<T>(a.e, [&](auto l, auto c) {
         constexpr int LPR = decltype(l)::value, CV = decltype(c)::value;
         const size_t lds = (size_t)(2 * a.e + 1) * 4;
-        hipLaunchKernelGGL((k_balance_rows<T, LPR, CV>), dim3(a.parts), dim3(BAL_NT), lds, st, a);
+        // sixteen waves while their registers suffice
+        constexpr int NT = CV == 1 ? 1024 : CV <= 4 ? 512 : 256;
+        hipLaunchKernelGGL((k_balance_rows<T, LPR, CV, NT>), dim3(a.parts), dim3(NT), lds, st, a);
     });
-    hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(BJ_NT), 0, st, a);
+    hipLaunchKernelGGL(k_balance_join, dim3((a.e + 63) / 64), dim3(BJ_NT), 0, st, a);
     return hipGetLastError();
 }
 
@@ -277,9 +343,9 @@ template <typename T>
 static hipError_t balance_grad(const BalanceArgs& a, hipStream_t st) {
     with_row<T>(a.e, [&](auto l, auto c) {
         constexpr int LPR = decltype(l)::value, CV = decltype(c)::value;
-        const int64_t per = BAL_W * (64 / LPR), blocks = (a.n + per - 1) / per;
-        hipLaunchKernelGGL((k_balance_grad<T, LPR, CV>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)),
-                           dim3(BAL_NT), 0, st, a);
+        const int64_t per = BG_W * (64 / LPR), blocks = (a.n + per - 1) / per;
+        hipLaunchKernelGGL((k_balance_grad<T, LPR, CV>), dim3((unsigned)(blocks < 2048 ? blocks : 2048)),
+                           dim3(64 * BG_W), 0, st, a);
     });
     return hipGetLastError();
 }
@@ -293,7 +359,7 @@ extern "C" {
 size_t gmm_balance_loss_workspace_bytes(int64_t n, int32_t e, int32_t m) {
     if (!balance_ok(n, e, m) || !balance_fits(n, e, m)) return 0;
     const size_t parts = balance_parts(n);
-    return bal_up(parts * e * 4) + bal_up(parts * (e + 1) * 4);
+    return bal_up(parts * e * sizeof(BalancePart)) + bal_up(parts * 4) + bal_up(64 * sizeof(BalanceSum)) + 256;
 }
 
 int gmm_balance_loss(const void* logits, int64_t n, int32_t e, int64_t ldz, int32_t dtype,
@@ -319,8 +385,13 @@ int gmm_balance_loss(const void* logits, int64_t n, int32_t e, int64_t ldz, int3
     a.prob = prob;
     a.counts = counts;
     a.totals = totals;
-    a.part_p = (float*)workspace;
-    a.part_c = (int32_t*)((char*)workspace + bal_up((size_t)a.parts * e * 4));
+    char* ws = (char*)workspace;
+    a.part = (BalancePart*)ws;
+    ws += bal_up((size_t)a.parts * e * sizeof(BalancePart));
+    a.part_rows = (int32_t*)ws;
+    ws += bal_up((size_t)a.parts * 4);
+    a.sum = (BalanceSum*)ws;
+    a.done = (int32_t*)(ws + bal_up(64 * sizeof(BalanceSum)));
     const hipError_t err = dtype == GMM_F32 ? balance<float>(a, (hipStream_t)stream)
                                             : balance<uint16_t>(a, (hipStream_t)stream);
     return err == hipSuccess ? GMM_OK : GMM_E_HIP;

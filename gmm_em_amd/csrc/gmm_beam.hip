@@ -5,7 +5,7 @@
 //
 // A beam's m best codes are those of its row of logits (gmm_score.hip: one pass, the rows of dead
 // and ended beams are not read); within a beam the order of the scores is that of the
-// logits, so the m best of all are a merge of w sorted lists, made by one wave with a beam in each lane.
+// logits, so the m best of all are a merge of w sorted lists, where each entry counts those before it.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -29,55 +29,58 @@ struct BeamArgs {
     float* score;
 };
 
-__global__ __launch_bounds__(64) void k_beam_join(BeamArgs p) {
-    __shared__ float sv[TOP_MAX * TOP_MAX];
-    __shared__ int si[TOP_MAX * TOP_MAX];
-    const int lane = threadIdx.x;
+// A thread per continuation of the search's w lists finds its place: the entries before it in its
+// own list, and in each other list those that are larger (or equal, in an earlier beam's).
+constexpr int BJ_NT = TOP_MAX * TOP_MAX;
+__global__ __launch_bounds__(BJ_NT) void k_beam_join(BeamArgs p) {
+    __shared__ __align__(16) uint32_t key[TOP_MAX][TOP_MAX];  // 0: none
+    __shared__ int parent[TOP_MAX], codes[TOP_MAX];
+    __shared__ float scores[TOP_MAX];
+    const int tid = threadIdx.x, w = tid / TOP_MAX, j = tid % TOP_MAX;
+    const bool in = w < p.w && j < p.per;
     for (int64_t b = blockIdx.x; b < p.b; b += gridDim.x) {
-        const int64_t r0 = b * p.w;
-        for (int e = lane; e < p.w * p.per; e += 64) {
-            const int w = e / p.per, j = e - w * p.per;
-            const int64_t row = r0 + w;
-            float v = -INFINITY;
-            int i = -1;
-            if (beam_alive(p.scores, row)) {
-                if (beam_ended(p.last, p.end, row)) {
-                    if (j == 0) {
-                        v = p.scores[row];
-                        i = p.end;
-                    }
-                } else {
-                    i = p.top_idx[row * p.per + j];
-                    if (i >= 0) v = p.scores[row] + p.top_logprob[row * p.per + j];
-                }
+        float score = -INFINITY;
+        int code = -1;
+        if (in) {
+            const int64_t row = b * p.w + w, e = row * p.per + j;
+            // unwritten for beams that are dead or have ended
+            const int i = p.top_idx[e];
+            const float lp = p.top_logprob[e], s = p.scores[row];
+            const bool ended = beam_ended(p.last, p.end, row);
+            if (fabsf(s) < INFINITY && (ended ? j == 0 : i >= 0)) {
+                score = ended ? s : s + lp;
+                code = ended ? p.end : i;
             }
-            sv[e] = v > -INFINITY ? v : -INFINITY;  // NaN is no continuation
-            si[e] = i;
+        }
+        const uint32_t mine = score > -INFINITY ? order_of(score) : 0;  // NaN is no continuation
+        key[w][j] = mine;
+        if (tid < TOP_MAX) {
+            parent[tid] = codes[tid] = -1;
+            scores[tid] = -INFINITY;
         }
         __syncthreads();
-        int at = 0;  // this lane's beam: entries taken
-        float head = lane < p.w ? sv[lane * p.per] : -INFINITY;
-        int parent = -1, code = -1;
-        float score = -INFINITY;
-        for (int j = 0; j < p.m; ++j) {
-            const float best = wave_max(head);
-            if (best == -INFINITY) break;
-            const int w = wave_min(head == best ? lane : 64);
-            const int c = __builtin_amdgcn_readlane(lane < p.w && at < p.per ? si[lane * p.per + at] : -1, w);
-            if (lane == j) {
-                parent = w;
-                code = c;
-                score = best;
+        int rank = j;
+#pragma unroll 4
+        for (int q = 0; q < p.w; ++q) {
+            const uint32_t least = q < w ? mine - 1 : mine;  // mine > 0 where it counts
+            int more = 0;
+#pragma unroll
+            for (int k = 0; k < TOP_MAX; k += 4) {
+                const uint4 o = *(const uint4*)&key[q][k];
+                more += (o.x > least) + (o.y > least) + (o.z > least) + (o.w > least);
             }
-            if (lane == w) {
-                ++at;
-                head = at < p.per ? sv[lane * p.per + at] : -INFINITY;
-            }
+            rank += q == w ? 0 : more;
         }
-        if (lane < p.m) {
-            p.parent[b * p.m + lane] = parent;
-            p.code[b * p.m + lane] = code;
-            p.score[b * p.m + lane] = score;
+        if (mine > 0 && rank < p.m) {
+            parent[rank] = w;
+            codes[rank] = code;
+            scores[rank] = score;
+        }
+        __syncthreads();
+        if (tid < p.m) {
+            p.parent[b * p.m + tid] = parent[tid];
+            p.code[b * p.m + tid] = codes[tid];
+            p.score[b * p.m + tid] = scores[tid];
         }
         __syncthreads();
     }
@@ -229,7 +232,7 @@ int gmm_beam_step(const void* logits, int64_t b, int32_t w, int32_t v, int64_t l
     if (launch_score(s, dtype, ws + q.o_score, st) != hipSuccess) return GMM_E_HIP;
     const BeamArgs a{scores, last, s.top_idx, s.top_logprob, b, w, m, q.per, end, parent, code, score};
     const int64_t most = (int64_t)1 << 20;
-    hipLaunchKernelGGL(k_beam_join, dim3((unsigned)(b < most ? b : most)), dim3(64), 0, st, a);
+    hipLaunchKernelGGL(k_beam_join, dim3((unsigned)(b < most ? b : most)), dim3(BJ_NT), 0, st, a);
     return hipGetLastError() == hipSuccess ? GMM_OK : GMM_E_HIP;
 }
 

@@ -5,14 +5,16 @@
 // The forward call is a gather of whole rows: a wave per row (or part of a long one).
 //
 // Gradient: the rows are sorted by code (stable, so that every sum has one order), cut
-// into segments of 64 and summed segment by segment: the work of a segment does not depend
+// into segments of 8 to 64 and summed segment by segment: the work of a segment does not depend
 // on how often its codes occur. A run of one code that lies inside a segment is written
 // from there; what a run leaves in each of several segments goes to the workspace and is
 // added in order by k_embed_join. The sort is by digits of the code, lowest first:
 //   k_embed_count: per tile of rows, how often each digit occurs
 //   k_embed_place: the place of a tile's digits from everyone's counts, then its rows in
 //                  order (one ballot per bit ranks 64 rows among those of the same digit)
-// Codes that no row has are told by a bitmap and set to 0 by waves of the summing kernel.
+// Codes that no row has are found in the sorted keys and set to 0 by waves of the summing
+// kernel. Up to 1024 rows take one launch instead (k_embed_few): the first row of a code adds
+// the others.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -88,18 +90,17 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs p) {
         for (int u = 0; u < EMB_U; ++u) {
             const int k = k0 + u * 64 * VE;
             if (k >= p.d) continue;
-            Raw16 o = {{0u, 0u, 0u, 0u}};
+            float o[VE];
 #pragma unroll
-            for (int j = 0; j < VE; ++j)
-                Vec<T>::set(o, j, there ? Vec<T>::get(r[u], j) * p.scale : none);
-            row_put(y, whole<VE>(k, p.d), p.d, o);
+            for (int j = 0; j < VE; ++j) o[j] = there ? Vec<T>::get(r[u], j) * p.scale : none;
+            row_put(y, whole<VE>(k, p.d), p.d, pack16<T>(o));
         }
     }
 }
 
 // ---- the sort of the rows by code
 
-constexpr int ES_BITS = 9, ES_BINS = 1 << ES_BITS;  // a digit
+constexpr int ES_BITS = 10, ES_BINS = 1 << ES_BITS;  // a digit, at most
 constexpr int ES_NT = 1024, ES_W = ES_NT / 64;
 constexpr int ES_MAX_TILES = 256;
 
@@ -107,10 +108,9 @@ struct SortArgs {
     const int32_t* codes;            // of the caller (first digit), else keys
     const uint32_t *key_in, *row_in;
     uint32_t *key, *row;             // sorted by this digit and the ones before
-    uint32_t* mat;                   // [tiles][ES_BINS]
-    uint32_t* present;               // a bit for each code that occurs
+    uint32_t* mat;                   // [tiles][2^bits]
     int64_t n, tile;                 // tile: rows per workgroup, a multiple of ES_NT
-    int32_t v, tiles, shift, words;
+    int32_t v, tiles, shift, bits;
 };
 
 // Sort key of row i: its code, or v where that is none (those rows come last).
@@ -122,48 +122,43 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& p, int64_t i) {
 
 __global__ __launch_bounds__(ES_NT) void k_embed_count(SortArgs p) {
     __shared__ uint32_t h[ES_BINS];
-    const int tid = threadIdx.x;
-    if (p.codes)
-        for (int64_t j = (int64_t)blockIdx.x * ES_NT + tid; j < p.words; j += (int64_t)gridDim.x * ES_NT)
-            p.present[j] = 0;
-    if (tid < ES_BINS) h[tid] = 0;
+    const int tid = threadIdx.x, bins = 1 << p.bits;
+    h[tid] = 0;
     __syncthreads();
     const int64_t b = blockIdx.x * p.tile, e = b + p.tile < p.n ? b + p.tile : p.n;
-    for (int64_t i = b + tid; i < e; i += ES_NT)
-        atomicAdd(&h[(sort_key(p, i) >> p.shift) & (ES_BINS - 1)], 1u);
+    for (int64_t i = b + tid; i < e; i += ES_NT) atomicAdd(&h[(sort_key(p, i) >> p.shift) & (bins - 1)], 1u);
     __syncthreads();
-    if (tid < ES_BINS) p.mat[(int64_t)blockIdx.x * ES_BINS + tid] = h[tid];
+    if (tid < bins) p.mat[(int64_t)blockIdx.x * bins + tid] = h[tid];
 }
 
 __global__ __launch_bounds__(ES_NT) void k_embed_place(SortArgs p) {
     __shared__ uint32_t at[ES_W][ES_BINS];  // each wave's next place for a digit
-    __shared__ uint32_t tot[2][ES_BINS], bef[2][ES_BINS], sums[ES_BINS / 64];
+    __shared__ uint32_t tot[ES_NT], bef[ES_NT], sums[ES_BINS / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int t0 = blockIdx.x;
+    const int t0 = blockIdx.x, bins = 1 << p.bits, per_bin = ES_NT >> p.bits;
     // how many rows of each digit there are, and how many in the tiles before
     {
-        const int bin = tid & (ES_BINS - 1), half = tid >> ES_BITS;
+        const int bin = tid & (bins - 1);
         uint32_t all = 0, before = 0;
 #pragma unroll 8
-        for (int t = half; t < p.tiles; t += ES_NT / ES_BINS) {
-            const uint32_t c = p.mat[(int64_t)t * ES_BINS + bin];
+        for (int t = tid >> p.bits; t < p.tiles; t += per_bin) {
+            const uint32_t c = p.mat[(int64_t)t * bins + bin];
             all += c;
             before += t < t0 ? c : 0;
         }
-        tot[half][bin] = all;
-        bef[half][bin] = before;
+        tot[tid] = all;
+        bef[tid] = before;
     }
-    for (int j = tid; j < ES_W * ES_BINS; j += ES_NT) (&at[0][0])[j] = 0;
-    __syncthreads();
     // each wave counts its own stretch of the tile
+    for (int j = lane; j < bins; j += 64) at[wave][j] = 0;
     const int64_t per = p.tile / ES_W;
     const int64_t b = blockIdx.x * p.tile + wave * per;
     const int64_t e = b + per < p.n ? b + per : p.n;
-    for (int64_t i = b + lane; i < e; i += 64)
-        atomicAdd(&at[wave][(sort_key(p, i) >> p.shift) & (ES_BINS - 1)], 1u);
+    for (int64_t i = b + lane; i < e; i += 64) atomicAdd(&at[wave][(sort_key(p, i) >> p.shift) & (bins - 1)], 1u);
+    __syncthreads();
     uint32_t mine = 0, scan = 0;
-    if (tid < ES_BINS) {
-        mine = tot[0][tid] + tot[1][tid];
+    if (tid < bins) {
+        for (int q = 0; q < per_bin; ++q) mine += tot[q * bins + tid];
         scan = mine;  // prefix over the wave's 64 digits
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -173,8 +168,9 @@ __global__ __launch_bounds__(ES_NT) void k_embed_place(SortArgs p) {
         if (lane == 63) sums[wave] = scan;
     }
     __syncthreads();
-    if (tid < ES_BINS) {
-        uint32_t run = scan - mine + bef[0][tid] + bef[1][tid];
+    if (tid < bins) {
+        uint32_t run = scan - mine;
+        for (int q = 0; q < per_bin; ++q) run += bef[q * bins + tid];
         for (int w = 0; w < wave; ++w) run += sums[w];
         for (int w = 0; w < ES_W; ++w) {
             const uint32_t c = at[w][tid];
@@ -189,10 +185,9 @@ __global__ __launch_bounds__(ES_NT) void k_embed_place(SortArgs p) {
         const bool in = i < e;
         const uint32_t key = in ? sort_key(p, i) : 0;
         const uint32_t row = in ? (p.codes ? (uint32_t)i : p.row_in[i]) : 0;
-        const uint32_t dig = (key >> p.shift) & (ES_BINS - 1);
+        const uint32_t dig = (key >> p.shift) & (bins - 1);
         uint64_t same = __builtin_amdgcn_ballot_w64(in);
-#pragma unroll
-        for (int bit = 0; bit < ES_BITS; ++bit) {
+        for (int bit = 0; bit < p.bits; ++bit) {
             const bool set = (dig >> bit) & 1;
             const uint64_t m = __builtin_amdgcn_ballot_w64(set);
             same &= set ? m : ~m;
@@ -204,183 +199,312 @@ __global__ __launch_bounds__(ES_NT) void k_embed_place(SortArgs p) {
             p.row[to] = row;
             // one wave: its LDS accesses complete in order, so the reads above come first
             if ((same & below) == 0) at[wave][dig] = first + __popcll(same);
-            if (p.codes && key < (uint32_t)p.v) {
-                const uint32_t bit = 1u << (key & 31);
-                uint32_t* word = p.present + (key >> 5);
-                if (!(__hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & bit))
-                    atomicOr(word, bit);
-            }
         }
     }
 }
 
 // ---- the sums
 
-constexpr int EG_SEG = 64;  // sorted rows of a segment: one per lane
 constexpr int EG_U = 8;     // rows in flight
 
 struct EmbedGradArgs {
     const void* g;
     void* out;
-    const uint32_t *key, *row, *present;
+    const int32_t* codes;
+    const uint32_t *key, *row;
     float* part;  // [segments][2][dp]: the segment's share of a run from before, and of one that goes on
     int64_t n, ldg, ldt, segs;
-    int32_t v, d, dp, cols;  // cols: blocks of 64 VE dims
+    int32_t seg;          // sorted rows of a segment, at most one per lane
+    int32_t v, d, dp;
+    int32_t cols, width;  // a row's blocks of `width` vectors, one per lane
     float scale;
 };
 
 template <typename T>
 __device__ __forceinline__ void embed_out(const EmbedGradArgs& p, uint32_t code, int k, const float* acc) {
     constexpr int VE = Vec<T>::VE;
-    Raw16 o = {{0u, 0u, 0u, 0u}};
+    float o[VE];
 #pragma unroll
-    for (int j = 0; j < VE; ++j) Vec<T>::set(o, j, acc[j] * p.scale);
-    row_put((T*)p.out + code * p.ldt, k, p.d, o);
+    for (int j = 0; j < VE; ++j) o[j] = acc[j] * p.scale;
+    row_put((T*)p.out + code * p.ldt, k, p.d, pack16<T>(o));
+}
+
+// A row of zeros, by a wave.
+template <typename T>
+__device__ __forceinline__ void embed_zero_row(const EmbedGradArgs& p, int64_t code, int lane) {
+    constexpr int VE = Vec<T>::VE;
+    T* y = (T*)p.out + code * p.ldt;
+    for (int k = lane * VE; k < p.d; k += 64 * VE) row_put(y, whole<VE>(k, p.d), p.d, Raw16{{0u, 0u, 0u, 0u}});
+}
+
+// acc += EG_U rows of this lane's VE dims; rows from `cnt` on add nothing.
+template <typename T, typename F>
+__device__ __forceinline__ void embed_rows(const EmbedGradArgs& p, bool has, int k, int j0, int cnt, F row_of,
+                                           Raw16* r) {
+#pragma unroll
+    for (int u = 0; u < EG_U; ++u) {
+        const uint32_t at = row_of(j0 + u < cnt ? j0 + u : cnt - 1);
+        r[u] = Raw16{{0u, 0u, 0u, 0u}};
+        if (has) r[u] = row_get((const T*)p.g + (int64_t)at * p.ldg, k, p.d);
+    }
 }
 
 template <typename T>
 __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs p) {
     constexpr int VE = Vec<T>::VE;
     const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t work = p.segs * p.cols, zero = (p.v + 63) / 64;
-    for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < work + zero;
-         item += (int64_t)gridDim.x * 4) {
+    for (int64_t item = (int64_t)blockIdx.x * 4 + wave; item < work + zero; item += (int64_t)gridDim.x * 4) {
         if (item >= work) {
-            // 64 codes: those that no row has
-            const int c0 = (int)(item - work) * 64;
-            const int c = c0 + lane;
-            const bool none = c < p.v && !((p.present[c >> 5] >> (c & 31)) & 1);
-            uint64_t left = __builtin_amdgcn_ballot_w64(none);
-            const Raw16 zeros = {{0u, 0u, 0u, 0u}};
-            while (left) {
-                const int j = __builtin_ctzll(left);
-                left &= left - 1;
-                T* y = (T*)p.out + (int64_t)(c0 + j) * p.ldt;
-                for (int k = lane * VE; k < p.d; k += 64 * VE) row_put(y, whole<VE>(k, p.d), p.d, zeros);
+            // 64 codes: those that the sorted keys do not hold
+            const int64_t c0 = (item - work) * 64;
+            const uint32_t c = (uint32_t)(c0 + lane);
+            int64_t lo = 0, hi = p.n;  // the first key not below c lies in [lo, hi]
+            while (__builtin_amdgcn_ballot_w64(lo < hi)) {
+                const int64_t mid = lo + (hi - lo) / 2;
+                if (lo < hi) {
+                    if (p.key[mid] < c)
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
             }
+            const bool none = c < (uint32_t)p.v && (lo == p.n || p.key[lo] != c);
+            for (uint64_t left = __builtin_amdgcn_ballot_w64(none); left; left &= left - 1)
+                embed_zero_row<T>(p, c0 + __builtin_ctzll(left), lane);
             continue;
         }
         const int64_t seg = item / p.cols;
-        const int kc = (int)(item - seg * p.cols) * 64 * VE + lane * VE;
-        const bool has = kc < p.d;
+        const int kc = ((int)(item - seg * p.cols) * p.width + lane) * VE;
+        const bool has = lane < p.width && kc < p.d;
         const int k = whole<VE>(kc, p.d);
-        const int64_t i0 = seg * EG_SEG;
-        const bool in = i0 + lane < p.n;
+        const int64_t i0 = seg * p.seg;
+        const bool in = lane < p.seg && i0 + lane < p.n;
         const uint32_t key = in ? p.key[i0 + lane] : (uint32_t)p.v;
         const uint32_t row = in ? p.row[i0 + lane] : 0;
         const uint32_t before = i0 > 0 ? p.key[i0 - 1] : 0xffffffffu;
-        const uint32_t after = i0 + EG_SEG < p.n ? p.key[i0 + EG_SEG] : 0xffffffffu;
+        const uint32_t after = i0 + p.seg < p.n ? p.key[i0 + p.seg] : 0xffffffffu;
         const int cnt = __popcll(__builtin_amdgcn_ballot_w64(key < (uint32_t)p.v));
+        auto key_at = [&](int j) { return (uint32_t)__builtin_amdgcn_readlane((int)key, j); };
+        auto row_at = [&](int j) { return (uint32_t)__builtin_amdgcn_readlane((int)row, j); };
         float acc[VE];
 #pragma unroll
         for (int j = 0; j < VE; ++j) acc[j] = 0.f;
-        bool whole_run = true;  // the run began in this segment
+        bool began = key_at(0) != before;  // the run began in this segment
         for (int j0 = 0; j0 < cnt; j0 += EG_U) {
             Raw16 r[EG_U];
-#pragma unroll
-            for (int u = 0; u < EG_U; ++u) {
-                const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)row, j0 + u < cnt ? j0 + u : cnt - 1);
-                r[u] = Raw16{{0u, 0u, 0u, 0u}};
-                if (has) r[u] = row_get((const T*)p.g + (int64_t)at * p.ldg, k, p.d);
-            }
+            embed_rows<T>(p, has, k, j0, cnt, row_at, r);
 #pragma unroll
             for (int u = 0; u < EG_U; ++u) {
                 const int j = j0 + u;
                 if (j >= cnt) break;
-                const uint32_t code = (uint32_t)__builtin_amdgcn_readlane((int)key, j);
-                const uint32_t next = j + 1 < EG_SEG
-                                          ? (uint32_t)__builtin_amdgcn_readlane((int)key, j + 1 < 64 ? j + 1 : 63)
-                                          : after;
-                if (j == 0) whole_run = code != before;
 #pragma unroll
                 for (int q = 0; q < VE; ++q) acc[q] += Vec<T>::get(r[u], q);
-                if (next == code && j + 1 < EG_SEG) continue;
+                const uint32_t code = key_at(j);
+                const bool last = j + 1 == p.seg;
+                const uint32_t next = last ? after : key_at(j + 1 < 64 ? j + 1 : 63);
+                if (next == code && !last) continue;
                 if (has) {
-                    if (whole_run && next != code) {
+                    if (began && next != code) {
                         embed_out<T>(p, code, k, acc);
                     } else {
-                        float* to = p.part + (seg * 2 + (whole_run ? 1 : 0)) * p.dp + kc;
+                        float* to = p.part + (seg * 2 + (began ? 1 : 0)) * p.dp + kc;
 #pragma unroll
                         for (int q = 0; q < VE; ++q) to[q] = acc[q];
                     }
                 }
 #pragma unroll
                 for (int q = 0; q < VE; ++q) acc[q] = 0.f;
-                whole_run = true;
+                began = true;
             }
         }
     }
 }
 
-// Adds what a run left in its segments, in their order: a workgroup per segment (and 64 VE
-// dims) in which a run begins that goes on; its waves share the run's segments.
-constexpr int EJ_W = 4;
+// The sum of the waves' acc, in their order, in wave 0's. All threads call it.
+template <int W, int VE>
+__device__ __forceinline__ void join_waves(float (*sh)[64][VE + 1], float* acc, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < VE; ++q) sh[wave][lane][q] = acc[q];
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+        for (int w = 1; w < W; ++w)
+#pragma unroll
+            for (int q = 0; q < VE; ++q) acc[q] += sh[w][lane][q];
+    }
+}
+
+// acc += shares [a, z) of the run that begins in segment seg, in order: that segment's second
+// slot, then the first slots of those that follow.
+template <int VE>
+__device__ __forceinline__ void embed_shares(const EmbedGradArgs& p, int64_t seg, int64_t a, int64_t z, int kc,
+                                             float* acc) {
+#pragma unroll 8
+    for (int64_t t = a; t < z; ++t) {
+        const float* from = p.part + ((seg + t) * 2 + (t == 0 ? 1 : 0)) * p.dp + kc;
+#pragma unroll
+        for (int q = 0; q < VE; ++q) acc[q] += from[q];
+    }
+}
+
+// Adds what a run left in its segments, in their order. A wave per segment (and block of dims)
+// looks whether a run begins in it that goes on and adds up to EJ_FEW shares itself; the waves of
+// its workgroup share longer runs.
+constexpr int EJ_W = 16, EJ_FEW = 8;
 template <typename T>
 __global__ __launch_bounds__(64 * EJ_W) void k_embed_join(EmbedGradArgs p) {
     constexpr int VE = Vec<T>::VE;
     __shared__ float sh[EJ_W][64][VE + 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int kc = blockIdx.y * 64 * VE + lane * VE;
-    const bool has = kc < p.d;
-    for (int64_t seg = blockIdx.x; seg + 1 < p.segs; seg += gridDim.x) {
-        const int64_t i0 = seg * EG_SEG, last = i0 + EG_SEG - 1;
-        const uint32_t code = p.key[last];
-        if (code >= (uint32_t)p.v || p.key[last + 1] != code) continue;
-        if (p.key[i0] == code && i0 > 0 && p.key[i0 - 1] == code) continue;  // began before
-        int64_t end = seg + 1;  // first segment that does not begin with this code
-        for (;;) {
-            const int64_t t = end + lane;
-            const bool on = t < p.segs && p.key[t * EG_SEG] == code;
-            const uint64_t m = __builtin_amdgcn_ballot_w64(on);
-            end += __popcll(m);
-            if (m != ~uint64_t(0)) break;
-        }
-        // shares of segments seg (its second) and seg + 1 .. end - 1 (their first)
-        const int64_t count = end - seg;
-        const int64_t a = count * wave / EJ_W, z = count * (wave + 1) / EJ_W;
+    __shared__ int64_t lengths[EJ_W];
+    __shared__ uint32_t codes[EJ_W];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kc = (blockIdx.y * p.width + lane) * VE;
+    const bool has = lane < p.width && kc < p.d;
+    for (int64_t base = (int64_t)blockIdx.x * EJ_W; base + 1 < p.segs; base += (int64_t)gridDim.x * EJ_W) {
+        const int64_t seg = base + wave;
+        int64_t count = 0;
+        uint32_t code = 0;
         float acc[VE];
 #pragma unroll
         for (int q = 0; q < VE; ++q) acc[q] = 0.f;
-        if (has) {
-#pragma unroll 4
-            for (int64_t t = a; t < z; ++t) {
-                const float* from = p.part + ((seg + t) * 2 + (t == 0 ? 1 : 0)) * p.dp + kc;
-#pragma unroll
-                for (int q = 0; q < VE; ++q) acc[q] += from[q];
+        if (seg + 1 < p.segs) {
+            const int64_t i0 = seg * p.seg, last = i0 + p.seg - 1;
+            code = p.key[last];
+            const uint32_t next = p.key[last + 1], first = p.key[i0], before = i0 > 0 ? p.key[i0 - 1] : 0xffffffffu;
+            if (code < (uint32_t)p.v && next == code && !(first == code && before == code)) {
+                count = 1;  // segments that the run lies in
+                for (;;) {
+                    const int64_t t = seg + count + lane;
+                    const bool on = t < p.segs && p.key[t * p.seg] == code;
+                    const uint64_t m = __builtin_amdgcn_ballot_w64(on);
+                    count += __popcll(m);
+                    if (m != ~uint64_t(0)) break;
+                }
             }
         }
-#pragma unroll
-        for (int q = 0; q < VE; ++q) sh[wave][lane][q] = acc[q];
-        __syncthreads();
-        if (wave == 0 && has) {
-#pragma unroll
-            for (int q = 0; q < VE; ++q) {
-                float s = sh[0][lane][q];
-#pragma unroll
-                for (int w = 1; w < EJ_W; ++w) s += sh[w][lane][q];
-                acc[q] = s;
-            }
+        if (count > 0 && count <= EJ_FEW && has) {
+            embed_shares<VE>(p, seg, 0, count, kc, acc);
             embed_out<T>(p, code, whole<VE>(kc, p.d), acc);
+        }
+        if (lane == 0) {
+            lengths[wave] = count > EJ_FEW ? count : 0;
+            codes[wave] = code;
+        }
+        __syncthreads();
+        for (int w = 0; w < EJ_W; ++w) {
+            const int64_t n = lengths[w];
+            if (n == 0) continue;
+#pragma unroll
+            for (int q = 0; q < VE; ++q) acc[q] = 0.f;
+            if (has) embed_shares<VE>(p, base + w, n * wave / EJ_W, n * (wave + 1) / EJ_W, kc, acc);
+            join_waves<EJ_W, VE>(sh, acc, wave, lane);
+            if (wave == 0 && has) embed_out<T>(p, codes[w], whole<VE>(kc, p.d), acc);
+            __syncthreads();
         }
         __syncthreads();
     }
 }
 
+// Up to EF_ROWS rows in one launch: a workgroup per row (and block of dims) looks for its code
+// among all rows; the code's first row adds them, the waves sharing its list. Further
+// workgroups set 64 codes each to 0 where no row has them.
+constexpr int EF_ROWS = 1024, EF_W = 4, EF_NT = 64 * EF_W;
+template <typename T>
+__global__ __launch_bounds__(EF_NT) void k_embed_few(EmbedGradArgs p) {
+    constexpr int VE = Vec<T>::VE, CH = EF_ROWS / EF_NT;
+    __shared__ float sh[EF_W][64][VE + 1];
+    __shared__ int list[EF_ROWS], cnt[CH][EF_W];
+    const int tid = threadIdx.x, lane = tid & 63, n = (int)p.n;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t work = (uint32_t)(n * p.cols);
+    const uint32_t item = blockIdx.x;
+    if (item >= work) {
+        const int64_t c0 = (int64_t)(item - work) * 64;
+        if (tid < 64) list[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += EF_NT) {
+            const int64_t c = (int64_t)p.codes[i] - c0;
+            if (c >= 0 && c < 64) list[c] = 1;
+        }
+        __syncthreads();
+        uint64_t left = __builtin_amdgcn_ballot_w64(c0 + lane < p.v && list[lane] == 0);
+        for (int k = 0; left; left &= left - 1, ++k)
+            if (k % EF_W == wave) embed_zero_row<T>(p, c0 + __builtin_ctzll(left), lane);
+        return;
+    }
+    const int r = (int)(item / (uint32_t)p.cols);
+    const int code = p.codes[r];
+    if (code < 0 || code >= p.v) return;
+    uint64_t mask[CH];
+    int before = 0;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const int i = j * EF_NT + tid;
+        const bool same = i < n && p.codes[i] == code;
+        before |= same && i < r;
+        mask[j] = __builtin_amdgcn_ballot_w64(same && i >= r);
+        if (lane == 0) cnt[j][wave] = __popcll(mask[j]);
+    }
+    if (__syncthreads_or(before)) return;
+    int total = 0;
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int w = 0; w < EF_W; ++w) {
+            if (w == wave && (mask[j] >> lane & 1))
+                list[total + __popcll(mask[j] & ((uint64_t(1) << lane) - 1))] = j * EF_NT + tid;
+            total += cnt[j][w];
+        }
+    __syncthreads();
+    const int kc = ((int)(item - (uint32_t)r * p.cols) * p.width + lane) * VE;
+    const bool has = lane < p.width && kc < p.d;
+    const int k = whole<VE>(kc, p.d);
+    const int a = total * wave / EF_W, z = total * (wave + 1) / EF_W;
+    float acc[VE];
+#pragma unroll
+    for (int q = 0; q < VE; ++q) acc[q] = 0.f;
+    for (int j0 = a; j0 < z; j0 += EG_U) {
+        Raw16 x[EG_U];
+        embed_rows<T>(p, has, k, j0, z, [&](int j) { return (uint32_t)list[j]; }, x);
+#pragma unroll
+        for (int u = 0; u < EG_U; ++u)
+            if (j0 + u < z) {
+#pragma unroll
+                for (int q = 0; q < VE; ++q) acc[q] += Vec<T>::get(x[u], q);
+            }
+    }
+    join_waves<EF_W, VE>(sh, acc, wave, lane);
+    if (wave == 0 && has) embed_out<T>(p, (uint32_t)code, k, acc);
+}
+
 struct EmbedPlan {
-    int32_t passes, tiles, words, dp;
+    int32_t passes, bits, tiles, dp, cols, width, seg;
     int64_t tile, segs;
-    size_t o_key[2], o_row[2], o_mat, o_present, o_part, bytes;
+    size_t o_key[2], o_row[2], o_mat, o_part, bytes;
 };
-static EmbedPlan embed_plan(int64_t n, int32_t d, int32_t v) {
+static EmbedPlan embed_plan(int64_t n, int32_t d, int32_t v, int ve) {
     EmbedPlan q{};
+    const int vecs = (d + ve - 1) / ve;
+    q.cols = (vecs + 63) / 64;
+    q.width = (vecs + q.cols - 1) / q.cols;  // blocks of about one size
+    q.dp = (d + 7) / 8 * 8;
+    if (n <= EF_ROWS) {
+        q.bytes = 256;
+        return q;
+    }
     const int bits = 32 - __builtin_clz((unsigned)v);  // of keys 0 .. v
     q.passes = (bits + ES_BITS - 1) / ES_BITS;
+    q.bits = (bits + q.passes - 1) / q.passes;
     q.tile = ES_NT;
     while ((n + q.tile - 1) / q.tile > ES_MAX_TILES) q.tile *= 2;
     q.tiles = (int32_t)((n + q.tile - 1) / q.tile);
-    q.segs = (n + EG_SEG - 1) / EG_SEG;
-    q.words = (v + 31) / 32 + 1;  // 64 codes are looked at at a time
-    q.dp = (d + 7) / 8 * 8;
+    // shorter segments while the chip has room for more waves
+    q.seg = 64;
+    while (q.seg > 8 && (n + q.seg - 1) / q.seg * q.cols < 4096) q.seg /= 2;
+    q.segs = (n + q.seg - 1) / q.seg;
     size_t off = 0;
     auto take = [&](size_t b) {
         const size_t o = off;
@@ -391,10 +515,9 @@ static EmbedPlan embed_plan(int64_t n, int32_t d, int32_t v) {
         q.o_key[i] = take((size_t)n * 4);
         q.o_row[i] = take((size_t)n * 4);
     }
-    q.o_mat = take((size_t)q.tiles * ES_BINS * 4);
-    q.o_present = take((size_t)q.words * 4);
+    q.o_mat = take(((size_t)q.tiles << q.bits) * 4);
     q.o_part = take((size_t)q.segs * 2 * q.dp * 4);
-    q.bytes = off < 256 ? 256 : off;
+    q.bytes = off;
     return q;
 }
 
@@ -404,37 +527,43 @@ static unsigned grid_of(int64_t blocks) {
 }
 
 template <typename T>
-static hipError_t embed_grad(EmbedGradArgs a, const EmbedPlan& q, const int32_t* codes, char* ws, hipStream_t st) {
+static hipError_t embed_grad(EmbedGradArgs a, const EmbedPlan& q, char* ws, hipStream_t st) {
+    a.dp = q.dp;
+    a.cols = q.cols;
+    a.width = q.width;
+    const int64_t zero = (a.v + 63) / 64;
+    if (a.n <= EF_ROWS) {
+        hipLaunchKernelGGL((k_embed_few<T>), dim3((unsigned)(a.n * q.cols + zero)), dim3(EF_NT), 0, st, a);
+        return hipGetLastError();
+    }
     SortArgs s{};
     s.mat = (uint32_t*)(ws + q.o_mat);
-    s.present = (uint32_t*)(ws + q.o_present);
     s.n = a.n;
     s.tile = q.tile;
     s.v = a.v;
     s.tiles = q.tiles;
-    s.words = q.words;
+    s.bits = q.bits;
     for (int i = 0; i < q.passes; ++i) {
-        s.codes = i == 0 ? codes : nullptr;
+        s.codes = i == 0 ? a.codes : nullptr;
         s.key_in = s.key;
         s.row_in = s.row;
         s.key = (uint32_t*)(ws + q.o_key[i & 1]);
         s.row = (uint32_t*)(ws + q.o_row[i & 1]);
-        s.shift = i * ES_BITS;
+        s.shift = i * q.bits;
         hipLaunchKernelGGL(k_embed_count, dim3(q.tiles), dim3(ES_NT), 0, st, s);
         hipLaunchKernelGGL(k_embed_place, dim3(q.tiles), dim3(ES_NT), 0, st, s);
     }
     a.key = s.key;
     a.row = s.row;
-    a.present = s.present;
     a.part = (float*)(ws + q.o_part);
+    a.seg = q.seg;
     a.segs = q.segs;
-    a.dp = q.dp;
-    const int block = 64 * Vec<T>::VE;
-    a.cols = (a.d + block - 1) / block;
-    const int64_t waves = a.segs * a.cols + (a.v + 63) / 64;
-    hipLaunchKernelGGL((k_embed_sum<T>), dim3(grid_of((waves + 3) / 4)), dim3(256), 0, st, a);
-    if (a.segs > 1)
-        hipLaunchKernelGGL((k_embed_join<T>), dim3(grid_of(a.segs - 1), a.cols), dim3(64 * EJ_W), 0, st, a);
+    hipLaunchKernelGGL((k_embed_sum<T>), dim3(grid_of((a.segs * a.cols + zero + 3) / 4)), dim3(256), 0, st, a);
+    if (a.segs > 1) {
+        const int64_t blocks = (a.segs - 2) / EJ_W + 1;
+        hipLaunchKernelGGL((k_embed_join<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096), a.cols), dim3(64 * EJ_W),
+                           0, st, a);
+    }
     return hipGetLastError();
 }
 
@@ -471,7 +600,8 @@ int gmm_embed(const void* table, int32_t v, int32_t d, int64_t ldt, int32_t dtyp
 
 size_t gmm_embed_backward_workspace_bytes(int64_t n, int32_t d, int32_t v) {
     if (n < 0 || n > EMB_MAX_ROWS || d < 1 || d > EMB_MAX_DIM || v < 1 || v > EMB_MAX_CODES) return 0;
-    return embed_plan(n, d, v).bytes;
+    const EmbedPlan a = embed_plan(n, d, v, 4), b = embed_plan(n, d, v, 8);  // fp32, bf16
+    return a.bytes > b.bytes ? a.bytes : b.bytes;
 }
 
 int gmm_embed_backward(const void* grad, int64_t n, int32_t d, int64_t ldg, int32_t dtype,
@@ -482,7 +612,7 @@ int gmm_embed_backward(const void* grad, int64_t n, int32_t d, int64_t ldg, int3
         return GMM_E_INVALID;
     if (n > EMB_MAX_ROWS || d > EMB_MAX_DIM || v > EMB_MAX_CODES) return GMM_E_UNSUPPORTED;
     if (n > 0 && (!grad || !codes)) return GMM_E_INVALID;
-    const EmbedPlan q = embed_plan(n, d, v);
+    const EmbedPlan q = embed_plan(n, d, v, dtype == GMM_F32 ? 4 : 8);
     if (!workspace || workspace_bytes < q.bytes || (uintptr_t)workspace % 256 != 0)
         return GMM_E_WORKSPACE;
     hipStream_t st = (hipStream_t)stream;
@@ -496,6 +626,7 @@ int gmm_embed_backward(const void* grad, int64_t n, int32_t d, int64_t ldg, int3
     }
     EmbedGradArgs a{};
     a.g = grad;
+    a.codes = codes;
     a.out = d_table;
     a.n = n;
     a.ldg = ldg;
@@ -503,8 +634,8 @@ int gmm_embed_backward(const void* grad, int64_t n, int32_t d, int64_t ldg, int3
     a.v = v;
     a.d = d;
     a.scale = scale;
-    const hipError_t e = dtype == GMM_F32 ? embed_grad<float>(a, q, codes, (char*)workspace, st)
-                                          : embed_grad<uint16_t>(a, q, codes, (char*)workspace, st);
+    const hipError_t e = dtype == GMM_F32 ? embed_grad<float>(a, q, (char*)workspace, st)
+                                          : embed_grad<uint16_t>(a, q, (char*)workspace, st);
     return e == hipSuccess ? GMM_OK : GMM_E_HIP;
 }
 

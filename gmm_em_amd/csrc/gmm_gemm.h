@@ -6,6 +6,8 @@
 // bit (24 bits in three parts of 8, rounded to nearest): the product is then the sum
 // of six plane products, smallest first, in the same fp32 accumulators; the three that are
 // left out are below 2^-24 of it together, of either sign. bf16 and fp16 operands have one plane.
+// 8-bit integers are taken as pairs: a "value" below is two of them, a step 128, and the sums
+// are exact 32-bit integers (gmm_quant.hip).
 //
 // B may also lie with the contracted axis across (TB): panels of 64 of its rows,
 // [n / 64][k][64], as the product before wrote them with those rows contiguous. Its
@@ -34,12 +36,16 @@ namespace gmm {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));  // sums, or 16 8-bit integers
 
 __device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ f32x4 mfma32(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ i32x4 mfma32(i32x4 a, i32x4 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
 constexpr int GK = 64;  // contracted values per step
@@ -64,8 +70,8 @@ __device__ __forceinline__ void gemm_pair(int pairs, int p, int* pa, int* pb) {
     *pb = (0x118 >> (2 * q)) & 3;  // 0 2 1 0 1 0
 }
 
-// ONE: operands of one plane. TB: b lies with the contracted axis across.
-template <int BM, int BN, int WM, int WN, bool ONE, bool TB = false>
+// ONE: operands of one plane. TB: b lies with the contracted axis across. Acc: the sums' type.
+template <int BM, int BN, int WM, int WN, bool ONE, bool TB = false, typename Acc = f32x4>
 struct Gemm {
     static constexpr int NT = 64 * WM * WN;
     static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 blocks per wave
@@ -73,7 +79,7 @@ struct Gemm {
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int COPIES = STAGE / 1024 / (NT / 64);  // per wave and step
 
-    f32x4 acc[TM][TN];
+    Acc acc[TM][TN];
 
     // LDS byte offset of piece p of row r within an operand's step
     static __device__ __forceinline__ int at(int r, int p) { return r * 128 + ((p ^ (r & 7)) << 4); }
@@ -212,7 +218,7 @@ struct Gemm {
 #pragma unroll
         for (int x = 0; x < TM; ++x)
 #pragma unroll
-            for (int y = 0; y < TN; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int y = 0; y < TN; ++y) acc[x][y] = Acc{0, 0, 0, 0};
         auto read = [&](V8(&fa)[TM], V8(&fb)[TN], const unsigned char* da, int c) {
             const unsigned char* db = da + A_BYTES;
 #pragma unroll

@@ -39,6 +39,7 @@
 #include "gmm_gemm.h"
 #include "gmm_nn.h"
 #include "gmm_softmax.h"
+#include "gmm_tiles.h"
 
 namespace gmm {
 
@@ -676,77 +677,17 @@ __global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
 
 // ---- host side
 
-static size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
-static int pad(int64_t k) { return (int)((k + GK - 1) / GK * GK); }
-// Workgroup tiles: codes or dims by rows.
-template <int ID>
-struct Tile;
-template <>
-struct Tile<0> {
-    static constexpr int BM = 256, BN = 256, WM = 2, WN = 4;
-};
-template <>
-struct Tile<1> {
-    static constexpr int BM = 192, BN = 256, WM = 2, WN = 4;
-};
-template <>
-struct Tile<2> {
-    static constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
-};
-template <>
-struct Tile<3> {
-    static constexpr int BM = 64, BN = 64, WM = 2, WN = 2;
-};
-
-// The tile and the split of the contracted axis that take least time by a
-// model of it: rounds of workgroups over the chip, each of a fixed part and a
-// part per step, and the writing and reading of a split's partial sums.
-// per_step: measured over long products of bf16 rows read in place, per workgroup with the chip
+// Costs of the tiles. per_step: measured over long products of bf16 rows read in place, per workgroup with the chip
 // full; the gradients' operands take longer (a step of 192 x 256 1.6 us), all tiles alike.
 // What it picks against the best of the four tiles with splits of 1, 2, 4, 8 and 16 (microseconds of
 // a call for dh, for dW; in those dx has the tile too), bf16: 8192 x 768 x 16384 469 and 461 (469,
 // 474), 4096 x 1024 x 8192 179 and 155 (167, 167), 2048 x 512 x 32768 188 and 170 (206, 170), 1024 x
 // 768 x 4096 50 and 44 (49, 44), 300 x 256 x 5000 37 and 26 (36, 26); fp32: 2048 x 768 x 8192 315 and
 // 309 (323, 326), 777 x 100 x 1001 35 and 34 (34, 32).
-struct TileCost {
-    int bm, bn, at_once;  // workgroups on the chip
-    float per_step, fixed;  // microseconds
-};
 constexpr TileCost TILE_COST[4] = {
     {256, 256, 256, 1.42f, 6.f}, {192, 256, 256, 1.12f, 6.f}, {128, 128, 512, 0.92f, 4.f},
     {64, 64, 1024, 0.55f, 3.f}};
 
-struct Choice {
-    int tile, split;
-};
-static Choice choose_tile(int64_t m, int64_t n, int64_t steps, int max_split) {
-    Choice best{0, 1};
-    double least = 1e300;
-    for (int t = 0; t < 4; ++t) {
-        const TileCost& c = TILE_COST[t];
-        const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
-        for (int s = 1; s <= max_split && s <= steps; ++s) {
-            if (s > 1 && (size_t)s * m * n * 4 > HEAD_SPLIT_BYTES) break;
-            const int64_t rounds = (tiles * s + c.at_once - 1) / c.at_once;
-            double us = rounds * (c.fixed + c.per_step * (double)((steps + s - 1) / s));
-            if (s > 1) us += 4.0 + (double)m * n * 8 * s / 4.0e6;
-            if (us < least) {
-                least = us;
-                best = Choice{t, s};
-            }
-        }
-    }
-    return best;
-}
-template <typename F>
-static void with_tile(int tile, F f) {
-    switch (tile) {
-        case 0: f(std::integral_constant<int, 0>()); break;
-        case 1: f(std::integral_constant<int, 1>()); break;
-        case 2: f(std::integral_constant<int, 2>()); break;
-        default: f(std::integral_constant<int, 3>()); break;
-    }
-}
 
 // Workspace of a head call: operands that need laying out, then the chunk's
 // scratch. Offsets in bytes; a part that is not needed takes none.
@@ -839,10 +780,6 @@ static void planes_t(const LayoutPair& p, const int32_t* dim_exp, const int32_t*
                                  row_exp);
 }
 
-static unsigned tile_grid(int mt, int nt) {
-    return (unsigned)(((int64_t)mt * nt + 7) / 8 * 8);
-}
-
 // walk: the kernel's workgroups walk over the tiles, as many as the chip holds.
 template <int ID, typename K, typename A>
 static void launch_tiles(K kernel, A& a, int split, bool walk, hipStream_t st) {
@@ -857,7 +794,8 @@ static void launch_tiles(K kernel, A& a, int split, bool walk, hipStream_t st) {
 // out = the product of o.in, with the tile and split that suit it.
 template <typename T, bool TB>
 static void launch_grad(GradOut& o, float* part, hipStream_t st) {
-    const Choice c = choose_tile(o.in.m, o.in.n, (int64_t)o.in.kp / GK * o.in.pairs, HEAD_MAX_SPLIT);
+    const Choice c = choose_tile(TILE_COST, o.in.m, o.in.n, (int64_t)o.in.kp / GK * o.in.pairs, HEAD_MAX_SPLIT,
+                                 HEAD_SPLIT_BYTES);
     o.split = c.split;
     o.part = part;
     o.fours = o.in.m % 4 == 0 && o.ldo % 4 == 0 && (uintptr_t)o.out % (4 * sizeof(T)) == 0;
@@ -938,7 +876,7 @@ static hipError_t head_score(const HeadIn& x, const HeadPlan& q, ScoreArgs s, ch
             a.s.top_idx = s.top_idx + r0 * s.m;
             a.s.top_logprob = s.top_logprob + r0 * s.m;
         }
-        const Choice c = choose_tile(x.v, rows, (int64_t)q.dp / GK * q.pairs, 1);
+        const Choice c = choose_tile(TILE_COST, x.v, rows, (int64_t)q.dp / GK * q.pairs, 1, 0);
         with_tile(c.tile, [&](auto b) {
             constexpr int B = decltype(b)::value;
             constexpr bool ONE = Planes<T>::P == 1;
@@ -1000,7 +938,7 @@ static hipError_t head_grad(const HeadIn& x, const HeadPlan& q, HeadArgs a, void
         a.entropy = all.entropy ? all.entropy + r0 : nullptr;
         a.g_logprob = all.g_logprob ? all.g_logprob + r0 : nullptr;
         a.g_entropy = all.g_entropy ? all.g_entropy + r0 : nullptr;
-        const Choice c = choose_tile(x.v, rows, (int64_t)q.dp / GK * q.pairs, 1);
+        const Choice c = choose_tile(TILE_COST, x.v, rows, (int64_t)q.dp / GK * q.pairs, 1, 0);
         with_tile(c.tile, [&](auto b) {
             constexpr int B = decltype(b)::value;
             using C = Tile<B>;

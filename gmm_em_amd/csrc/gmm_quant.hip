@@ -7,20 +7,25 @@
 // k_quant_few: few rows. The product is the reading of w: 16 weight rows by 16 rows of q
 // per matrix instruction, both straight from memory, the contracted axis split over the
 // waves and joined in LDS.
+// k_quant_tiles: more rows, by the tiles of gmm_gemm.h (codes are the tile rows, so that a lane
+// has four neighbouring codes of a row to write). Operands whose rows are not 16-byte
+// aligned, or not whole steps of 128 long, are laid out in panels first.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gmm_em.h"
+#include "gmm_gemm.h"
 #include "gmm_nn.h"
 #include "gmm_softmax.h"
+#include "gmm_tiles.h"
 
 namespace gmm {
 
 constexpr int32_t QU_MAX_DIM = (1 << 17) - 1;  // 128 * 128 * d stays below 2^31
 constexpr int32_t QU_MAX_CODES = 1 << 22;
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // ---- rows to integers
 
@@ -99,8 +104,7 @@ struct ProductArgs {
 };
 
 __device__ __forceinline__ i32x4 mfma_i8(const Raw16& a, const Raw16& b, i32x4 c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
-                                                 0, 0, 0);
+    return mfma32(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c);
 }
 
 // 16 bytes of a row, 0 at or past `end`.
@@ -163,18 +167,242 @@ __global__ __launch_bounds__(64 * QF_W) void k_quant_few(ProductArgs p) {
     }
 }
 
+// ---- tiles
+
+constexpr int QT_STEP = 2 * GK;              // integers of a step
+constexpr int64_t QT_MAX_LD = (int64_t)1 << 23;  // 256 rows span at most 2^31 bytes
+constexpr size_t QT_PACK_BYTES = (size_t)256 << 20;   // rows of q laid out at a time
+constexpr size_t QT_SPLIT_BYTES = (size_t)128 << 20;  // partial sums of a split product
+constexpr int QT_MAX_SPLIT = 16;
+constexpr int QT_FEW_ROWS = 64;
+
+struct TilesArgs {
+    GemmIn in;           // a: codes, b: rows of q
+    int32_t mt, nt, split;
+    const float *q_scale, *w_scale;
+    void* y;
+    int64_t ldy;
+    int32_t* part;       // [split][rows][codes]
+};
+
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Four {
+    T v[4];
+};
+
+template <typename T, int BM, int BN, int WM, int WN, bool SPLIT>
+__global__ __launch_bounds__(64 * WM * WN) void k_quant_tiles(TilesArgs p) {
+    using G = Gemm<BM, BN, WM, WN, true, false, i32x4>;
+    __shared__ __align__(16) unsigned char l0[G::STAGE], l1[G::STAGE];
+    if constexpr (SPLIT) {
+        int tm, tn;
+        if (!gemm_tile(blockIdx.x, p.mt, p.nt, &tm, &tn)) return;
+        const int m0 = tm * BM, n0 = tn * BN, steps = G::all_steps(p.in);
+        G g;
+        g.begin(p.in, m0, n0, steps * (int)blockIdx.y / p.split, steps * ((int)blockIdx.y + 1) / p.split, l0, l1);
+        g.template finish<i32x4>(p.in, m0, n0, l0, l1);
+#pragma unroll
+        for (int y = 0; y < G::TN; ++y) {
+            const int r = n0 + G::col(y);
+            if (r >= p.in.n) continue;
+            int32_t* o = p.part + ((int64_t)blockIdx.y * p.in.n + r) * p.in.m;
+#pragma unroll
+            for (int x = 0; x < G::TM; ++x) {
+                const int c = m0 + G::row(x);
+                if (c + 4 <= p.in.m) {
+                    *(Four<int32_t>*)(o + c) = __builtin_bit_cast(Four<int32_t>, g.acc[x][y]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (c + q < p.in.m) o[c + q] = g.acc[x][y][q];
+                }
+            }
+        }
+    } else {
+        gemm_walk<i32x4, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
+            Four<float> ws[G::TM];
+#pragma unroll
+            for (int x = 0; x < G::TM; ++x) {
+                const int c = m0 + G::row(x);
+                if (c + 4 <= p.in.m) {
+                    ws[x] = *(const Four<float>*)(p.w_scale + c);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) ws[x].v[q] = c + q < p.in.m ? p.w_scale[c + q] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < G::TN; ++y) {
+                const int r = n0 + G::col(y);
+                if (r >= p.in.n) continue;
+                const float qs = p.q_scale[r];
+                T* o = (T*)p.y + (int64_t)r * p.ldy;
+#pragma unroll
+                for (int x = 0; x < G::TM; ++x) {
+                    const int c = m0 + G::row(x);
+                    Four<T> u;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) u.v[q] = scaled_sum<T>(g.acc[x][y][q], qs, ws[x].v[q]);
+                    if (c + 4 <= p.in.m) {
+                        *(Four<T>*)(o + c) = u;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (c + q < p.in.m) o[c + q] = u.v[q];
+                    }
+                }
+            }
+        });
+    }
+}
+
+// The sums of a split product, four codes of a row per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_quant_sum(TilesArgs p) {
+    const int per = (p.in.m + 3) / 4;
+    const int64_t total = (int64_t)p.in.n * per, plane = (int64_t)p.in.n * p.in.m;
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total; j += (int64_t)gridDim.x * 256) {
+        const int64_t r = j / per;
+        const int c = (int)(j - r * per) * 4, left = p.in.m - c < 4 ? p.in.m - c : 4;
+        const int32_t* from = p.part + r * p.in.m + c;
+        int acc[4] = {0, 0, 0, 0};
+        for (int s = 0; s < p.split; ++s)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < left) acc[q] += from[s * plane + q];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (q < left)
+                ((T*)p.y)[r * p.ldy + c + q] = scaled_sum<T>(acc[q], p.q_scale[r], p.w_scale[c + q]);
+    }
+}
+
+// Operands in panels of 128 integers, 0 past the d-th (blockIdx.y: w, then q; rows == 0 is none).
+struct PackArgs {
+    struct {
+        const int8_t* x;
+        int64_t rows, ld;
+        int8_t* out;
+    } o[2];
+    int32_t d, dp;
+};
+__global__ __launch_bounds__(256) void k_quant_pack(PackArgs p) {
+    const auto o = p.o[blockIdx.y];
+    const int per = p.dp / 16;
+    const int64_t total = o.rows * per;
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total; j += (int64_t)gridDim.x * 256) {
+        const int64_t r = j / per;
+        const int k = (int)(j - r * per) * 16;
+        const Raw16 v = load_bytes(o.x + r * o.ld, k, p.d);
+        *(uint4*)(o.out + ((k / QT_STEP) * o.rows + r) * QT_STEP + k % QT_STEP) =
+            uint4{v.w[0], v.w[1], v.w[2], v.w[3]};
+    }
+}
+
+static bool quant_direct(const int8_t* x, int32_t d, int64_t ld) {
+    return d % QT_STEP == 0 && ld % 16 == 0 && ld <= QT_MAX_LD && (uintptr_t)x % 16 == 0;
+}
+
+struct QuantPlan {
+    int32_t dp;
+    int64_t chunk;  // rows at a time
+    size_t o_w, o_q, o_part, bytes;
+};
+// pack_q, pack_w: whether the operands have to be laid out (the sizing entry point assumes both).
+static QuantPlan quant_plan(int64_t n, int32_t d, int32_t v, bool pack_q, bool pack_w) {
+    QuantPlan q{};
+    if (n <= QT_FEW_ROWS) {
+        q.bytes = 256;
+        return q;
+    }
+    q.dp = (d + QT_STEP - 1) / QT_STEP * QT_STEP;
+    q.chunk = (int64_t)(QT_PACK_BYTES / q.dp) / 256 * 256;
+    if (q.chunk > n) q.chunk = n;
+    size_t off = 0;
+    auto take = [&](size_t b) {
+        const size_t o = off;
+        off += up256(b);
+        return o;
+    };
+    q.o_w = take(pack_w ? (size_t)v * q.dp : 0);
+    q.o_q = take(pack_q ? (size_t)q.chunk * q.dp : 0);
+    const size_t most = (size_t)q.chunk * v * 4 * QT_MAX_SPLIT;
+    q.o_part = take(most < QT_SPLIT_BYTES ? most : QT_SPLIT_BYTES);
+    q.bytes = off;
+    return q;
+}
+
+// Costs of the tiles (gmm_tiles.h), a step of 128 integers.
+constexpr TileCost QUANT_COST[4] = {
+    {256, 256, 256, 1.42f, 6.f}, {192, 256, 256, 1.12f, 6.f}, {128, 128, 512, 0.92f, 4.f},
+    {64, 64, 1024, 0.55f, 3.f}};
+
 template <typename T>
 static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) {
-    (void)ws;
-    const int64_t mt = (a.v + 15) / 16;
-    auto grid = [&](int rows) {
-        const int64_t b = mt * ((a.n + rows - 1) / rows), most = (int64_t)1 << 22;
-        return dim3((unsigned)(b < most ? b : most));
-    };
-    if (a.n <= 16)
-        hipLaunchKernelGGL((k_quant_few<T, 1>), grid(16), dim3(64 * QF_W), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_quant_few<T, 4>), grid(64), dim3(64 * QF_W), 0, st, a);
+    if (a.n <= QT_FEW_ROWS) {
+        const int64_t mt = (a.v + 15) / 16;
+        auto grid = [&](int rows) {
+            const int64_t b = mt * ((a.n + rows - 1) / rows), most = (int64_t)1 << 22;
+            return dim3((unsigned)(b < most ? b : most));
+        };
+        if (a.n <= 16)
+            hipLaunchKernelGGL((k_quant_few<T, 1>), grid(16), dim3(64 * QF_W), 0, st, a);
+        else
+            hipLaunchKernelGGL((k_quant_few<T, 4>), grid(64), dim3(64 * QF_W), 0, st, a);
+        return hipGetLastError();
+    }
+    const bool pq = !quant_direct(a.q, a.d, a.ldq), pw = !quant_direct(a.w, a.d, a.ldw);
+    const QuantPlan q = quant_plan(a.n, a.d, a.v, pq, pw);
+    TilesArgs t{};
+    t.w_scale = a.w_scale;
+    t.ldy = a.ldy;
+    t.part = (int32_t*)(ws + q.o_part);
+    t.in.pairs = 1;
+    t.in.kp = q.dp / 2;
+    t.in.m = a.v;
+    t.in.a = (const uint16_t*)(pw ? (const int8_t*)ws + q.o_w : a.w);
+    t.in.lda = pw ? GK : a.ldw / 2;
+    t.in.step_a = pw ? (int64_t)a.v * GK : GK;
+    for (int64_t r0 = 0; r0 < a.n; r0 += q.chunk) {
+        const int64_t rows = a.n - r0 < q.chunk ? a.n - r0 : q.chunk;
+        PackArgs p{};
+        p.d = a.d;
+        p.dp = q.dp;
+        if (pw && r0 == 0) p.o[0] = {a.w, a.v, a.ldw, (int8_t*)ws + q.o_w};
+        if (pq) p.o[1] = {a.q + r0 * a.ldq, rows, a.ldq, (int8_t*)ws + q.o_q};
+        const int64_t most = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
+        if (most > 0) {
+            const int64_t b = (most * (q.dp / 16) + 255) / 256;
+            hipLaunchKernelGGL(k_quant_pack, dim3((unsigned)(b < 65536 ? b : 65536), 2), dim3(256), 0, st, p);
+        }
+        t.in.b = (const uint16_t*)(pq ? (const int8_t*)ws + q.o_q : a.q + r0 * a.ldq);
+        t.in.ldb = pq ? GK : a.ldq / 2;
+        t.in.step_b = pq ? rows * GK : GK;
+        t.in.n = (int32_t)rows;
+        t.q_scale = a.q_scale + r0;
+        t.y = (T*)a.y + r0 * a.ldy;
+        const Choice c = choose_tile(QUANT_COST, a.v, rows, q.dp / QT_STEP, QT_MAX_SPLIT, QT_SPLIT_BYTES);
+        t.split = c.split;
+        with_tile(c.tile, [&](auto id) {
+            using C = Tile<decltype(id)::value>;
+            t.mt = (a.v + C::BM - 1) / C::BM;
+            t.nt = (int32_t)((rows + C::BN - 1) / C::BN);
+            unsigned grid = tile_grid(t.mt, t.nt);
+            const dim3 block(64 * C::WM * C::WN);
+            if (c.split > 1) {
+                hipLaunchKernelGGL((k_quant_tiles<T, C::BM, C::BN, C::WM, C::WN, true>), dim3(grid, c.split), block, 0,
+                                   st, t);
+            } else {
+                const unsigned most_at_once = (unsigned)QUANT_COST[decltype(id)::value].at_once;
+                if (grid > most_at_once) grid = most_at_once;
+                hipLaunchKernelGGL((k_quant_tiles<T, C::BM, C::BN, C::WM, C::WN, false>), dim3(grid), block, 0, st, t);
+            }
+        });
+        if (c.split > 1) {
+            const int64_t work = (rows * ((a.v + 3) / 4) + 255) / 256;
+            hipLaunchKernelGGL((k_quant_sum<T>), dim3((unsigned)(work < 16384 ? work : 16384)), dim3(256), 0, st, t);
+        }
+    }
     return hipGetLastError();
 }
 
@@ -203,7 +431,7 @@ int gmm_quantize_rows(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t 
 
 size_t gmm_quantized_product_workspace_bytes(int64_t n, int32_t d, int32_t v) {
     if (n < 0 || n > SC_MAX_ROWS || d < 1 || v < 1 || d > QU_MAX_DIM || v > QU_MAX_CODES) return 0;
-    return 256;
+    return quant_plan(n, d, v, true, true).bytes;
 }
 
 int gmm_quantized_product(const int8_t* q, int64_t n, int32_t d, int64_t ldq, const float* q_scale,

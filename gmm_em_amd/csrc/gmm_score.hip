@@ -11,7 +11,7 @@
 // bound that m values of the row reach and hardly more than m do (about
 // 64 ln(64 / (64 - m))). The values of the few threads whose maximum reaches it are
 // read again by all threads (they are in the caches), those at the bound are gathered
-// in LDS, and one wave picks the m best. Where ties or a mask put more values at the bound than LDS holds, the m
+// in LDS, and each finds its place by counting those before it. Where ties or a mask put more values at the bound than LDS holds, the m
 // best are found one by one over the whole row.
 // Gradient: dx = scale (g_lp ([v = t] - p) - g_H p (log p + H)) with p from the
 // stored m and log s: each logit is read once and its gradient written once.
@@ -79,8 +79,8 @@ struct RowPart {
 template <typename T, int NT, bool TOP, bool BEAM = false>
 __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
     constexpr int VE = Vec<T>::VE, NW = NT / 64, G = NT / 64, CHUNK = NT * VE * SC_U;
-    __shared__ float sst[NW][3], gmax[64], cv[SC_CAND], best_v;
-    __shared__ int ci[SC_CAND], hot[NT], hots, count, best_i;
+    __shared__ float sst[NW][3], gmax[64], cv[SC_CAND], ov[TOP_MAX], best_v;
+    __shared__ int ci[SC_CAND], oi[TOP_MAX], hot[NT], hots, count, best_i;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int64_t item = blockIdx.x; item < p.n * p.parts; item += gridDim.x) {
         const int64_t row = item / p.parts;
@@ -134,6 +134,10 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
             if (TOP && lane % G == 0) gmax[tid / G] = gm;
         }
         if (TOP && tid == 0) hots = count = 0;
+        if (TOP && tid < TOP_MAX) {
+            ov[tid] = -INFINITY;
+            oi[tid] = 0x7fffffff;
+        }
         __syncthreads();
         if constexpr (NW > 1) {
             if (wave == 0) {
@@ -150,20 +154,24 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
             auto in = [&](float l) { return l > -INFINITY && order_of(l) >= bound; };
             if (in(cm)) hot[atomicAdd(&hots, 1)] = tid;
             __syncthreads();
-            // the hot threads' values, a value per thread at a time
-            const uint32_t mine = (x.len + CHUNK - 1) / CHUNK * SC_U * VE;  // values of a thread
-            const uint32_t total = (uint32_t)hots * mine;  // at most the row, rounded up
+            // the hot threads' vectors, one per thread at a time
+            const uint32_t mine = (x.len + CHUNK - 1) / CHUNK * SC_U;  // vectors of a thread
+            const uint32_t total = (uint32_t)hots * mine;
             for (uint32_t e = tid; e < total; e += NT) {
                 const int h = (int)(e / mine), j = (int)(e - h * mine);
-                const int u = j / VE, k = j % VE;
-                const int at = u / SC_U * CHUNK + (u % SC_U * NT + hot[h]) * VE + k;
-                if (at < x.len) {
-                    const float l = scaled(Vec<T>::one(x.x + at), p.scale);
+                const int at = j / SC_U * CHUNK + (j % SC_U * NT + hot[h]) * VE;
+                if (at >= x.len) continue;
+                Raw16 r = x.get(at);
+                x.mask(r, at);
+                const int first = (int)i0 + x.first(at);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    const float l = scaled(Vec<T>::get(r, k), p.scale);
                     if (in(l)) {
                         const int to = atomicAdd(&count, 1);
                         if (to < SC_CAND) {
                             cv[to] = l;
-                            ci[to] = (int)i0 + at;
+                            ci[to] = first + k;
                         }
                     }
                 }
@@ -213,21 +221,12 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
                 }
                 cnt = p.m;
             }
-            if (wave == 0) {
-                auto pick = [&](auto per) {
-                    constexpr int C = decltype(per)::value;
-                    float v[C];
-                    int i[C];
-#pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const int e = c * 64 + lane;
-                        v[c] = e < cnt ? cv[e] : -INFINITY;
-                        i[c] = e < cnt ? ci[e] : 0x7fffffff;
-                    }
-                    return top_pick<C>(v, i, p.m, lane);
-                };
-                top = cnt <= 64 ? pick(std::integral_constant<int, 1>())
-                                : pick(std::integral_constant<int, SC_CAND / 64>());
+            // every candidate counts those before it
+            top_rank(cv, ci, cnt, p.m, ov, oi, tid, NT);
+            __syncthreads();
+            if (wave == 0 && lane < p.m) {
+                top.v = ov[lane];
+                top.i = oi[lane];
             }
         }
         if (wave == 0) {

@@ -72,6 +72,27 @@ struct Vec<uint16_t> {
     static __device__ __forceinline__ uint16_t store(float v) { return (uint16_t)f32_to_bf16(v); }
 };
 
+// VE values as 16 bytes; bf16 by the hardware's conversion of pairs (round to nearest even).
+template <typename T>
+__device__ __forceinline__ Raw16 pack16(const float* v);
+template <>
+__device__ __forceinline__ Raw16 pack16<float>(const float* v) {
+    Raw16 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.w[k] = __float_as_uint(v[k]);
+    return r;
+}
+template <>
+__device__ __forceinline__ Raw16 pack16<uint16_t>(const float* v) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    Raw16 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        r.w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * k], v[2 * k + 1]}, bf16x2));
+    return r;
+}
+
 // The VE values of p[i .. i+VE), those at or past `end` as -inf.
 template <typename T>
 __device__ __forceinline__ Raw16 load_vec(const T* p, int64_t i, int64_t end) {

@@ -105,10 +105,35 @@ def test_gradient_of_uneven_codes(ops, kind, dtype):
     assert torch.equal(a, ops.embed_backward(grad, codes, v, 2.0))
 
 
+@pytest.mark.parametrize("n,run", [(1025, 8), (2048, 16), (5000, 32), (300_000, 64), (70_000, 2000)])
+def test_runs_that_meet_segments(ops, n, run):
+    # runs as long as segments are, a shorter one in front so that they straddle them, one code none
+    g = _gen(n)
+    for first in (0, 1, run // 2):
+        codes = ((torch.arange(n, device=DEV) + first) // run).to(torch.int32)
+        codes[codes == 3] = -1
+        v = int(codes.max()) + 5
+        perm = torch.randperm(n, generator=g, device=DEV)
+        grad = torch.randn(n, 20, generator=g, device=DEV)
+        for c in (codes, codes[perm].contiguous()):
+            _check_grad(ops.embed_backward(grad, c, v), grad, c, v, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [1024, 1025])
+@pytest.mark.parametrize("d", [3, 260, 513, 1500])
+def test_either_side_of_few_rows(ops, n, d, dtype):
+    g = _gen(n + d)
+    codes = _codes(n, 90, g)
+    codes[::5] = 17
+    grad = torch.randn(n, d, generator=g, device=DEV).to(dtype)
+    _check_grad(ops.embed_backward(grad, codes, 90, 0.5), grad, codes, 90, 0.5)
+
+
 def test_three_digits(ops):
-    # codes of more than 18 bits are sorted in three steps
+    # codes of more than 20 bits are sorted in three steps
     g = _gen(8)
-    v, n, d = 300_007, 20_000, 24
+    v, n, d = 3_000_007, 20_000, 24
     codes = torch.randint(0, v, (n,), generator=g, device=DEV, dtype=torch.int32)
     codes[::3] = v - 1
     grad = torch.randn(n, d, generator=g, device=DEV)
