@@ -87,13 +87,16 @@ template <typename T, int LPR, int CV, int NT>
 __global__ __launch_bounds__(NT) void k_balance_rows(BalanceArgs p) {
     using Row = RouterRow<T, LPR, CV>;
     constexpr int C = Row::C, RPW = 64 / LPR, W = NT / 64;
-    extern __shared__ float sums[];  // [e], then counts [e + 1]
-    int* cnt = (int*)(sums + p.e);
+    // the waves' sums [SLABS][e], then counts [e] and each wave's rows
+    constexpr int SLABS = CV == 1 ? W : 1;
+    extern __shared__ float sums[];
+    int* cnt = (int*)(sums + SLABS * p.e);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int gl = lane % LPR, grp = lane / LPR;
     if (blockIdx.x == 0 && tid == 0) *p.done = 0;  // for the kernel after this one
-    for (int c = tid; c <= p.e; c += NT) cnt[c] = 0;
+    for (int c = tid; c < p.e; c += NT) cnt[c] = 0;
     __syncthreads();
+    int rows = 0;  // of this wave, with a pick
     float acc[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) acc[j] = 0.f;
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(NT) void k_balance_rows(BalanceArgs p) {
         const bool picked = pick >= 0 && pick < p.e;
         const bool live = (__builtin_amdgcn_ballot_w64(picked) & mine) != 0;
         if (picked) atomicAdd(&cnt[pick], 1);
-        if (gl == 0 && live) atomicAdd(&cnt[p.e], 1);
+        rows += __popcll(__builtin_amdgcn_ballot_w64(gl == 0 && live));
         float m = -3.402823466e38f, s = 0.f;
 #pragma unroll
         for (int j = 0; j < C; ++j) m = fmaxf(m, x.v[j]);
@@ -136,13 +139,13 @@ __global__ __launch_bounds__(NT) void k_balance_rows(BalanceArgs p) {
         s = group_reduce_sum<LPR>(s);
         const bool none = s == 0.f;  // every logit -inf
         if (live) {
-            const float inv = none ? 0.f : 1.f / s;
+            const float inv = none ? 0.f : __builtin_amdgcn_rcpf(s);
 #pragma unroll
             for (int j = 0; j < C; ++j) acc[j] = fmaf(x.v[j], inv, acc[j]);
         }
         if (gl == 0 && in) {
             p.norm[2 * row] = !live ? INFINITY : none ? -INFINITY : (s == s ? m : NAN);
-            p.norm[2 * row + 1] = !live || none ? 0.f : logf(s);
+            p.norm[2 * row + 1] = !live || none ? 0.f : __builtin_amdgcn_logf(s) * 0.693147180559945309f;
         }
     }
     // the rows of a wave, then its workgroup's waves in order
@@ -151,19 +154,38 @@ __global__ __launch_bounds__(NT) void k_balance_rows(BalanceArgs p) {
         if (LPR < 32) acc[j] += __shfl_xor(acc[j], 16);
         if (LPR < 64) acc[j] += __shfl_xor(acc[j], 32);
     }
-    for (int w = 0; w < W; ++w) {
-        if (w == wave && grp == 0) {
+    if (lane == 0) cnt[p.e + wave] = rows;
+    if constexpr (SLABS > 1) {
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                const int c = Row::at(gl, j);
-                if (c < p.e) sums[c] = w == 0 ? acc[j] : sums[c] + acc[j];
-            }
+        for (int j = 0; j < C; ++j) {
+            const int c = Row::at(gl, j);
+            if (grp == 0 && c < p.e) sums[wave * p.e + c] = acc[j];
         }
         __syncthreads();
+        for (int c = tid; c < p.e; c += NT) {
+            float s = sums[c];
+#pragma unroll
+            for (int w = 1; w < SLABS; ++w) s += sums[w * p.e + c];
+            sums[c] = s;  // (read and written by this thread alone)
+        }
+    } else {
+        for (int w = 0; w < W; ++w) {
+            if (w == wave && grp == 0) {
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    const int c = Row::at(gl, j);
+                    if (c < p.e) sums[c] = w == 0 ? acc[j] : sums[c] + acc[j];
+                }
+            }
+            __syncthreads();
+        }
     }
     for (int c = tid; c < p.e; c += NT)
         p.part[(int64_t)blockIdx.x * p.e + c] = BalancePart{sums[c], cnt[c]};
-    if (tid == 0) p.part_rows[blockIdx.x] = cnt[p.e];
+    if (tid == 0) {
+        for (int w = 1; w < W; ++w) rows += cnt[p.e + w];
+        p.part_rows[blockIdx.x] = rows;
+    }
 }
 
 // A workgroup adds the parts of 64 experts, 16 groups of parts side by side, then the groups in
@@ -330,10 +352,17 @@ template <typename T>
 static hipError_t balance(const BalanceArgs& a, hipStream_t st) {
     with_row<T>(a.e, [&](auto l, auto c) {
         constexpr int LPR = decltype(l)::value, CV = decltype(c)::value;
-        const size_t lds = (size_t)(2 * a.e + 1) * 4;
-        // sixteen waves while their registers suffice
-        constexpr int NT = CV == 1 ? 1024 : CV <= 4 ? 512 : 256;
-        hipLaunchKernelGGL((k_balance_rows<T, LPR, CV, NT>), dim3(a.parts), dim3(NT), lds, st, a);
+        auto launch = [&](auto nt) {
+            constexpr int NT = decltype(nt)::value, SLABS = CV == 1 ? NT / 64 : 1;
+            const size_t lds = ((size_t)(SLABS + 1) * a.e + NT / 64) * 4;
+            hipLaunchKernelGGL((k_balance_rows<T, LPR, CV, NT>), dim3(a.parts), dim3(NT), lds, st, a);
+        };
+        // sixteen waves where there are rows and registers for them
+        constexpr int MOST = CV == 1 ? 1024 : CV <= 4 ? 512 : 256;
+        if (a.n <= 32 * a.parts)
+            launch(std::integral_constant<int, 256>());
+        else
+            launch(std::integral_constant<int, MOST>());
     });
     hipLaunchKernelGGL(k_balance_join, dim3((a.e + 63) / 64), dim3(BJ_NT), 0, st, a);
     return hipGetLastError();

@@ -88,11 +88,6 @@ __global__ __launch_bounds__(BJ_NT) void k_beam_join(BeamArgs p) {
 
 // ---- states
 
-// 16 bytes at any address.
-struct __attribute__((packed, aligned(1))) Any16 {
-    uint32_t w[4];
-};
-
 struct ReorderArgs {
     const char* in;
     char* out;

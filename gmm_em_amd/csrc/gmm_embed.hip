@@ -40,13 +40,6 @@ struct EmbedArgs {
     float scale;
 };
 
-// A vector's first value: one that would pass the row's end is the last whole one instead
-// (the values that it shares with its neighbour are written twice, the same).
-template <int VE>
-__device__ __forceinline__ int whole(int k, int d) {
-    return k + VE <= d || d < VE ? k : d - VE;
-}
-
 // VE values of a row from k = whole(k), or the fewer that a short row has.
 template <typename T>
 __device__ __forceinline__ Raw16 row_get(const T* x, int k, int d) {

@@ -37,60 +37,186 @@ struct QuantArgs {
     int32_t d;
 };
 
-// The integer nearest x / s, ties to the even one, within 127. The quotient's rounding is put
-// right by the remainder, which is exact: |q| s is a few bits longer than s, and x - q s
-// shorter than either.
-__device__ __forceinline__ int quant(float x, float s, float inv) {
+// Integers by adding 1.5 2^23, whose last digit is worth 1: the low byte of the sum's bits.
+constexpr float QR_ROUND = 12582912.f;
+
+// The bits of 1.5 2^23 + the integer nearest x / s, ties to the even one, within 127. The estimate
+// is off by one at most; the remainder of it is exact (|q| s is a few bits longer than s, and
+// x - q s shorter than either) and tells.
+__device__ __forceinline__ uint32_t quant(float x, float s, float inv) {
     float q = rintf(x * inv);
     const float r = fmaf(-q, s, x), a = fabsf(r), half = 0.5f * s;
-    // a tie goes to the even integer; the estimate is off by one at most
-    if (a > half || (a == half && (((int)q) & 1))) q += r > 0.f ? 1.f : -1.f;
-    return (int)fminf(fmaxf(q, -127.f), 127.f);
+    if (a > half || (a == half && ((int)q & 1))) q += r > 0.f ? 1.f : -1.f;
+    return __float_as_uint(fminf(fmaxf(q, -127.f), 127.f) + QR_ROUND);
 }
 
-// A workgroup per row: its largest value, then its integers (the row's second reading comes
-// from the caches).
-constexpr int QR_NT = 256;
+// 16 values of a row, as a thread holds them.
 template <typename T>
-__global__ __launch_bounds__(QR_NT) void k_quant_rows(QuantArgs p) {
-    constexpr int VE = Vec<T>::VE;
-    __shared__ float part[QR_NT / 64];
+struct QuantRun {
+    static constexpr int VE = Vec<T>::VE, NV = 16 / VE;
+    Raw16 r[NV];
+    __device__ __forceinline__ float get(int j) const { return Vec<T>::get(r[j / VE], j % VE); }
+    // from k on; a run that would pass the end is the last whole one (short rows: 0 behind it)
+    __device__ __forceinline__ void load(const T* x, int k, int d) {
+        if (d >= 16) {
+#pragma unroll
+            for (int h = 0; h < NV; ++h) r[h] = *reinterpret_cast<const Raw16*>(x + whole<16>(k, d) + h * VE);
+        } else {
+#pragma unroll
+            for (int h = 0; h < NV; ++h) r[h] = load_zero(x, k + h * VE, (int64_t)d);
+        }
+    }
+    // the largest magnitude; infinite for a NaN
+    __device__ __forceinline__ float most() const {
+        float m = 0.f, sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            m = fmaxf(m, fabsf(get(j)));
+            sum = fmaf(get(j), 0.f, sum);  // NaN with an infinity or a NaN, else 0
+        }
+        return sum == 0.f ? m : INFINITY;
+    }
+    __device__ __forceinline__ void store(int8_t* q, int k, int d, float s, float inv, float up) const {
+        uint32_t b[16];
+        if (inv > 0.f) {  // the same for the row
+            float worst = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float t = fmaf(get(j), inv, QR_ROUND);
+                b[j] = __float_as_uint(t);
+                worst = fmaxf(worst, fabsf(fmaf(-(t - QR_ROUND), s, get(j))));
+            }
+            // a remainder of half a step or more: the estimate may be the other neighbour
+            if (worst >= 0.5f * s || up != 1.f) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) b[j] = quant(get(j) * up, s, inv);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) b[j] = 0;
+        }
+        Any16 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o.w[j] = (b[4 * j] & 255) | (b[4 * j + 1] & 255) << 8 | (b[4 * j + 2] & 255) << 16 | b[4 * j + 3] << 24;
+        if (d >= 16) {
+            *reinterpret_cast<Any16*>(q + whole<16>(k, d)) = o;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 15; ++j)
+                if (k + j < d) q[k + j] = (int8_t)(o.w[j >> 2] >> (8 * (j & 3)));
+        }
+    }
+};
+
+// The largest of a group of LPR lanes.
+template <int LPR>
+__device__ __forceinline__ float lanes_max(float v) {
+    if constexpr (LPR == 64) return wave_max(v);
+    if constexpr (LPR == 16) return max16(v);
+    v = fmaxf(v, lane_move<0xb1>(v));
+    v = fmaxf(v, lane_move<0x4e>(v));
+    return fmaxf(v, lane_move<0x141>(v));
+}
+
+// A row's scale, and what its integers are made with: s, 1 / s (0: they are 0), and the power of two
+// that rows whose 1 / s would leave fp32 are multiplied by first (nothing is rounded by it).
+struct QuantScale {
+    float scale, s, inv, up;
+    __device__ __forceinline__ QuantScale(float m) {
+        scale = m < INFINITY ? m / 127.f : NAN;
+        up = scale < 0x1p-100f ? 0x1p100f : 1.f;
+        s = scale * up;
+        inv = s > 0.f ? 1.f / s : 0.f;
+    }
+};
+
+// LPR lanes per row, which holds it: at most 16 LPR U values.
+// 8192 x 4096 bf16 in QROWS us.
+template <typename T, int LPR, int U>
+__global__ __launch_bounds__(256) void k_quant_rows(QuantArgs p) {
+    constexpr int RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63, gl = lane % LPR, grp = lane / LPR;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t r0 = wave * RPW; r0 < p.n; r0 += (int64_t)gridDim.x * 4 * RPW) {
+        const int64_t row = r0 + grp;
+        const bool in = row < p.n;
+        const T* x = (const T*)p.x + (in ? row : p.n - 1) * p.ldx;
+        QuantRun<T> v[U];
+        float m = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (u * LPR + gl) * 16;
+            if (k < p.d) v[u].load(x, k, p.d);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if ((u * LPR + gl) * 16 < p.d) m = fmaxf(m, v[u].most());
+        const QuantScale c(lanes_max<LPR>(m));
+        if (!in) continue;
+        if (gl == 0) p.scale[row] = c.scale;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (u * LPR + gl) * 16;
+            if (k < p.d) v[u].store(p.q + row * p.ldq, k, p.d, c.s, c.inv, c.up);
+        }
+    }
+}
+
+// A workgroup per longer row. HOLD: its registers hold it, else it is read twice.
+template <typename T, int NT, bool HOLD>
+__global__ __launch_bounds__(NT) void k_quant_long(QuantArgs p) {
+    constexpr int U = HOLD ? 4 : 1;
+    __shared__ float part[NT / 64];
     const int tid = threadIdx.x;
     for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x) {
         const T* x = (const T*)p.x + row * p.ldx;
-        int8_t* q = p.q + row * p.ldq;
+        QuantRun<T> v[U];
         float m = 0.f;
-        bool bad = false;
-        for (int k = tid * VE; k < p.d; k += QR_NT * VE) {
-            const Raw16 r = load_zero(x, k, (int64_t)p.d);
+        for (int k0 = tid * 16; k0 < p.d; k0 += U * NT * 16) {
 #pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                const float v = fabsf(Vec<T>::get(r, j));
-                m = fmaxf(m, v);
-                bad |= !(v < INFINITY);
-            }
+            for (int u = 0; u < U; ++u)
+                if (k0 + u * NT * 16 < p.d) v[u].load(x, k0 + u * NT * 16, p.d);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (k0 + u * NT * 16 < p.d) m = fmaxf(m, v[u].most());
         }
-        m = wave_max(bad ? INFINITY : m);
+        m = wave_max(m);
         if ((tid & 63) == 0) part[tid >> 6] = m;
         __syncthreads();
         m = part[0];
 #pragma unroll
-        for (int w = 1; w < QR_NT / 64; ++w) m = fmaxf(m, part[w]);
-        float s = m < INFINITY ? m / 127.f : NAN;
-        if (tid == 0) p.scale[row] = s;
-        const bool zero = !(s > 0.f);
-        // rows whose 1 / s would leave fp32 are divided 2^100 higher up, where nothing is rounded
-        const float up = s < 0x1p-100f ? 0x1p100f : 1.f;
-        s *= up;
-        const float inv = zero ? 0.f : 1.f / s;
-        for (int k = tid * VE; k < p.d; k += QR_NT * VE) {
-            const Raw16 r = load_zero(x, k, (int64_t)p.d);
+        for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, part[w]);
+        const QuantScale c(m);
+        if (tid == 0) p.scale[row] = c.scale;
+        for (int k0 = tid * 16; k0 < p.d; k0 += U * NT * 16)
 #pragma unroll
-            for (int j = 0; j < VE; ++j)
-                if (k + j < p.d) q[k + j] = zero ? 0 : (int8_t)quant(Vec<T>::get(r, j) * up, s, inv);
-        }
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * NT * 16;
+                if (k >= p.d) break;
+                if (!HOLD) v[u].load(x, k, p.d);
+                v[u].store(p.q + row * p.ldq, k, p.d, c.s, c.inv, c.up);
+            }
         __syncthreads();
     }
+}
+
+template <typename T>
+static void quant_rows(const QuantArgs& a, hipStream_t st) {
+    auto grid = [&](int64_t rows) {
+        const int64_t b = (a.n + rows - 1) / rows, most = (int64_t)1 << 22;
+        return dim3((unsigned)(b < most ? b : most));
+    };
+    if (a.d <= 8 * 16)
+        hipLaunchKernelGGL((k_quant_rows<T, 8, 1>), grid(32), dim3(256), 0, st, a);
+    else if (a.d <= 2 * 16 * 16)
+        hipLaunchKernelGGL((k_quant_rows<T, 16, 2>), grid(16), dim3(256), 0, st, a);
+    else if (a.d <= 4 * 64 * 16)
+        hipLaunchKernelGGL((k_quant_rows<T, 64, 4>), grid(4), dim3(256), 0, st, a);
+    else if (a.d <= 4 * 256 * 16)
+        hipLaunchKernelGGL((k_quant_long<T, 256, true>), grid(1), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_quant_long<T, 1024, false>), grid(1), dim3(1024), 0, st, a);
 }
 
 // ---- products
@@ -109,7 +235,7 @@ __device__ __forceinline__ i32x4 mfma_i8(const Raw16& a, const Raw16& b, i32x4 c
 
 // 16 bytes of a row, 0 at or past `end`.
 __device__ __forceinline__ Raw16 load_bytes(const int8_t* p, int i, int end) {
-    if (i + 16 <= end) return *reinterpret_cast<const Raw16*>(p + i);
+    if (i + 16 <= end) return __builtin_bit_cast(Raw16, *reinterpret_cast<const Any16*>(p + i));
     Raw16 r = {{0u, 0u, 0u, 0u}};
 #pragma unroll
     for (int k = 0; k < 16; ++k)
@@ -122,49 +248,47 @@ __device__ __forceinline__ T scaled_sum(int acc, float qs, float ws) {
     return Vec<T>::store((float)acc * qs * ws);
 }
 
+// 16 codes by up to 16 rows.
 constexpr int QF_W = 4;
-template <typename T, int TT>
+template <typename T>
 __global__ __launch_bounds__(64 * QF_W) void k_quant_few(ProductArgs p) {
-    __shared__ int sh[QF_W][TT][64][4];
-    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 4, i = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t mt = (p.v + 15) / 16, nt = (p.n + 16 * TT - 1) / (16 * TT);
-    for (int64_t item = blockIdx.x; item < mt * nt; item += gridDim.x) {
-        const int64_t c0 = item % mt * 16, r0 = item / mt * (16 * TT);
-        const int8_t* w = p.w + (c0 + i < p.v ? c0 + i : p.v - 1) * p.ldw;
-        const int8_t* q[TT];
-        i32x4 acc[TT];
+    __shared__ i32x4 sh[QF_W][64];
+    const int lane = threadIdx.x & 63, h = lane >> 4, i = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c0 = blockIdx.x * 16;
+    const int8_t* w = p.w + (int64_t)(c0 + i < p.v ? c0 + i : p.v - 1) * p.ldw;
+    const int8_t* q = p.q + (i < p.n ? i : p.n - 1) * p.ldq;
+    i32x4 acc = {0, 0, 0, 0};
+    // steps of 64 integers, step s for wave s % QF_W, in groups whose loads are in flight together
+    constexpr int STEP = 64 * QF_W;
+    int k = wave * 64 + h * 16;
+    auto steps = [&](auto count) {
+        constexpr int U = decltype(count)::value;
+        for (; k - h * 16 + (U - 1) * STEP + 64 <= p.d; k += U * STEP) {
+            Any16 a[U], b[U];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int64_t r = r0 + t * 16 + i;
-            q[t] = p.q + (r < p.n ? r : p.n - 1) * p.ldq;
-            acc[t] = i32x4{0, 0, 0, 0};
-        }
-        for (int k = wave * 64 + h * 16; k - h * 16 < p.d; k += 64 * QF_W) {
-            const Raw16 a = load_bytes(w, k, p.d);
-#pragma unroll
-            for (int t = 0; t < TT; ++t) acc[t] = mfma_i8(a, load_bytes(q[t], k, p.d), acc[t]);
-        }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) *(i32x4*)sh[wave][t][lane] = acc[t];
-        __syncthreads();
-        // lane (h, i) of a tile holds codes 4 h .. 4 h + 3 of row i
-        for (int t = wave; t < TT; t += QF_W) {
-            const int64_t r = r0 + t * 16 + i;
-            if (r >= p.n) continue;
-            const float qs = p.q_scale[r];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t c = c0 + 4 * h + j;
-                if (c >= p.v) continue;
-                int s = 0;
-#pragma unroll
-                for (int x = 0; x < QF_W; ++x) s += sh[x][t][lane][j];
-                ((T*)p.y)[r * p.ldy + c] = scaled_sum<T>(s, qs, p.w_scale[c]);
+            for (int u = 0; u < U; ++u) {
+                a[u] = *reinterpret_cast<const Any16*>(w + k + u * STEP);
+                b[u] = *reinterpret_cast<const Any16*>(q + k + u * STEP);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                acc = mfma32(__builtin_bit_cast(i32x4, a[u]), __builtin_bit_cast(i32x4, b[u]), acc);
         }
-        __syncthreads();
-    }
+    };
+    steps(std::integral_constant<int, 8>());
+    steps(std::integral_constant<int, 2>());
+    steps(std::integral_constant<int, 1>());
+    if (k - h * 16 < p.d) acc = mfma_i8(load_bytes(w, k, p.d), load_bytes(q, k, p.d), acc);
+    sh[wave][lane] = acc;
+    __syncthreads();
+    // lane (h, i) holds codes 4 h .. 4 h + 3 of row i: one of them for each wave
+    const int c = c0 + 4 * h + wave;
+    if (i >= p.n || c >= p.v) return;
+    int sum = 0;
+#pragma unroll
+    for (int x = 0; x < QF_W; ++x) sum += ((const int*)&sh[x][lane])[wave];
+    ((T*)p.y)[i * p.ldy + c] = scaled_sum<T>(sum, p.q_scale[i], p.w_scale[c]);
 }
 
 // ---- tiles
@@ -174,7 +298,7 @@ constexpr int64_t QT_MAX_LD = (int64_t)1 << 23;  // 256 rows span at most 2^31 b
 constexpr size_t QT_PACK_BYTES = (size_t)256 << 20;   // rows of q laid out at a time
 constexpr size_t QT_SPLIT_BYTES = (size_t)128 << 20;  // partial sums of a split product
 constexpr int QT_MAX_SPLIT = 16;
-constexpr int QT_FEW_ROWS = 64;
+constexpr int QT_FEW_ROWS = 16;
 
 struct TilesArgs {
     GemmIn in;           // a: codes, b: rows of q
@@ -334,21 +458,13 @@ static QuantPlan quant_plan(int64_t n, int32_t d, int32_t v, bool pack_q, bool p
 
 // Costs of the tiles (gmm_tiles.h), a step of 128 integers.
 constexpr TileCost QUANT_COST[4] = {
-    {256, 256, 256, 1.42f, 6.f}, {192, 256, 256, 1.12f, 6.f}, {128, 128, 512, 0.92f, 4.f},
-    {64, 64, 1024, 0.55f, 3.f}};
+    {256, 256, 256, 1.75f, 6.f, 1.25f}, {192, 256, 256, 1.35f, 6.f, 1.0f}, {128, 128, 512, 1.13f, 4.f, 0.7f},
+    {64, 64, 1024, 0.82f, 3.f, 0.25f}};
 
 template <typename T>
 static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) {
     if (a.n <= QT_FEW_ROWS) {
-        const int64_t mt = (a.v + 15) / 16;
-        auto grid = [&](int rows) {
-            const int64_t b = mt * ((a.n + rows - 1) / rows), most = (int64_t)1 << 22;
-            return dim3((unsigned)(b < most ? b : most));
-        };
-        if (a.n <= 16)
-            hipLaunchKernelGGL((k_quant_few<T, 1>), grid(16), dim3(64 * QF_W), 0, st, a);
-        else
-            hipLaunchKernelGGL((k_quant_few<T, 4>), grid(64), dim3(64 * QF_W), 0, st, a);
+        hipLaunchKernelGGL((k_quant_few<T>), dim3((unsigned)((a.v + 15) / 16)), dim3(64 * QF_W), 0, st, a);
         return hipGetLastError();
     }
     const bool pq = !quant_direct(a.q, a.d, a.ldq), pw = !quant_direct(a.w, a.d, a.ldw);
@@ -420,12 +536,10 @@ int gmm_quantize_rows(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t 
     if (n > 0 && (!x || !q || !scale)) return GMM_E_INVALID;
     if (n == 0) return GMM_OK;
     const QuantArgs a{x, q, scale, n, ldx, ldq, d};
-    const int64_t most = (int64_t)1 << 22;
-    const dim3 grid((unsigned)(n < most ? n : most));
     if (dtype == GMM_F32)
-        hipLaunchKernelGGL((k_quant_rows<float>), grid, dim3(QR_NT), 0, (hipStream_t)stream, a);
+        quant_rows<float>(a, (hipStream_t)stream);
     else
-        hipLaunchKernelGGL((k_quant_rows<uint16_t>), grid, dim3(QR_NT), 0, (hipStream_t)stream, a);
+        quant_rows<uint16_t>(a, (hipStream_t)stream);
     return hipGetLastError() == hipSuccess ? GMM_OK : GMM_E_HIP;
 }
 

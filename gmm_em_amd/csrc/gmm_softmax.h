@@ -29,6 +29,11 @@ struct __attribute__((packed, aligned(2))) Raw16 {
     uint32_t w[4];
 };
 
+// 16 bytes at any address.
+struct __attribute__((packed, aligned(1))) Any16 {
+    uint32_t w[4];
+};
+
 __device__ __forceinline__ float bf16_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 // round to nearest even; NaN stays a quiet NaN
 __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
@@ -71,6 +76,13 @@ struct Vec<uint16_t> {
     }
     static __device__ __forceinline__ uint16_t store(float v) { return (uint16_t)f32_to_bf16(v); }
 };
+
+// A vector's first value: one that would pass the row's end is the last whole one instead
+// (the values that it shares with its neighbour are written twice, the same).
+template <int VE>
+__device__ __forceinline__ int whole(int k, int d) {
+    return k + VE <= d || d < VE ? k : d - VE;
+}
 
 // VE values as 16 bytes; bf16 by the hardware's conversion of pairs (round to nearest even).
 template <typename T>
