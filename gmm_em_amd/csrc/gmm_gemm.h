@@ -84,13 +84,20 @@ struct Gemm {
     // LDS byte offset of piece p of row r within an operand's step
     static __device__ __forceinline__ int at(int r, int p) { return r * 128 + ((p ^ (r & 7)) << 4); }
 
+    // Integer sums: A's rows lie turned within each 32, so that a lane's four rows of two blocks are
+    // eight neighbours (16 bytes of bf16 to write): row 16 b + 4 h + q is the operand's 8 h + 4 b + q.
+    static constexpr bool TURN = std::is_same<Acc, i32x4>::value;
+
     // copies BR rows of one step: wave w takes every NT / 64-th group of 8 rows
-    template <int BR>
+    template <int BR, bool TURNED = false>
     static __device__ __forceinline__ void copy(__amdgpu_buffer_rsrc_t rs, uint32_t row_bytes,
                                                 unsigned char* dst, int wave, int lane) {
         // row (8 grp + r) & 7 == r: the piece that belongs at place p is p ^ r
         const int r = lane >> 3, p = lane & 7;
-        const uint32_t off = (uint32_t)(wave * 8 + r) * row_bytes + (uint32_t)((p ^ r) << 4);
+        static_assert(!TURNED || NT / 64 % 4 == 0, "a wave's groups lie alike within 32 rows");
+        const int first = TURNED ? 32 * (wave >> 2) + 16 * (wave & 1) + 8 * (r >> 2) + 4 * (wave >> 1 & 1) + (r & 3)
+                                 : wave * 8 + r;
+        const uint32_t off = (uint32_t)first * row_bytes + (uint32_t)((p ^ r) << 4);
 #pragma unroll
         for (int g = 0; g < BR / 8 / (NT / 64); ++g)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -149,7 +156,7 @@ struct Gemm {
     __device__ __forceinline__ void issue(const GemmIn& in, int m, int n, bool real, unsigned char* d) {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        copy<BM>(__builtin_amdgcn_make_buffer_rsrc((void*)next_a, (short)0, real ? bytes_a : 0, BUF_RSRC_WORD3),
+        copy<BM, TURN>(__builtin_amdgcn_make_buffer_rsrc((void*)next_a, (short)0, real ? bytes_a : 0, BUF_RSRC_WORD3),
                  (uint32_t)in.lda * 2, d, wave, lane);
         const uint16_t* pb = next_b;
         if constexpr (TB) {  // a wave's own panel: uniform, but not to the compiler
@@ -293,6 +300,8 @@ struct Gemm {
 
     // row of this lane's first of four rows of blocks x, its column in blocks y
     static __device__ __forceinline__ int row(int x) {
+        if constexpr (TURN)
+            return (threadIdx.x >> 6) / WN * TM * 16 + x / 2 * 32 + 8 * ((threadIdx.x & 63) >> 4) + 4 * (x & 1);
         return ((threadIdx.x >> 6) / WN * TM + x) * 16 + 4 * ((threadIdx.x & 63) >> 4);
     }
     static __device__ __forceinline__ int col(int y) {

@@ -309,10 +309,12 @@ struct TilesArgs {
     int32_t* part;       // [split][rows][codes]
 };
 
-template <typename T>
-struct __attribute__((packed, aligned(sizeof(T)))) Four {
-    T v[4];
+// Values of neighbouring codes, at any element's address.
+template <typename T, int N>
+struct __attribute__((packed, aligned(sizeof(T)))) Run {
+    T v[N];
 };
+constexpr int QT_RUN = 8;  // codes that a lane has of two blocks
 
 template <typename T, int BM, int BN, int WM, int WN, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN) void k_quant_tiles(TilesArgs p) {
@@ -331,48 +333,55 @@ __global__ __launch_bounds__(64 * WM * WN) void k_quant_tiles(TilesArgs p) {
             if (r >= p.in.n) continue;
             int32_t* o = p.part + ((int64_t)blockIdx.y * p.in.n + r) * p.in.m;
 #pragma unroll
-            for (int x = 0; x < G::TM; ++x) {
+            for (int x = 0; x < G::TM; x += 2) {
                 const int c = m0 + G::row(x);
-                if (c + 4 <= p.in.m) {
-                    *(Four<int32_t>*)(o + c) = __builtin_bit_cast(Four<int32_t>, g.acc[x][y]);
+                Run<int32_t, QT_RUN> v;
+#pragma unroll
+                for (int q = 0; q < QT_RUN; ++q) v.v[q] = g.acc[x + q / 4][y][q % 4];
+                if (c + QT_RUN <= p.in.m) {
+                    *(Run<int32_t, QT_RUN>*)(o + c) = v;
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (c + q < p.in.m) o[c + q] = g.acc[x][y][q];
+                    for (int q = 0; q < QT_RUN; ++q)
+                        if (c + q < p.in.m) o[c + q] = v.v[q];
                 }
             }
         }
     } else {
+        constexpr int VE = Vec<T>::VE;
         gemm_walk<i32x4, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
-            Four<float> ws[G::TM];
-#pragma unroll
-            for (int x = 0; x < G::TM; ++x) {
-                const int c = m0 + G::row(x);
-                if (c + 4 <= p.in.m) {
-                    ws[x] = *(const Four<float>*)(p.w_scale + c);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) ws[x].v[q] = c + q < p.in.m ? p.w_scale[c + q] : 0.f;
-                }
-            }
+            float qs[G::TN];
 #pragma unroll
             for (int y = 0; y < G::TN; ++y) {
                 const int r = n0 + G::col(y);
-                if (r >= p.in.n) continue;
-                const float qs = p.q_scale[r];
-                T* o = (T*)p.y + (int64_t)r * p.ldy;
+                qs[y] = p.q_scale[r < p.in.n ? r : p.in.n - 1];
+            }
 #pragma unroll
-                for (int x = 0; x < G::TM; ++x) {
-                    const int c = m0 + G::row(x);
-                    Four<T> u;
+            for (int x = 0; x < G::TM; x += 2) {
+                const int c = m0 + G::row(x);
+                const bool full = c + QT_RUN <= p.in.m;
+                Run<float, QT_RUN> ws;
+                if (full) {
+                    ws = *(const Run<float, QT_RUN>*)(p.w_scale + c);
+                } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) u.v[q] = scaled_sum<T>(g.acc[x][y][q], qs, ws[x].v[q]);
-                    if (c + 4 <= p.in.m) {
-                        *(Four<T>*)(o + c) = u;
+                    for (int q = 0; q < QT_RUN; ++q) ws.v[q] = c + q < p.in.m ? p.w_scale[c + q] : 0.f;
+                }
+#pragma unroll
+                for (int y = 0; y < G::TN; ++y) {
+                    const int r = n0 + G::col(y);
+                    if (r >= p.in.n) continue;
+                    T* o = (T*)p.y + (int64_t)r * p.ldy + c;
+                    float v[QT_RUN];
+#pragma unroll
+                    for (int q = 0; q < QT_RUN; ++q) v[q] = (float)g.acc[x + q / 4][y][q % 4] * qs[y] * ws.v[q];
+                    if (full) {
+#pragma unroll
+                        for (int q = 0; q < QT_RUN; q += VE) *(Raw16*)(o + q) = pack16<T>(v + q);
                     } else {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (c + q < p.in.m) o[c + q] = u.v[q];
+                        for (int q = 0; q < QT_RUN; ++q)
+                            if (c + q < p.in.m) o[q] = Vec<T>::store(v[q]);
                     }
                 }
             }
@@ -459,7 +468,7 @@ static QuantPlan quant_plan(int64_t n, int32_t d, int32_t v, bool pack_q, bool p
 // Costs of the tiles (gmm_tiles.h), a step of 128 integers.
 constexpr TileCost QUANT_COST[4] = {
     {256, 256, 256, 1.75f, 6.f, 1.25f}, {192, 256, 256, 1.35f, 6.f, 1.0f}, {128, 128, 512, 1.13f, 4.f, 0.7f},
-    {64, 64, 1024, 0.82f, 3.f, 0.25f}};
+    {64, 64, 1024, 0.82f, 3.f, 0.4f}};
 
 template <typename T>
 static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) {
