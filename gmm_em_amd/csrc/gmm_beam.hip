@@ -224,6 +224,14 @@ int gmm_beam_step(const void* logits, int64_t b, int32_t w, int32_t v, int64_t l
     s.beam_score = scores;
     s.beam_last = last;
     s.beam_end = end;
+    if (w == 1 && score_plan(b, v, q.per).parts == 1) {
+        // one beam: its list is the result (8 codes of 4 x 16384 fp32: BEAM1 us, with the merge BEAM2)
+        s.top_logprob = score;
+        s.beam_parent = parent;
+        s.beam_code = code;
+        s.beam_m = m;
+        return launch_score(s, dtype, ws + q.o_score, st) == hipSuccess ? GMM_OK : GMM_E_HIP;
+    }
     if (launch_score(s, dtype, ws + q.o_score, st) != hipSuccess) return GMM_E_HIP;
     const BeamArgs a{scores, last, s.top_idx, s.top_logprob, b, w, m, q.per, end, parent, code, score};
     const int64_t most = (int64_t)1 << 20;

@@ -40,6 +40,8 @@ struct ScoreArgs {
     const float* beam_score;
     const int32_t* beam_last;
     int32_t beam_end;
+    int32_t *beam_parent, *beam_code;  // one beam a search: its list is the result (top_logprob: scores)
+    int32_t beam_m;                    // places of the result, m at most of which a row fills
 };
 
 // A beam goes on with the codes of its row: its score is finite and its last code is not the end.

@@ -48,6 +48,15 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
+// Place `at` of the result of a search with one beam.
+__device__ __forceinline__ void beam_out(const ScoreArgs& p, int64_t row, float score, int code, int at) {
+    if (at >= p.beam_m) return;
+    const bool there = score > -INFINITY;  // NaN is no continuation
+    p.beam_parent[row * p.beam_m + at] = there ? 0 : -1;
+    p.beam_code[row * p.beam_m + at] = there ? code : -1;
+    p.top_logprob[row * p.beam_m + at] = there ? score : -INFINITY;
+}
+
 // A part of a row, read in vectors: vector j of NT * SC_U threads' worth starts at value
 // j VE; one that would pass the end is the last whole one instead, and the
 // values that belong to others are -inf in it.
@@ -84,7 +93,13 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int64_t item = blockIdx.x; item < p.n * p.parts; item += gridDim.x) {
         const int64_t row = item / p.parts;
-        if (BEAM && (!beam_alive(p.beam_score, row) || beam_ended(p.beam_last, p.beam_end, row))) continue;
+        if constexpr (BEAM) {
+            const bool alive = beam_alive(p.beam_score, row);
+            if (!alive || beam_ended(p.beam_last, p.beam_end, row)) {
+                if (p.beam_parent) beam_out(p, row, alive && tid == 0 ? p.beam_score[row] : -INFINITY, p.beam_end, tid);
+                continue;
+            }
+        }
         const int part = (int)(item - row * p.parts);
         const int64_t i0 = (int64_t)part * p.part_len;
         const RowPart<T> x{(const T*)p.x + row * p.ldl + i0,
@@ -230,7 +245,10 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
             }
         }
         if (wave == 0) {
-            if (p.parts == 1) {
+            if (BEAM && p.beam_parent) {
+                const float lp = (top.v - st.m) - logf(st.s);
+                beam_out(p, row, top.v > -INFINITY ? p.beam_score[row] + lp : -INFINITY, top.i, lane);
+            } else if (p.parts == 1) {
                 score_out(p, row, st, target_logit<T>(p, row, lane), top.v, top.i, lane);
             } else {
                 if (lane == 0) p.part[item] = ScorePart{st.m, st.s, st.a};

@@ -283,21 +283,24 @@ class Scores(NamedTuple):
     top_logprob: Optional[torch.Tensor]  # (N, m) float32
 
 
+_DTYPES = {torch.float32: GMM_F32, torch.bfloat16: GMM_BF16}
+
+
 def _rows2(t, name):
     """(dtype code, leading dimension) of a 2-D row-major device tensor."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor with unit stride along columns")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    (n, d), (step, unit) = t.shape, t.stride()
+    if unit != 1 and d > 1:
+        raise ValueError(f"{name} must be a 2-D tensor with unit stride along columns")
+    if n > 1 and step < d:
         raise ValueError(f"the rows of {name} must not overlap")
-    if t.dtype == torch.float32:
-        dt = GMM_F32
-    elif t.dtype == torch.bfloat16:
-        dt = GMM_BF16
-    else:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float32 or bfloat16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return dt, max(t.stride(0), t.shape[1])
+    return dt, step if step > d else d
 
 
 def _int32(*sizes):
@@ -350,7 +353,7 @@ class _On:
     def __enter__(self):
         index = self.device.index
         self.guard = None
-        if torch.cuda.current_device() != index:
+        if torch._C._cuda_getDevice() != index:
             self.guard = torch.cuda.device(self.device)
             self.guard.__enter__()
         return torch._C._cuda_getCurrentRawStream(index)
@@ -509,8 +512,8 @@ def moe_layer(x, w_in, w_out, gate=None, m: int = 2, share_all: bool = False, id
 def _new_like_rows(out, n, d, x, name="out"):
     """(tensor, leading dimension) of an (n, d) result in x's type: the caller's, or a new one."""
     if out is None:
-        out = torch.empty((n, d), dtype=x.dtype, device=x.device)
-    elif tuple(out.shape) != (n, d) or out.dtype != x.dtype or out.device != x.device:
+        return torch.empty((n, d), dtype=x.dtype, device=x.device), d
+    if tuple(out.shape) != (n, d) or out.dtype != x.dtype or out.device != x.device:
         raise ValueError(f"{name} must be an ({n}, {d}) tensor of the operand's type and device")
     return out, _rows2(out, name)[1]
 
@@ -555,13 +558,16 @@ def _bytes2(t, name):
     """Leading dimension of a 2-D row-major int8 device tensor."""
     if t.dtype != torch.int8:
         raise TypeError(f"{name} must be int8")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor with unit stride along columns")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    (n, d), (step, unit) = t.shape, t.stride()
+    if unit != 1 and d > 1:
+        raise ValueError(f"{name} must be a 2-D tensor with unit stride along columns")
+    if n > 1 and step < d:
         raise ValueError(f"the rows of {name} must not overlap")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return max(t.stride(0), t.shape[1])
+    return step if step > d else d
 
 
 def quantize_rows(x):
@@ -591,7 +597,8 @@ def quantized_product(q, q_scale, weight, weight_scale, dtype=torch.bfloat16, ou
     v = weight.shape[0]
     if weight.shape[1] != d or weight.device != q.device:
         raise ValueError("q (N, D) and weight (V, D) must agree in D and device")
-    if dtype not in (torch.float32, torch.bfloat16):
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise TypeError("dtype must be float32 or bfloat16")
     _int32(d, v)
     dev = q.device
@@ -599,10 +606,11 @@ def quantized_product(q, q_scale, weight, weight_scale, dtype=torch.bfloat16, ou
     wsc = _row(weight_scale, v, "weight_scale", torch.float32, dev)
     ws, nb = _scratch(lib.gmm_quantized_product_workspace_bytes(n, d, v), ws, dev)
     if out is None:
-        out = torch.empty((n, v), dtype=dtype, device=dev)
+        out, ldy = torch.empty((n, v), dtype=dtype, device=dev), v
     elif tuple(out.shape) != (n, v) or out.dtype != dtype or out.device != dev:
         raise ValueError(f"out must be an ({n}, {v}) tensor of dtype on q's device")
-    dt, ldy = _rows2(out, "out")
+    else:
+        ldy = _rows2(out, "out")[1]
     with _On(dev) as stream:
         _check(lib.gmm_quantized_product(q.data_ptr(), n, d, ldq, qs, weight.data_ptr(), v, ldw, wsc,
                                          out.data_ptr(), ldy, dt, ws.data_ptr(), nb, stream))
@@ -619,8 +627,8 @@ class Beams(NamedTuple):
 
 def _grid2(t, shape, name, dtype, device):
     """Address of a contiguous 2-D tensor of a given shape."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on the operand's device")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {shape} tensor of {dtype} on the operand's device")
     return t.data_ptr()
 
 
@@ -659,6 +667,12 @@ def beam_step(logits, scores, last=None, end: int = -1, m: Optional[int] = None,
 
 def _state(t, dim, name):
     """(outer, outer stride, row stride, row bytes) of a tensor as rows along ``dim``, in bytes."""
+    if t.is_contiguous():
+        row = t.element_size()
+        for k in t.shape[dim + 1:]:
+            row *= k
+        step = row * t.shape[dim]
+        return t.numel() * t.element_size() // step, step, row, row
     size, stride, es = list(t.shape), list(t.stride()), t.element_size()
     inner = 1
     for k in range(t.dim() - 1, dim, -1):

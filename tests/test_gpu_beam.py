@@ -140,6 +140,24 @@ def test_ended_and_dead_beams(ops, v, dtype):
         assert all(torch.equal(p, q) for p, q in zip(a, ops.beam_step(x, s)))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("v", [5, 9000, 200_000])
+def test_searches_of_one_beam(ops, v, dtype):
+    g = _gen(v + 1)
+    for m in (1, 8, 16):
+        x = _logits(9, v, dtype, g, True)
+        scores = -2 * torch.rand(9, 1, generator=g, device=DEV)
+        last = torch.zeros(9, 1, dtype=torch.int32, device=DEV)
+        last[1], last[2], scores[2], scores[3] = 4, 4, -INF, float("nan")  # ended, ended but dead, dead
+        x[1:4] = float("nan")
+        x[4, 1], x[5, 2], x[6] = float("nan"), INF, -INF
+        x[7], x[7, 3] = -INF, 0.5
+        r, _ = _check(ops, x, scores, last, 4, m=m)
+        assert r.code[1, 0] == 4 and r.score[1, 0] == scores[1, 0]
+        assert r.parent[1:8, 1:].eq(-1).all() and r.parent[2:7].eq(-1).all()
+        assert r.code[7, 0] == 3 and abs(r.score[7, 0] - scores[7, 0]) <= 2.0 ** -22
+
+
 def test_order_of_equal_scores(ops):
     # equal logits everywhere: beams in order, then codes
     for v, m in ((4, 10), (5000, 16), (200_000, 3)):
