@@ -4,7 +4,7 @@
 //   loss = E sum_c f_c P_c        dz_c = g E / rows p_c (f_c - sum_c' f_c' p_c')
 // (f is constant for the gradient: picks have none).
 //
-// One pass over the logits: 16, 32 or 64 lanes hold a row, so that a wave has up to four
+// One pass over the logits: 8, 16, 32 or 64 lanes hold a row, so that a wave has up to eight
 // rows at once and a lane always the same experts: their sums of p stay in its registers. A
 // workgroup leaves its sums and counts in the workspace and k_balance_join adds them in order.
 #include <hip/hip_runtime.h>
@@ -52,6 +52,11 @@ struct BalanceArgs {
 // over groups of LPR lanes
 template <int LPR>
 __device__ __forceinline__ float group_reduce_max(float v) {
+    if constexpr (LPR == 8) {
+        v = fmaxf(v, lane_move<0xb1>(v));
+        v = fmaxf(v, lane_move<0x4e>(v));
+        return fmaxf(v, lane_move<0x141>(v));
+    }
     v = max16(v);
     if (LPR > 16) v = fmaxf(v, __shfl_xor(v, 16));
     if (LPR > 32) v = fmaxf(v, __shfl_xor(v, 32));
@@ -59,6 +64,11 @@ __device__ __forceinline__ float group_reduce_max(float v) {
 }
 template <int LPR>
 __device__ __forceinline__ float group_reduce_sum(float v) {
+    if constexpr (LPR == 8) {
+        v += lane_move<0xb1>(v);
+        v += lane_move<0x4e>(v);
+        return v + lane_move<0x141>(v);
+    }
     v = sum16(v);
     if (LPR > 16) v += __shfl_xor(v, 16);
     if (LPR > 32) v += __shfl_xor(v, 32);
@@ -83,7 +93,9 @@ struct RouterRow {
     }
 };
 
-template <typename T, int LPR, int CV, int NT>
+// A wave takes 64 / LPR rows at once and U such groups in one go (their loads, and the next
+// go's, are in flight together).
+template <typename T, int LPR, int CV, int NT, int U>
 __global__ __launch_bounds__(NT) void k_balance_rows(BalanceArgs p) {
     using Row = RouterRow<T, LPR, CV>;
     constexpr int C = Row::C, RPW = 64 / LPR, W = NT / 64;
@@ -100,57 +112,65 @@ __global__ __launch_bounds__(NT) void k_balance_rows(BalanceArgs p) {
     float acc[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) acc[j] = 0.f;
-    const int64_t step = (int64_t)p.parts * W * RPW;
+    const int64_t step = (int64_t)p.parts * W * RPW * U;
     const uint64_t mine = (LPR == 64 ? ~uint64_t(0) : (uint64_t(1) << (LPR & 63)) - 1) << (grp * LPR);
     struct Next {
         Raw16 z[CV];
         int pick;
-    };
+    } next[U];
     auto fetch = [&](int64_t r0) {
-        const int64_t row = r0 + grp < p.n ? r0 + grp : p.n - 1;
-        Next x;
-        x.pick = gl < p.m ? p.idx[row * p.m + gl] : -1;
-        Row::fetch((const T*)p.z + row * p.ldz, p.e, gl, x.z);
-        return x;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            int64_t row = r0 + u * RPW + grp;
+            row = row < p.n ? row : p.n - 1;
+            next[u].pick = gl < p.m ? p.idx[row * p.m + gl] : -1;
+            Row::fetch((const T*)p.z + row * p.ldz, p.e, gl, next[u].z);
+        }
     };
-    int64_t r0 = ((int64_t)blockIdx.x * W + wave) * RPW;
-    Next next;
-    if (r0 < p.n) next = fetch(r0);
+    int64_t r0 = ((int64_t)blockIdx.x * W + wave) * RPW * U;
+    if (r0 < p.n) fetch(r0);
     for (; r0 < p.n; r0 += step) {
-        const int64_t row = r0 + grp;
-        const bool in = row < p.n;
-        Row x;
-        x.take(next.z);
-        const int pick = in ? next.pick : -1;
-        if (r0 + step < p.n) next = fetch(r0 + step);
-        const bool picked = pick >= 0 && pick < p.e;
-        const bool live = (__builtin_amdgcn_ballot_w64(picked) & mine) != 0;
-        if (picked) atomicAdd(&cnt[pick], 1);
-        rows += __popcll(__builtin_amdgcn_ballot_w64(gl == 0 && live));
-        float m = -3.402823466e38f, s = 0.f;
+        Row x[U];
+        int pick[U];
 #pragma unroll
-        for (int j = 0; j < C; ++j) m = fmaxf(m, x.v[j]);
-        m = group_reduce_max<LPR>(m);
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            x.v[j] = exp_neg(x.v[j] - m);
-            s += x.v[j];
+        for (int u = 0; u < U; ++u) {
+            x[u].take(next[u].z);
+            pick[u] = r0 + u * RPW + grp < p.n ? next[u].pick : -1;
         }
-        s = group_reduce_sum<LPR>(s);
-        const bool none = s == 0.f;  // every logit -inf
-        if (live) {
-            const float inv = none ? 0.f : __builtin_amdgcn_rcpf(s);
+        if (r0 + step < p.n) fetch(r0 + step);
 #pragma unroll
-            for (int j = 0; j < C; ++j) acc[j] = fmaf(x.v[j], inv, acc[j]);
-        }
-        if (gl == 0 && in) {
-            p.norm[2 * row] = !live ? INFINITY : none ? -INFINITY : (s == s ? m : NAN);
-            p.norm[2 * row + 1] = !live || none ? 0.f : __builtin_amdgcn_logf(s) * 0.693147180559945309f;
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = r0 + u * RPW + grp;
+            const bool picked = pick[u] >= 0 && pick[u] < p.e;
+            const bool live = (__builtin_amdgcn_ballot_w64(picked) & mine) != 0;
+            if (picked) atomicAdd(&cnt[pick[u]], 1);
+            rows += __popcll(__builtin_amdgcn_ballot_w64(gl == 0 && live));
+            float m = -3.402823466e38f, s = 0.f;
+#pragma unroll
+            for (int j = 0; j < C; ++j) m = fmaxf(m, x[u].v[j]);
+            m = group_reduce_max<LPR>(m);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                x[u].v[j] = exp_neg(x[u].v[j] - m);
+                s += x[u].v[j];
+            }
+            s = group_reduce_sum<LPR>(s);
+            const bool none = s == 0.f;  // every logit -inf
+            if (live) {
+                const float inv = none ? 0.f : __builtin_amdgcn_rcpf(s);
+#pragma unroll
+                for (int j = 0; j < C; ++j) acc[j] = fmaf(x[u].v[j], inv, acc[j]);
+            }
+            if (gl == 0 && row < p.n) {
+                p.norm[2 * row] = !live ? INFINITY : none ? -INFINITY : (s == s ? m : NAN);
+                p.norm[2 * row + 1] = !live || none ? 0.f : __builtin_amdgcn_logf(s) * 0.693147180559945309f;
+            }
         }
     }
     // the rows of a wave, then its workgroup's waves in order
 #pragma unroll
     for (int j = 0; j < C; ++j) {
+        if (LPR < 16) acc[j] += __shfl_xor(acc[j], 8);
         if (LPR < 32) acc[j] += __shfl_xor(acc[j], 16);
         if (LPR < 64) acc[j] += __shfl_xor(acc[j], 32);
     }
@@ -256,7 +276,9 @@ __global__ __launch_bounds__(BJ_NT) void k_balance_join(BalanceArgs p) {
 }
 
 constexpr int BG_W = 4;
-template <typename T, int LPR, int CV>
+// Workgroups, at most: the preparation of f is paid by several rows.
+constexpr int64_t bg_most(int cv) { return cv == 1 ? 1024 : cv <= 4 ? 512 : 256; }
+template <typename T, int LPR, int CV, int U>
 __global__ __launch_bounds__(64 * BG_W) void k_balance_grad(BalanceArgs p) {
     using Row = RouterRow<T, LPR, CV>;
     constexpr int C = Row::C, RPW = 64 / LPR, VE = Vec<T>::VE;
@@ -273,52 +295,61 @@ __global__ __launch_bounds__(64 * BG_W) void k_balance_grad(BalanceArgs p) {
     struct Next {
         Raw16 z[CV];
         float m, logs;
-    };
+    } next[U];
     auto fetch = [&](int64_t r0) {
-        const int64_t row = r0 + grp < p.n ? r0 + grp : p.n - 1;
-        Next x;
-        x.m = p.norm[2 * row];
-        x.logs = p.norm[2 * row + 1];
-        Row::fetch((const T*)p.z + row * p.ldz, p.e, gl, x.z);
-        return x;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            int64_t row = r0 + u * RPW + grp;
+            row = row < p.n ? row : p.n - 1;
+            next[u].m = p.norm[2 * row];
+            next[u].logs = p.norm[2 * row + 1];
+            Row::fetch((const T*)p.z + row * p.ldz, p.e, gl, next[u].z);
+        }
     };
     // p.dz may be p.z: the rows fetched ahead are other ones than those written
-    const int64_t step = (int64_t)gridDim.x * BG_W * RPW;
-    int64_t r0 = ((int64_t)blockIdx.x * BG_W + wave) * RPW;
-    Next next;
-    if (r0 < p.n) next = fetch(r0);
+    const int64_t step = (int64_t)gridDim.x * BG_W * RPW * U;
+    int64_t r0 = ((int64_t)blockIdx.x * BG_W + wave) * RPW * U;
+    if (r0 < p.n) fetch(r0);
     for (; r0 < p.n; r0 += step) {
-        const int64_t row = r0 + grp;
-        Row x;
-        x.take(next.z);
-        const float m = next.m, logs = next.logs;
-        if (r0 + step < p.n) next = fetch(r0 + step);
-        const bool off = m == INFINITY || m == -INFINITY;  // left out, or no logit above -inf
-        float s = 0.f;
+        Row x[U];
+        float m[U], logs[U];
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-            x.v[j] = off ? 0.f : exp_neg((x.v[j] - m) - logs);
-            s = fmaf(f[j], x.v[j], s);
+        for (int u = 0; u < U; ++u) {
+            x[u].take(next[u].z);
+            m[u] = next[u].m;
+            logs[u] = next[u].logs;
         }
-        s = group_reduce_sum<LPR>(s);
-        if (row >= p.n) continue;
-        T* out = (T*)p.dz + row * p.lddz;
+        if (r0 + step < p.n) fetch(r0 + step);
 #pragma unroll
-        for (int q = 0; q < CV; ++q) {
-            const int64_t i = (int64_t)(q * LPR + gl) * VE;
-            float w[VE];
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = r0 + u * RPW + grp;
+            const bool off = m[u] == INFINITY || m[u] == -INFINITY;  // left out, or no logit above -inf
+            float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < VE; ++k) {
-                const int j = q * VE + k;
-                w[k] = off ? 0.f : by * (x.v[j] * (f[j] - s));
+            for (int j = 0; j < C; ++j) {
+                x[u].v[j] = off ? 0.f : exp_neg((x[u].v[j] - m[u]) - logs[u]);
+                s = fmaf(f[j], x[u].v[j], s);
             }
-            const Raw16 o = pack16<T>(w);
-            if (i + VE <= p.e) {
-                *reinterpret_cast<Raw16*>(out + i) = o;
-            } else {
+            s = group_reduce_sum<LPR>(s);
+            if (row >= p.n) continue;
+            T* out = (T*)p.dz + row * p.lddz;
 #pragma unroll
-                for (int k = 0; k < VE; ++k)
-                    if (i + k < p.e) out[i + k] = Vec<T>::store(Vec<T>::get(o, k));
+            for (int q = 0; q < CV; ++q) {
+                const int64_t i = (int64_t)(q * LPR + gl) * VE;
+                float w[VE];
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    const int j = q * VE + k;
+                    w[k] = off ? 0.f : by * (x[u].v[j] * (f[j] - s));
+                }
+                const Raw16 o = pack16<T>(w);
+                if (i + VE <= p.e) {
+                    *reinterpret_cast<Raw16*>(out + i) = o;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < VE; ++k)
+                        if (i + k < p.e) out[i + k] = Vec<T>::store(Vec<T>::get(o, k));
+                }
             }
         }
     }
@@ -336,12 +367,14 @@ static bool balance_fits(int64_t n, int32_t e, int32_t m) {
     return e <= BAL_MAX_EXPERTS && n <= 0x7fffffff / m;  // counts are 32-bit
 }
 
-// Lanes of a row and vectors of a lane: as few lanes as hold the row in one vector each.
+// Lanes of a row and vectors of a lane: as few lanes as hold the row in one vector each (and its
+// m picks, one each).
 template <typename T, typename F>
-static void with_row(int e, F f) {
+static void with_row(int e, int m, F f) {
     constexpr int VE = Vec<T>::VE;
     using std::integral_constant;
-    if (e <= 16 * VE) f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (e <= 8 * VE && m <= 8) f(integral_constant<int, 8>(), integral_constant<int, 1>());
+    else if (e <= 16 * VE) f(integral_constant<int, 16>(), integral_constant<int, 1>());
     else if (e <= 32 * VE) f(integral_constant<int, 32>(), integral_constant<int, 1>());
     else if (e <= 64 * VE) f(integral_constant<int, 64>(), integral_constant<int, 1>());
     else if (e <= 256 * VE) f(integral_constant<int, 64>(), integral_constant<int, 4>());
@@ -350,19 +383,20 @@ static void with_row(int e, F f) {
 
 template <typename T>
 static hipError_t balance(const BalanceArgs& a, hipStream_t st) {
-    with_row<T>(a.e, [&](auto l, auto c) {
+    with_row<T>(a.e, a.m, [&](auto l, auto c) {
         constexpr int LPR = decltype(l)::value, CV = decltype(c)::value;
-        auto launch = [&](auto nt) {
-            constexpr int NT = decltype(nt)::value, SLABS = CV == 1 ? NT / 64 : 1;
+        auto launch = [&](auto nt, auto groups) {
+            constexpr int NT = decltype(nt)::value, U = decltype(groups)::value, SLABS = CV == 1 ? NT / 64 : 1;
             const size_t lds = ((size_t)(SLABS + 1) * a.e + NT / 64) * 4;
-            hipLaunchKernelGGL((k_balance_rows<T, LPR, CV, NT>), dim3(a.parts), dim3(NT), lds, st, a);
+            hipLaunchKernelGGL((k_balance_rows<T, LPR, CV, NT, U>), dim3(a.parts), dim3(NT), lds, st, a);
         };
-        // sixteen waves where there are rows and registers for them
+        using std::integral_constant;
+        // sixteen waves and several groups where there are rows and registers for them
         constexpr int MOST = CV == 1 ? 1024 : CV <= 4 ? 512 : 256;
         if (a.n <= 32 * a.parts)
-            launch(std::integral_constant<int, 256>());
+            launch(integral_constant<int, 256>(), integral_constant<int, 1>());
         else
-            launch(std::integral_constant<int, MOST>());
+            launch(integral_constant<int, MOST>(), integral_constant<int, CV == 1 ? 4 : 1>());
     });
     hipLaunchKernelGGL(k_balance_join, dim3((a.e + 63) / 64), dim3(BJ_NT), 0, st, a);
     return hipGetLastError();
@@ -370,11 +404,19 @@ static hipError_t balance(const BalanceArgs& a, hipStream_t st) {
 
 template <typename T>
 static hipError_t balance_grad(const BalanceArgs& a, hipStream_t st) {
-    with_row<T>(a.e, [&](auto l, auto c) {
+    with_row<T>(a.e, 1, [&](auto l, auto c) {
         constexpr int LPR = decltype(l)::value, CV = decltype(c)::value;
-        const int64_t per = BG_W * (64 / LPR), blocks = (a.n + per - 1) / per;
-        hipLaunchKernelGGL((k_balance_grad<T, LPR, CV>), dim3((unsigned)(blocks < 2048 ? blocks : 2048)),
-                           dim3(64 * BG_W), 0, st, a);
+        auto launch = [&](auto groups) {
+            constexpr int U = decltype(groups)::value;
+            const int64_t per = BG_W * (64 / LPR) * U, blocks = (a.n + per - 1) / per;
+            hipLaunchKernelGGL((k_balance_grad<T, LPR, CV, U>), dim3((unsigned)(blocks < bg_most(CV) ? blocks : bg_most(CV))),
+                               dim3(64 * BG_W), 0, st, a);
+        };
+        using std::integral_constant;
+        if (CV > 1 || a.n <= 256 * BG_W * (64 / LPR))
+            launch(integral_constant<int, 1>());
+        else
+            launch(integral_constant<int, CV == 1 ? 4 : 1>());
     });
     return hipGetLastError();
 }

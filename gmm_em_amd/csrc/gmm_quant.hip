@@ -419,16 +419,17 @@ struct PackArgs {
     } o[2];
     int32_t d, dp;
 };
+// Eight lanes copy a row's piece of a panel, a wave eight rows: 1 KB in one piece.
 __global__ __launch_bounds__(256) void k_quant_pack(PackArgs p) {
     const auto o = p.o[blockIdx.y];
-    const int per = p.dp / 16;
-    const int64_t total = o.rows * per;
-    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < total; j += (int64_t)gridDim.x * 256) {
-        const int64_t r = j / per;
-        const int k = (int)(j - r * per) * 16;
-        const Raw16 v = load_bytes(o.x + r * o.ld, k, p.d);
-        *(uint4*)(o.out + ((k / QT_STEP) * o.rows + r) * QT_STEP + k % QT_STEP) =
-            uint4{v.w[0], v.w[1], v.w[2], v.w[3]};
+    const int lane = threadIdx.x & 63;
+    for (int64_t r = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 8 + (lane >> 3); r < o.rows;
+         r += (int64_t)gridDim.x * 32) {
+        const int8_t* x = o.x + r * o.ld;
+        int8_t* to = o.out + r * QT_STEP + (lane & 7) * 16;
+#pragma unroll 4
+        for (int k = (lane & 7) * 16; k < p.dp; k += QT_STEP, to += o.rows * QT_STEP)
+            *(Raw16*)to = load_bytes(x, k, p.d);
     }
 }
 
@@ -497,7 +498,7 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
         if (pq) p.o[1] = {a.q + r0 * a.ldq, rows, a.ldq, (int8_t*)ws + q.o_q};
         const int64_t most = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
         if (most > 0) {
-            const int64_t b = (most * (q.dp / 16) + 255) / 256;
+            const int64_t b = (most + 31) / 32;
             hipLaunchKernelGGL(k_quant_pack, dim3((unsigned)(b < 65536 ? b : 65536), 2), dim3(256), 0, st, p);
         }
         t.in.b = (const uint16_t*)(pq ? (const int8_t*)ws + q.o_q : a.q + r0 * a.ldq);
