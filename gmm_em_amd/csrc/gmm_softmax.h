@@ -287,6 +287,7 @@ __device__ __forceinline__ void top_rank(const float* cv, const int* ci, int cnt
         const int i = ci[c];
         if (v == -INFINITY) continue;
         int rank = 0;
+#pragma unroll 8
         for (int q = 0; q < cnt; ++q) rank += top_before(cv[q], ci[q], v, i);
         if (rank < m) {
             ov[rank] = v;
