@@ -509,6 +509,31 @@ def moe_layer(x, w_in, w_out, gate=None, m: int = 2, share_all: bool = False, id
     return y, idx, resp
 
 
+def _call(fn, device, *args):
+    """An entry point on ``device``'s current stream, with the device made current."""
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != GMM_OK:
+        raise GmmError(rc)
+
+
+_UNUSED = {}  # a buffer for each device that no kernel touches
+
+
+def _scratch_or_none(need, ws, device):
+    """:func:`_scratch` for entry points that need 256 bytes where they use none of them."""
+    if need == 256 and ws is None:
+        ws = _UNUSED.get(device)
+        if ws is None:
+            ws = _UNUSED[device] = torch.empty(256, dtype=torch.uint8, device=device)
+        return ws, 256
+    return _scratch(need, ws, device)
+
+
 def _new_like_rows(out, n, d, x, name="out"):
     """(tensor, leading dimension) of an (n, d) result in x's type: the caller's, or a new one."""
     if out is None:
@@ -531,8 +556,7 @@ def embed(table, codes, scale: float = 1.0, out=None):
     n = codes.numel()
     c = _row(codes, n, "codes", torch.int32, dev)
     out, ldo = _new_like_rows(out, n, d, table)
-    with _On(dev) as stream:
-        _check(lib.gmm_embed(table.data_ptr(), v, d, ldt, dt, c, n, scale, out.data_ptr(), ldo, stream))
+    _call(lib.gmm_embed, dev, table.data_ptr(), v, d, ldt, dt, c, n, scale, out.data_ptr(), ldo)
     return out
 
 
@@ -546,11 +570,10 @@ def embed_backward(grad, codes, v: int, scale: float = 1.0, out=None, ws=None):
     _int32(d, v)
     dev = grad.device
     c = _row(codes, n, "codes", torch.int32, dev)
-    ws, nb = _scratch(lib.gmm_embed_backward_workspace_bytes(n, d, v), ws, dev)
+    ws, nb = _scratch_or_none(lib.gmm_embed_backward_workspace_bytes(n, d, v), ws, dev)
     out, ldt = _new_like_rows(out, v, d, grad)
-    with _On(dev) as stream:
-        _check(lib.gmm_embed_backward(grad.data_ptr(), n, d, ldg, dt, c, v, scale, out.data_ptr(), ldt,
-                                      ws.data_ptr(), nb, stream))
+    _call(lib.gmm_embed_backward, dev, grad.data_ptr(), n, d, ldg, dt, c, v, scale, out.data_ptr(), ldt,
+          ws.data_ptr(), nb)
     return out
 
 
@@ -580,8 +603,7 @@ def quantize_rows(x):
     _int32(d)
     q = torch.empty((n, d), dtype=torch.int8, device=x.device)
     scale = torch.empty(n, dtype=torch.float32, device=x.device)
-    with _On(x.device) as stream:
-        _check(lib.gmm_quantize_rows(x.data_ptr(), n, d, ldx, dt, q.data_ptr(), d, scale.data_ptr(), stream))
+    _call(lib.gmm_quantize_rows, x.device, x.data_ptr(), n, d, ldx, dt, q.data_ptr(), d, scale.data_ptr())
     return q, scale
 
 
@@ -604,16 +626,15 @@ def quantized_product(q, q_scale, weight, weight_scale, dtype=torch.bfloat16, ou
     dev = q.device
     qs = _row(q_scale, n, "q_scale", torch.float32, dev)
     wsc = _row(weight_scale, v, "weight_scale", torch.float32, dev)
-    ws, nb = _scratch(lib.gmm_quantized_product_workspace_bytes(n, d, v), ws, dev)
+    ws, nb = _scratch_or_none(lib.gmm_quantized_product_workspace_bytes(n, d, v), ws, dev)
     if out is None:
         out, ldy = torch.empty((n, v), dtype=dtype, device=dev), v
     elif tuple(out.shape) != (n, v) or out.dtype != dtype or out.device != dev:
         raise ValueError(f"out must be an ({n}, {v}) tensor of dtype on q's device")
     else:
         ldy = _rows2(out, "out")[1]
-    with _On(dev) as stream:
-        _check(lib.gmm_quantized_product(q.data_ptr(), n, d, ldq, qs, weight.data_ptr(), v, ldw, wsc,
-                                         out.data_ptr(), ldy, dt, ws.data_ptr(), nb, stream))
+    _call(lib.gmm_quantized_product, dev, q.data_ptr(), n, d, ldq, qs, weight.data_ptr(), v, ldw, wsc,
+          out.data_ptr(), ldy, dt, ws.data_ptr(), nb)
     return out
 
 
@@ -658,10 +679,8 @@ def beam_step(logits, scores, last=None, end: int = -1, m: Optional[int] = None,
     i32 = torch.int32
     out = Beams(torch.empty((b, m), dtype=i32, device=dev), torch.empty((b, m), dtype=i32, device=dev),
                 torch.empty((b, m), dtype=torch.float32, device=dev))
-    with _On(dev) as stream:
-        _check(lib.gmm_beam_step(logits.data_ptr(), b, w, v, ldl, dt, sc, la, end, m, scale,
-                                 out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), nb,
-                                 stream))
+    _call(lib.gmm_beam_step, dev, logits.data_ptr(), b, w, v, ldl, dt, sc, la, end, m, scale,
+          out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), nb)
     return out
 
 
@@ -701,31 +720,32 @@ def beam_reorder(state, parent, w: int, dim: int = 0, out=None):
     """
     if not state.is_cuda:
         raise ValueError("state must be a device tensor")
-    if state.is_complex() or state.is_quantized or state.layout != torch.strided:
+    if state.is_complex() or state.is_quantized or state.layout is not torch.strided:
         raise TypeError("state must be a plain strided tensor")
-    if not -state.dim() <= dim < state.dim():
+    dims = state.dim()
+    if not -dims <= dim < dims:
         raise ValueError("dim must be a dim of state")
-    dim %= state.dim()
+    if dim < 0:
+        dim += dims
     if parent.dim() != 2:
         raise ValueError("parent must be a (B, m) tensor")
     dev = state.device
     b, m = parent.shape
     pa = _grid2(parent, (b, m), "parent", torch.int32, dev)
-    if state.shape[dim] != b * w:
+    shape = list(state.shape)
+    if shape[dim] != b * w:
         raise ValueError("state must have B * w rows along dim")
     _int32(w, m)
-    shape = (*state.shape[:dim], b * m, *state.shape[dim + 1:])
+    shape[dim] = b * m
     if out is None:
         out = torch.empty(shape, dtype=state.dtype, device=dev)
-    elif tuple(out.shape) != shape or out.dtype != state.dtype or out.device != dev:
+    elif list(out.shape) != shape or out.dtype != state.dtype or out.device != dev:
         raise ValueError("out must have state's shape with B * m rows, its type and device")
     if out.numel() == 0:
         return out
     outer, so, sr, nb = _state(state, dim, "state")
-    outer2, oo, orow, _ = _state(out, dim, "out")
-    with _On(dev) as stream:
-        _check(lib.gmm_beam_reorder(state.data_ptr(), outer, so, b, w, sr, nb, pa, m, out.data_ptr(), oo, orow,
-                                    stream))
+    _, oo, orow, _ = _state(out, dim, "out")
+    _call(lib.gmm_beam_reorder, dev, state.data_ptr(), outer, so, b, w, sr, nb, pa, m, out.data_ptr(), oo, orow)
     return out
 
 
@@ -759,10 +779,9 @@ def balance_loss(logits, idx, ws=None) -> Balance:
     out = Balance(torch.empty((), dtype=f32, device=dev), torch.empty(e, dtype=torch.int32, device=dev),
                   torch.empty(2, dtype=torch.int64, device=dev), torch.empty(e, dtype=f32, device=dev),
                   torch.empty((n, 2), dtype=f32, device=dev))
-    with _On(dev) as stream:
-        _check(lib.gmm_balance_loss(logits.data_ptr(), n, e, ldz, dt, ix, m, out[0].data_ptr(),
-                                    out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-                                    out[4].data_ptr(), ws.data_ptr(), nb, stream))
+    _call(lib.gmm_balance_loss, dev, logits.data_ptr(), n, e, ldz, dt, ix, m, out[0].data_ptr(),
+          out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(),
+          ws.data_ptr(), nb)
     return out
 
 
@@ -782,9 +801,8 @@ def balance_loss_backward(logits, counts, totals, norm, g_loss=None, out=None):
     if g_loss is not None and (g_loss.dtype != torch.float32 or g_loss.numel() != 1 or g_loss.device != dev):
         raise ValueError("g_loss must be a float32 tensor of one value on the device of the logits")
     out, ldo = _new_like_rows(out, n, e, logits)
-    with _On(dev) as stream:
-        _check(lib.gmm_balance_loss_backward(logits.data_ptr(), n, e, ldz, dt, c, t, norm.data_ptr(),
-                                             _addr(g_loss), out.data_ptr(), ldo, stream))
+    _call(lib.gmm_balance_loss_backward, dev, logits.data_ptr(), n, e, ldz, dt, c, t, norm.data_ptr(),
+          _addr(g_loss), out.data_ptr(), ldo)
     return out
 
 
