@@ -225,7 +225,7 @@ int gmm_beam_step(const void* logits, int64_t b, int32_t w, int32_t v, int64_t l
     s.beam_last = last;
     s.beam_end = end;
     if (w == 1 && score_plan(b, v, q.per).parts == 1) {
-        // one beam: its list is the result (8 codes of 4 x 16384 fp32: BEAM1 us, with the merge BEAM2)
+        // one beam: its list is the result (8 codes of 4 x 16384 fp32: 13.7 us a call, with the merge 15.7)
         s.top_logprob = score;
         s.beam_parent = parent;
         s.beam_code = code;

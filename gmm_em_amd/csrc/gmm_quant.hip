@@ -4,12 +4,16 @@
 // Products of 8-bit integers and their sums are exact in 32 bits, so the order of the sum
 // and the kernel that makes it leave no trace in y.
 //
-// k_quant_few: few rows. The product is the reading of w: 16 weight rows by 16 rows of q
+// k_quant_few: up to 16 rows. The product is the reading of w: 16 weight rows by 16 rows of q
 // per matrix instruction, both straight from memory, the contracted axis split over the
-// waves and joined in LDS.
-// k_quant_tiles: more rows, by the tiles of gmm_gemm.h (codes are the tile rows, so that a lane
-// has four neighbouring codes of a row to write). Operands whose rows are not 16-byte
-// aligned, or not whole steps of 128 long, are laid out in panels first.
+// waves and joined in LDS. 16 x 4096 x 16384 in 17.8 us (67 MB of w: 3.8 TB/s).
+// k_quant_tiles: more rows, by the tiles of gmm_gemm.h (codes are the tile rows, turned so that a
+// lane has eight neighbouring codes of a row to write: 16 bytes of bf16). Operands whose rows
+// are not 16-byte aligned, or not whole steps of 128 long, are laid out in panels first.
+// 8192^3 in 470 us (2340 TOP/s) and 8192 x 4096 x 16384 in 465 (bf16 results); with operands of
+// zeros 8192^3 takes 344: on other numbers the chip's power sets the pace. Not kept: stores of four
+// codes (500 and, 8192 x 768 x 16384, 164 against 136), blocks of 32 x 32 (508 at 8192^3), four
+// waves of 128 x 128 (770), stores past the caches (607).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -132,7 +136,7 @@ struct QuantScale {
 };
 
 // LPR lanes per row, which holds it: at most 16 LPR U values.
-// 8192 x 4096 bf16 in QROWS us.
+// 8192 x 4096 in 28 us (bf16, 3.6 TB/s) and 30 us (fp32, 5.6 TB/s).
 template <typename T, int LPR, int U>
 __global__ __launch_bounds__(256) void k_quant_rows(QuantArgs p) {
     constexpr int RPW = 64 / LPR;
@@ -298,6 +302,8 @@ constexpr int64_t QT_MAX_LD = (int64_t)1 << 23;  // 256 rows span at most 2^31 b
 constexpr size_t QT_PACK_BYTES = (size_t)256 << 20;   // rows of q laid out at a time
 constexpr size_t QT_SPLIT_BYTES = (size_t)128 << 20;  // partial sums of a split product
 constexpr int QT_MAX_SPLIT = 16;
+// Rows for k_quant_few. The tiles take 32 rows of 4096 against 16384 codes in 19 us, 2 or 4 blocks of
+// its 16 rows a workgroup took 33.
 constexpr int QT_FEW_ROWS = 16;
 
 struct TilesArgs {
@@ -466,7 +472,9 @@ static QuantPlan quant_plan(int64_t n, int32_t d, int32_t v, bool pack_q, bool p
     return q;
 }
 
-// Costs of the tiles (gmm_tiles.h), a step of 128 integers.
+// Costs of the tiles (gmm_tiles.h), a step of 128 integers. Calls with each tile in their order (us):
+// 8192^3 470, 532, 592, 867; 4096^3 58, 84, 72, 102; 2048^3 31, 25, 15, 17; 300 x 4096 x 4096 48, 40,
+// 28, 13 (the least is picked in each); 128 x 8192 x 4096 81, 65, 47, 33, as picked, split, 19.
 constexpr TileCost QUANT_COST[4] = {
     {256, 256, 256, 1.75f, 6.f, 1.25f}, {192, 256, 256, 1.35f, 6.f, 1.0f}, {128, 128, 512, 1.13f, 4.f, 0.7f},
     {64, 64, 1024, 0.82f, 3.f, 0.4f}};
@@ -566,9 +574,8 @@ int gmm_quantized_product(const int8_t* q, int64_t n, int32_t d, int64_t ldq, co
     if (n < 0 || n > SC_MAX_ROWS || d < 1 || v < 1 || ldq < d || ldw < d || ldy < v) return GMM_E_INVALID;
     if (d > QU_MAX_DIM || v > QU_MAX_CODES) return GMM_E_UNSUPPORTED;
     if (n > 0 && (!q || !q_scale || !w || !w_scale || !y)) return GMM_E_INVALID;
-    if (!workspace || workspace_bytes < gmm_quantized_product_workspace_bytes(n, d, v) ||
-        (uintptr_t)workspace % 256 != 0)
-        return GMM_E_WORKSPACE;
+    const QuantPlan plan = quant_plan(n, d, v, !quant_direct(q, d, ldq), !quant_direct(w, d, ldw));
+    if (!workspace || workspace_bytes < plan.bytes || (uintptr_t)workspace % 256 != 0) return GMM_E_WORKSPACE;
     if (n == 0) return GMM_OK;
     const ProductArgs a{q, w, q_scale, w_scale, y, n, ldq, ldw, ldy, d, v};
     const hipError_t e = dtype == GMM_F32 ? quant_product<float>(a, (char*)workspace, (hipStream_t)stream)

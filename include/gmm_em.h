@@ -361,7 +361,7 @@ int gmm_embed(const void* table, int32_t v, int32_t d, int64_t ldt, int32_t dtyp
  *   d_table[c] = scale * sum of grad[r] over the rows r with codes[r] = c
  * in grad's type, rounded once from fp32 sums; a code that no row has gets 0, rows whose code is
  * not in [0, v) add nothing. The rows are sorted by code, so every sum has one order (bitwise
- * reproducible) and a code that most rows have costs no more than others. d_table (v x d, leading
+ * reproducible) and the work is cut evenly however often a code occurs. d_table (v x d, leading
  * dimension ldt >= d) must not overlap grad. n = 0 sets d_table to 0. n < 2^31, d and v as for
  * gmm_embed (GMM_E_UNSUPPORTED beyond). The workspace (device, 256-byte aligned) has
  * gmm_embed_backward_workspace_bytes(n, d, v) bytes (0: invalid or unsupported sizes). */
@@ -389,7 +389,9 @@ int gmm_quantize_rows(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t 
  * head's logits in 8 bits, read by gmm_logits_score and gmm_beam_step. Any alignment; offsets are
  * 64-bit. n may be 0; n <= 2^40, d < 2^17, v <= 2^22 (GMM_E_UNSUPPORTED beyond). The workspace
  * (device, 256-byte aligned) has gmm_quantized_product_workspace_bytes bytes (0: invalid or
- * unsupported sizes). */
+ * unsupported sizes); it is bounded in n. Operands that are 16-byte aligned with a leading dimension
+ * that is a multiple of 16 and d a multiple of 128 are read in place, others (of more than 16 rows
+ * of q) are laid out in the workspace first. */
 size_t gmm_quantized_product_workspace_bytes(int64_t n, int32_t d, int32_t v);
 int gmm_quantized_product(const int8_t* q, int64_t n, int32_t d, int64_t ldq, const float* q_scale,
                           const int8_t* w, int32_t v, int64_t ldw, const float* w_scale, void* y,
