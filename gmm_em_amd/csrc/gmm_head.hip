@@ -685,8 +685,8 @@ __global__ __launch_bounds__(256) void k_head_sum(GradOut p) {
 // 768 x 4096 50 and 44 (49, 44), 300 x 256 x 5000 37 and 26 (36, 26); fp32: 2048 x 768 x 8192 315 and
 // 309 (323, 326), 777 x 100 x 1001 35 and 34 (34, 32).
 constexpr TileCost TILE_COST[4] = {
-    {256, 256, 256, 1.42f, 6.f, 1.42f}, {192, 256, 256, 1.12f, 6.f, 1.12f},
-    {128, 128, 512, 0.92f, 4.f, 0.92f}, {64, 64, 1024, 0.55f, 3.f, 0.55f}};
+    {256, 256, 256, 1.42f, 6.f}, {192, 256, 256, 1.12f, 6.f}, {128, 128, 512, 0.92f, 4.f},
+    {64, 64, 1024, 0.55f, 3.f}};
 
 
 // Workspace of a head call: operands that need laying out, then the chunk's

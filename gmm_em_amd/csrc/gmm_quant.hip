@@ -429,13 +429,13 @@ struct PackArgs {
 __global__ __launch_bounds__(256) void k_quant_pack(PackArgs p) {
     const auto o = p.o[blockIdx.y];
     const int lane = threadIdx.x & 63;
-    for (int64_t r = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 8 + (lane >> 3); r < o.rows;
-         r += (int64_t)gridDim.x * 32) {
-        const int8_t* x = o.x + r * o.ld;
-        int8_t* to = o.out + r * QT_STEP + (lane & 7) * 16;
-#pragma unroll 4
-        for (int k = (lane & 7) * 16; k < p.dp; k += QT_STEP, to += o.rows * QT_STEP)
-            *(Raw16*)to = load_bytes(x, k, p.d);
+    const uint32_t panels = (uint32_t)p.dp / QT_STEP, items = (uint32_t)((o.rows + 7) / 8) * panels;
+    for (uint32_t i = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < items; i += gridDim.x * 4) {
+        const uint32_t group = i / panels, panel = i - group * panels;
+        const int64_t r = (int64_t)group * 8 + (lane >> 3);
+        if (r >= o.rows) continue;
+        const int k = (int)panel * QT_STEP + (lane & 7) * 16;
+        *(Raw16*)(o.out + (panel * o.rows + r) * QT_STEP + (lane & 7) * 16) = load_bytes(o.x + r * o.ld, k, p.d);
     }
 }
 
@@ -472,12 +472,39 @@ static QuantPlan quant_plan(int64_t n, int32_t d, int32_t v, bool pack_q, bool p
     return q;
 }
 
-// Costs of the tiles (gmm_tiles.h), a step of 128 integers. Calls with each tile in their order (us):
-// 8192^3 470, 532, 592, 867; 4096^3 58, 84, 72, 102; 2048^3 31, 25, 15, 17; 300 x 4096 x 4096 48, 40,
-// 28, 13 (the least is picked in each); 128 x 8192 x 4096 81, 65, 47, 33, as picked, split, 19.
-constexpr TileCost QUANT_COST[4] = {
-    {256, 256, 256, 1.75f, 6.f, 1.25f}, {192, 256, 256, 1.35f, 6.f, 1.0f}, {128, 128, 512, 1.13f, 4.f, 0.7f},
-    {64, 64, 1024, 0.82f, 3.f, 0.4f}};
+// The tile and the split that take least time by a model of it: the chip's workgroups take
+// (fixed + steps * per_step) for each full load of the CUs; fewer workgroups per CU take their share of a
+// step's time, but not less than `alone`. A split adds the writing and reading of its sums.
+// Calls with each tile in their order (us, steps of 128 integers): 8192^3 470, 532, 592, 867; 4096^3
+// 58, 84, 72, 102; 2048^3 31, 25, 15, 17; 777 x 1024 x 5001 24, 19.5, 15.5, 13.8; 300 x 4096 x 4096 48,
+// 40, 28, 13 (the least is picked in each); 128 x 8192 x 4096 81, 65, 47, 33, as picked, split, 19.
+struct QuantCost {
+    int bm, bn, per_cu;
+    float per_step, fixed, alone;  // microseconds
+};
+constexpr QuantCost QUANT_COST[4] = {
+    {256, 256, 1, 1.75f, 6.f, 1.75f}, {192, 256, 1, 1.35f, 6.f, 1.35f}, {128, 128, 2, 1.13f, 4.f, 0.7f},
+    {64, 64, 4, 0.82f, 3.f, 0.4f}};
+static Choice quant_choice(int64_t m, int64_t n, int64_t steps) {
+    Choice best{0, 1};
+    double least = 1e300;
+    for (int t = 0; t < 4; ++t) {
+        const QuantCost& c = QUANT_COST[t];
+        const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
+        for (int s = 1; s <= QT_MAX_SPLIT && s <= steps; ++s) {
+            if (s > 1 && (size_t)s * m * n * 4 > QT_SPLIT_BYTES) break;
+            const double load = (double)((tiles * s + 255) / 256) / c.per_cu, each = (double)((steps + s - 1) / s);
+            const double part = c.per_step * load > c.alone ? c.per_step * load : c.alone;
+            double us = load >= 1.0 ? load * (c.fixed + c.per_step * each) : c.fixed + part * each;
+            if (s > 1) us += 4.0 + (double)m * n * 8 * s / 4.0e6;
+            if (us < least) {
+                least = us;
+                best = Choice{t, s};
+            }
+        }
+    }
+    return best;
+}
 
 template <typename T>
 static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) {
@@ -506,7 +533,7 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
         if (pq) p.o[1] = {a.q + r0 * a.ldq, rows, a.ldq, (int8_t*)ws + q.o_q};
         const int64_t most = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
         if (most > 0) {
-            const int64_t b = (most + 31) / 32;
+            const int64_t b = ((most + 7) / 8 * (q.dp / QT_STEP) + 3) / 4;
             hipLaunchKernelGGL(k_quant_pack, dim3((unsigned)(b < 65536 ? b : 65536), 2), dim3(256), 0, st, p);
         }
         t.in.b = (const uint16_t*)(pq ? (const int8_t*)ws + q.o_q : a.q + r0 * a.ldq);
@@ -515,7 +542,7 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
         t.in.n = (int32_t)rows;
         t.q_scale = a.q_scale + r0;
         t.y = (T*)a.y + r0 * a.ldy;
-        const Choice c = choose_tile(QUANT_COST, a.v, rows, q.dp / QT_STEP, QT_MAX_SPLIT, QT_SPLIT_BYTES);
+        const Choice c = quant_choice(a.v, rows, q.dp / QT_STEP);
         t.split = c.split;
         with_tile(c.tile, [&](auto id) {
             using C = Tile<decltype(id)::value>;
@@ -527,7 +554,7 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
                 hipLaunchKernelGGL((k_quant_tiles<T, C::BM, C::BN, C::WM, C::WN, true>), dim3(grid, c.split), block, 0,
                                    st, t);
             } else {
-                const unsigned most_at_once = (unsigned)QUANT_COST[decltype(id)::value].at_once;
+                const unsigned most_at_once = 256u * QUANT_COST[decltype(id)::value].per_cu;
                 if (grid > most_at_once) grid = most_at_once;
                 hipLaunchKernelGGL((k_quant_tiles<T, C::BM, C::BN, C::WM, C::WN, false>), dim3(grid), block, 0, st, t);
             }

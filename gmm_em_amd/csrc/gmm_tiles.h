@@ -33,12 +33,10 @@ struct Tile<3> {
 
 // The tile and the split of the contracted axis that take least time by a
 // model of it: rounds of workgroups over the chip, each of a fixed part and a
-// part per step, and the writing and reading of a split's partial sums. A last round that
-// does not fill the chip takes its share of a step's time, but not less than `alone`.
+// part per step, and the writing and reading of a split's partial sums.
 struct TileCost {
     int bm, bn, at_once;  // workgroups on the chip
     float per_step, fixed;  // microseconds
-    float alone;            // a step, for one workgroup per CU
 };
 
 struct Choice {
@@ -53,10 +51,8 @@ inline Choice choose_tile(const TileCost* costs, int64_t m, int64_t n, int64_t s
         const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
         for (int s = 1; s <= max_split && s <= steps; ++s) {
             if (s > 1 && (size_t)s * m * n * 4 > split_bytes) break;
-            const int64_t rounds = tiles * s / c.at_once, rest = tiles * s - rounds * c.at_once;
-            const double part = c.per_step * (double)((rest + 255) / 256 * 256) / c.at_once;
-            const double last = part > c.alone ? part : c.alone, each = (double)((steps + s - 1) / s);
-            double us = rounds * (c.fixed + c.per_step * each) + (rest > 0 ? c.fixed + last * each : 0.0);
+            const int64_t rounds = (tiles * s + c.at_once - 1) / c.at_once;
+            double us = rounds * (c.fixed + c.per_step * (double)((steps + s - 1) / s));
             if (s > 1) us += 4.0 + (double)m * n * 8 * s / 4.0e6;
             if (us < least) {
                 least = us;
