@@ -537,7 +537,7 @@ def _scratch_or_none(need, ws, device):
 def _new_like_rows(out, n, d, x, name="out"):
     """(tensor, leading dimension) of an (n, d) result in x's type: the caller's, or a new one."""
     if out is None:
-        return torch.empty((n, d), dtype=x.dtype, device=x.device), d
+        return x.new_empty((n, d)), d
     if tuple(out.shape) != (n, d) or out.dtype != x.dtype or out.device != x.device:
         raise ValueError(f"{name} must be an ({n}, {d}) tensor of the operand's type and device")
     return out, _rows2(out, name)[1]
@@ -676,9 +676,8 @@ def beam_step(logits, scores, last=None, end: int = -1, m: Optional[int] = None,
     sc = _grid2(scores, (b, w), "scores", torch.float32, dev)
     la = None if last is None else _grid2(last, (b, w), "last", torch.int32, dev)
     ws, nb = _scratch(lib.gmm_beam_step_workspace_bytes(b, w, v, m), ws, dev)
-    i32 = torch.int32
-    out = Beams(torch.empty((b, m), dtype=i32, device=dev), torch.empty((b, m), dtype=i32, device=dev),
-                torch.empty((b, m), dtype=torch.float32, device=dev))
+    parent = torch.empty((b, m), dtype=torch.int32, device=dev)
+    out = Beams(parent, torch.empty_like(parent), scores.new_empty((b, m)))
     _call(lib.gmm_beam_step, dev, logits.data_ptr(), b, w, v, ldl, dt, sc, la, end, m, scale,
           out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), nb)
     return out
@@ -737,14 +736,15 @@ def beam_reorder(state, parent, w: int, dim: int = 0, out=None):
         raise ValueError("state must have B * w rows along dim")
     _int32(w, m)
     shape[dim] = b * m
-    if out is None:
-        out = torch.empty(shape, dtype=state.dtype, device=dev)
+    new = out is None
+    if new:
+        out = state.new_empty(shape)
     elif list(out.shape) != shape or out.dtype != state.dtype or out.device != dev:
         raise ValueError("out must have state's shape with B * m rows, its type and device")
     if out.numel() == 0:
         return out
     outer, so, sr, nb = _state(state, dim, "state")
-    _, oo, orow, _ = _state(out, dim, "out")
+    oo, orow = (b * m * nb, nb) if new else _state(out, dim, "out")[1:3]
     _call(lib.gmm_beam_reorder, dev, state.data_ptr(), outer, so, b, w, sr, nb, pa, m, out.data_ptr(), oo, orow)
     return out
 

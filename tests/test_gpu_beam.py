@@ -193,6 +193,15 @@ def test_strides(ops, dtype):
     assert e.parent.shape == (0, 3)
 
 
+@pytest.mark.parametrize("w", [1, 2])
+def test_more_searches_than_workgroups(ops, w):
+    g = _gen(40 + w)
+    b, v = 1_100_003, 8
+    x = _logits(b * w, v, F32, g)
+    scores = -4 * torch.rand(b, w, generator=g, device=DEV)
+    _check(ops, x, scores, m=2)
+
+
 def test_offsets_beyond_32_bits(ops):
     g = _gen(4)
     b, w, v = 4200, 16, 33_000  # 2.2e9 logits

@@ -130,3 +130,36 @@ def test_decoding_step_in_a_graph(example, ops, result):
         torch.cuda.synchronize()
         for a, e in zip(got, step()):
             assert torch.equal(a, e)
+
+
+def test_calls_at_once_on_two_streams(ops):
+    # each call has a workspace of its own: neither sees the other
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+
+    def inputs():
+        grad = torch.randn(30_000, 256, generator=g, device=DEV)
+        codes = torch.randint(0, 500, (30_000,), generator=g, device=DEV, dtype=torch.int32)
+        z = torch.randn(30_000, 200, generator=g, device=DEV)
+        logits = torch.randn(64, 20_000, generator=g, device=DEV)
+        x, w = torch.randn(300, 500, generator=g, device=DEV), torch.randn(700, 500, generator=g, device=DEV)
+        return grad, codes, z, z.topk(3, 1).indices.to(torch.int32), logits, torch.zeros(8, 8, device=DEV), x, w
+
+    def work(grad, codes, z, idx, logits, scores, x, w):
+        r = ops.balance_loss(z, idx)
+        return (ops.embed_backward(grad, codes, 500), *r, ops.balance_loss_backward(z, r.counts, r.totals, r.norm),
+                *ops.beam_step(logits, scores), ops.quantized_product(*ops.quantize_rows(x), *ops.quantize_rows(w)))
+
+    data = [inputs(), inputs()]
+    want = [work(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for k, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[k].append(work(*data[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for result in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(result, want[k]))
