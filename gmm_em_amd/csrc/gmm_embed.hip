@@ -17,8 +17,9 @@
 // instead of all this (k_embed_few): the first row of a code adds the others.
 // The sum is bound by reading the rows and writing the table, everything else by the latency of
 // short kernels. 65536 x 768 bf16 against 16384 codes of uneven frequency, 52 us a call: counts 2 x
-// 3, places 2 x 6.5, sums 25 (126 MB, 5.0 TB/s), join 10. 2048 rows 26 (sort 8, sums 10, join
-// 8), 1024 rows 16 (sorted 23), 4096 rows sorted by one workgroup 12, by four launches 16.
+// 3, places 2 x 6.5, sums 25 (126 MB, 5.0 TB/s), join 10. 4096 rows 27 (sorted by four launches and their
+// codes without rows found by the sum, 34), 2048 rows 27 (sort 13 beside the zeros, sums 6, join 8), 1024
+// rows 11.
 // Not kept: a bitmap of the codes that occur (its atomics took 65 us), segments joined by a
 // workgroup each (19 us).
 #include <hip/hip_runtime.h>
@@ -203,13 +204,76 @@ __global__ __launch_bounds__(ES_NT) void k_embed_place(SortArgs p) {
     }
 }
 
+// ---- the sums
+
+constexpr int EG_U = 8;     // rows in flight
+// Waves below which the segments get shorter. 65536 x 768 against 16384 codes: bf16 51 us with
+// segments of 32 (57 with 64, 62 with 16), fp32 66 with 64 (73 with 32).
+constexpr int EG_WAVES = 2400;
+
+struct EmbedGradArgs {
+    const void* g;
+    void* out;
+    const int32_t* codes;
+    const uint32_t *key, *row;
+    float* part;  // [segments][2][dp]: the segment's share of a run from before, and of one that goes on
+    int64_t n, ldg, ldt, segs;
+    int32_t seg;          // sorted rows of a segment, at most one per lane
+    int32_t v, d, dp;
+    int32_t cols, width;  // a row's blocks of `width` vectors, one per lane
+    int32_t zero;         // k_embed_sum: waves that look for codes without rows
+    float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ void embed_out(const EmbedGradArgs& p, uint32_t code, int k, const float* acc) {
+    constexpr int VE = Vec<T>::VE;
+    float o[VE];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) o[j] = acc[j] * p.scale;
+    row_put((T*)p.out + code * p.ldt, k, p.d, pack16<T>(o));
+}
+
+// A row of zeros, by a wave.
+template <typename T>
+__device__ __forceinline__ void embed_zero_row(const EmbedGradArgs& p, int64_t code, int lane) {
+    constexpr int VE = Vec<T>::VE;
+    T* y = (T*)p.out + code * p.ldt;
+    for (int k = lane * VE; k < p.d; k += 64 * VE) row_put(y, whole<VE>(k, p.d), p.d, Raw16{{0u, 0u, 0u, 0u}});
+}
+
+// Sets those of the codes [c0, c0 + EF_ZERO) to 0 that none of n rows has; W waves, `seen`: EF_ZERO
+// words of LDS.
+constexpr int EF_ZERO = 64;
+template <typename T, int W>
+__device__ __forceinline__ void embed_zero_absent(const EmbedGradArgs& p, int n, int64_t c0, uint32_t* seen, int tid) {
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (tid < EF_ZERO) seen[tid] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < n; i += 64 * W) {
+        const int64_t c = (int64_t)p.codes[i] - c0;
+        if (c >= 0 && c < EF_ZERO) seen[c] = 1;
+    }
+    __syncthreads();
+    uint64_t left = __builtin_amdgcn_ballot_w64(c0 + lane < p.v && seen[lane] == 0);
+    for (int k = 0; left; left &= left - 1, ++k)
+        if (k % W == wave) embed_zero_row<T>(p, c0 + __builtin_ctzll(left), lane);
+}
+
 // All rows in one workgroup, in LDS, for up to EO_ROWS of them: each wave has its own stretch of the
-// rows, as in k_embed_place, and the digits are short.
+// rows, as in k_embed_place, and the digits are short. The other workgroups set codes without rows
+// to 0 meanwhile.
 constexpr int EO_ROWS = 4096, EO_PER = EO_ROWS / ES_NT, EO_BITS = 8, EO_BINS = 1 << EO_BITS;
-__global__ __launch_bounds__(ES_NT) void k_embed_sort(SortArgs p) {
+template <typename T>
+__global__ __launch_bounds__(ES_NT) void k_embed_sort(SortArgs p, EmbedGradArgs g) {
     __shared__ uint2 buf[EO_ROWS];               // key, row
     __shared__ uint32_t at[ES_W][EO_BINS], sums[EO_BINS / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = (int)p.n;
+    if (blockIdx.x > 0) {
+        embed_zero_absent<T, ES_W>(g, n, (int64_t)(blockIdx.x - 1) * EF_ZERO, &at[0][0], tid);
+        return;
+    }
     const int chunks = (n + ES_NT - 1) / ES_NT;  // of 64 rows, for each wave
     const int b = wave * chunks * 64;
     const uint64_t below = (uint64_t(1) << lane) - 1;
@@ -285,43 +349,6 @@ __global__ __launch_bounds__(ES_NT) void k_embed_sort(SortArgs p) {
     }
 }
 
-// ---- the sums
-
-constexpr int EG_U = 8;     // rows in flight
-// Waves below which the segments get shorter. 65536 x 768 against 16384 codes: bf16 51 us with
-// segments of 32 (57 with 64, 62 with 16), fp32 66 with 64 (73 with 32).
-constexpr int EG_WAVES = 2400;
-
-struct EmbedGradArgs {
-    const void* g;
-    void* out;
-    const int32_t* codes;
-    const uint32_t *key, *row;
-    float* part;  // [segments][2][dp]: the segment's share of a run from before, and of one that goes on
-    int64_t n, ldg, ldt, segs;
-    int32_t seg;          // sorted rows of a segment, at most one per lane
-    int32_t v, d, dp;
-    int32_t cols, width;  // a row's blocks of `width` vectors, one per lane
-    float scale;
-};
-
-template <typename T>
-__device__ __forceinline__ void embed_out(const EmbedGradArgs& p, uint32_t code, int k, const float* acc) {
-    constexpr int VE = Vec<T>::VE;
-    float o[VE];
-#pragma unroll
-    for (int j = 0; j < VE; ++j) o[j] = acc[j] * p.scale;
-    row_put((T*)p.out + code * p.ldt, k, p.d, pack16<T>(o));
-}
-
-// A row of zeros, by a wave.
-template <typename T>
-__device__ __forceinline__ void embed_zero_row(const EmbedGradArgs& p, int64_t code, int lane) {
-    constexpr int VE = Vec<T>::VE;
-    T* y = (T*)p.out + code * p.ldt;
-    for (int k = lane * VE; k < p.d; k += 64 * VE) row_put(y, whole<VE>(k, p.d), p.d, Raw16{{0u, 0u, 0u, 0u}});
-}
-
 // acc += EG_U rows of this lane's VE dims; rows from `cnt` on add nothing.
 template <typename T, typename F>
 __device__ __forceinline__ void embed_rows(const EmbedGradArgs& p, bool has, int k, int j0, int cnt, F row_of,
@@ -360,7 +387,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs p) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the codes without rows come first: their search takes longest
-    const int64_t zero = (p.v + EZ_CODES - 1) / EZ_CODES, items = p.segs * p.cols + zero;
+    const int64_t zero = p.zero, items = p.segs * p.cols + zero;
     for (int64_t item = (int64_t)blockIdx.x * 4 + wave - zero; item < items - zero; item += (int64_t)gridDim.x * 4) {
         if (item < 0) {
             const uint32_t c0 = (uint32_t)((item + zero) * EZ_CODES);
@@ -503,8 +530,8 @@ __global__ __launch_bounds__(64 * EJ_W) void k_embed_join(EmbedGradArgs p) {
 }
 
 // Up to EF_ROWS rows in one launch: a workgroup per row (and block of dims) looks for its code
-// among all rows; the code's first row adds them, the waves sharing its list. Further
-// workgroups set 64 codes each to 0 where no row has them.
+// among all rows; the code's first row adds them, the waves sharing its list. The first
+// workgroups set EF_ZERO codes each to 0 where no row has them.
 constexpr int EF_ROWS = 1024, EF_W = 4, EF_NT = 64 * EF_W;
 template <typename T>
 __global__ __launch_bounds__(EF_NT) void k_embed_few(EmbedGradArgs p) {
@@ -513,22 +540,12 @@ __global__ __launch_bounds__(EF_NT) void k_embed_few(EmbedGradArgs p) {
     __shared__ int list[EF_ROWS], cnt[CH][EF_W];
     const int tid = threadIdx.x, lane = tid & 63, n = (int)p.n;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t work = (uint32_t)(n * p.cols);
-    const uint32_t item = blockIdx.x;
-    if (item >= work) {
-        const int64_t c0 = (int64_t)(item - work) * 64;
-        if (tid < 64) list[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += EF_NT) {
-            const int64_t c = (int64_t)p.codes[i] - c0;
-            if (c >= 0 && c < 64) list[c] = 1;
-        }
-        __syncthreads();
-        uint64_t left = __builtin_amdgcn_ballot_w64(c0 + lane < p.v && list[lane] == 0);
-        for (int k = 0; left; left &= left - 1, ++k)
-            if (k % EF_W == wave) embed_zero_row<T>(p, c0 + __builtin_ctzll(left), lane);
+    const uint32_t zero = ((uint32_t)p.v + EF_ZERO - 1) / EF_ZERO;
+    if (blockIdx.x < zero) {
+        embed_zero_absent<T, EF_W>(p, n, (int64_t)blockIdx.x * EF_ZERO, (uint32_t*)list, tid);
         return;
     }
+    const uint32_t item = blockIdx.x - zero;
     const int r = (int)(item / (uint32_t)p.cols);
     const int code = p.codes[r];
     if (code < 0 || code >= p.v) return;
@@ -626,7 +643,7 @@ static hipError_t embed_grad(EmbedGradArgs a, const EmbedPlan& q, char* ws, hipS
     a.cols = q.cols;
     a.width = q.width;
     if (a.n <= EF_ROWS) {
-        const int64_t zero = (a.v + 63) / 64;
+        const int64_t zero = (a.v + EF_ZERO - 1) / EF_ZERO;
         hipLaunchKernelGGL((k_embed_few<T>), dim3((unsigned)(a.n * q.cols + zero)), dim3(EF_NT), 0, st, a);
         return hipGetLastError();
     }
@@ -642,7 +659,10 @@ static hipError_t embed_grad(EmbedGradArgs a, const EmbedPlan& q, char* ws, hipS
         s.bits = 32 - __builtin_clz((unsigned)a.v);
         s.key = (uint32_t*)(ws + q.o_key[0]);
         s.row = (uint32_t*)(ws + q.o_row[0]);
-        hipLaunchKernelGGL(k_embed_sort, dim3(1), dim3(ES_NT), 0, st, s);
+        hipLaunchKernelGGL((k_embed_sort<T>), dim3((unsigned)(1 + (a.v + EF_ZERO - 1) / EF_ZERO)), dim3(ES_NT), 0, st, s,
+                           a);
+    } else {
+        a.zero = (a.v + EZ_CODES - 1) / EZ_CODES;
     }
     for (int i = 0; a.n > EO_ROWS && i < q.passes; ++i) {
         s.codes = i == 0 ? a.codes : nullptr;
@@ -659,7 +679,7 @@ static hipError_t embed_grad(EmbedGradArgs a, const EmbedPlan& q, char* ws, hipS
     a.part = (float*)(ws + q.o_part);
     a.seg = q.seg;
     a.segs = q.segs;
-    const int64_t waves = a.segs * a.cols + (a.v + EZ_CODES - 1) / EZ_CODES;
+    const int64_t waves = a.segs * a.cols + a.zero;
     hipLaunchKernelGGL((k_embed_sum<T>), dim3(grid_of((waves + 3) / 4)), dim3(256), 0, st, a);
     if (a.segs > 1) {
         const int64_t blocks = (a.segs - 2) / EJ_W + 1;

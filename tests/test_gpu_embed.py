@@ -120,8 +120,8 @@ def test_runs_that_meet_segments(ops, n, run):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("n", [1024, 1025])
-@pytest.mark.parametrize("d", [3, 260, 513, 1500])
+@pytest.mark.parametrize("n", [1024, 1025, 2048, 2049, 4096, 4097])
+@pytest.mark.parametrize("d", [3, 260, 513, 1500, 5000])
 def test_either_side_of_few_rows(ops, n, d, dtype):
     g = _gen(n + d)
     codes = _codes(n, 90, g)
