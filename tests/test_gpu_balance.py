@@ -86,7 +86,8 @@ def _inputs(n, e, m, dtype, seed):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("n,e,m", [(1, 1, 1), (2, 3, 2), (5, 64, 4), (100, 65, 2), (333, 60, 2), (17, 128, 16),
                                    (70, 129, 3), (1000, 256, 8), (40, 257, 1), (33, 513, 5), (300, 1000, 2),
-                                   (20, 1025, 2), (9, 4096, 16), (50_001, 16, 2)])
+                                   (20, 1025, 2), (9, 4096, 16), (50_001, 16, 2), (8200, 60, 9), (8301, 100, 2),
+                                   (8200, 200, 3), (8203, 400, 2), (8200, 1500, 2), (1_000_001, 8, 1)])
 def test_loss_and_gradient(ops, n, e, m, dtype):
     print(f"# balance n={n} e={e} m={m} {dtype}", flush=True)
     z, idx = _inputs(n, e, min(m, e), dtype, n + e + m)

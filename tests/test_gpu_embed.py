@@ -130,6 +130,16 @@ def test_either_side_of_few_rows(ops, n, d, dtype):
     _check_grad(ops.embed_backward(grad, codes, 90, 0.5), grad, codes, 90, 0.5)
 
 
+@pytest.mark.parametrize("v", [1, 2, 3, 63, 64, 127, 1023, 1024, 1025])
+@pytest.mark.parametrize("n", [1500, 5000])
+def test_small_tables(ops, n, v):
+    # digits of one bit to ten, all rows in few runs
+    g = _gen(v)
+    codes = torch.randint(-1, v + 1, (n,), generator=g, device=DEV, dtype=torch.int32)
+    grad = torch.randn(n, 30, generator=g, device=DEV)
+    _check_grad(ops.embed_backward(grad, codes, v), grad, codes, v, 1.0)
+
+
 def test_three_digits(ops):
     # codes of more than 20 bits are sorted in three steps
     g = _gen(8)

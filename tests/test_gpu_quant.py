@@ -53,7 +53,9 @@ def _product(q, qs, w, ws, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("n,d", [(1, 1), (1, 768), (3, 7), (17, 64), (5, 1025), (300, 100), (2, 40001), (1000, 96)])
+@pytest.mark.parametrize("n,d", [(1, 1), (1, 768), (3, 7), (17, 64), (5, 1025), (300, 100), (2, 40001), (1000, 96),
+                                 (5, 15), (33, 16), (5, 17), (70, 128), (65, 129), (37, 512), (9, 513), (7, 4096),
+                                 (6, 4097), (3, 16384), (2, 16385), (2, 131071)])
 def test_rows(ops, n, d, dtype):
     g = _gen(n + d)
     x = (torch.randn(n, d, generator=g, device=DEV) * 3).to(dtype)
@@ -111,6 +113,17 @@ def test_product(ops, n, d, v, dtype):
     qs, ws = torch.rand(n, generator=g, device=DEV), torch.rand(v, generator=g, device=DEV)
     y = ops.quantized_product(q, qs, w, ws, dtype)
     assert y.dtype == dtype and torch.equal(y, _product(q, qs, w, ws, dtype))
+
+
+@pytest.mark.parametrize("d", [130_999, 130_944])
+def test_rows_in_chunks(ops, d):
+    # more rows than are taken at a time, laid out and in place
+    g = _gen(d)
+    n, v = 2100, 40
+    q = torch.randint(-128, 128, (n, d), generator=g, device=DEV, dtype=torch.int8)
+    w = torch.randint(-128, 128, (v, d), generator=g, device=DEV, dtype=torch.int8)
+    qs, ws = torch.rand(n, generator=g, device=DEV), torch.rand(v, generator=g, device=DEV)
+    assert torch.equal(ops.quantized_product(q, qs, w, ws, F32), _product(q, qs, w, ws, F32))
 
 
 def test_largest_sums(ops):
