@@ -14,6 +14,9 @@
 // zeros 8192^3 takes 344: on other numbers the chip's power sets the pace. Not kept: stores of four
 // codes (500 and, 8192 x 768 x 16384, 164 against 136), blocks of 32 x 32 (508 at 8192^3), four
 // waves of 128 x 128 (770), stores past the caches (607).
+// k_quant_odd: tiles of 64 x 64 read as the rows lie, where the layout would cost more than it saves
+// (odd rows in few tiles): 20 x 8191 x 32767 in 69 us, laid out 200; 64 x 8191 x 32767 86, 197;
+// 64 x 1003 x 32767 16, 26.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -247,6 +250,48 @@ __device__ __forceinline__ Raw16 load_bytes(const int8_t* p, int i, int end) {
     return r;
 }
 
+// 16 bytes of a row at a time where they lie within it. BYTES: rows at any address, read as the
+// aligned words that hold their bytes (up to three bytes before a row's first and behind its last
+// one come with them, never another word) and shifted into place: pieces of many rows whose words are
+// not aligned come at half the rate (1 x 8191 x 32767: 124 us so, 70 shifted; 16 rows 227, 106).
+template <bool BYTES>
+struct ByteRow {
+    const int8_t* row;
+    uint32_t shift, more;  // bytes from a word's start; from there to the word of the 16th byte
+    __device__ __forceinline__ void set(const int8_t* p) {
+        shift = BYTES ? (uint32_t)(uintptr_t)p & 3 : 0;
+        more = (shift + 15) & ~3u;
+        row = p - shift;
+    }
+    struct __attribute__((packed, aligned(4))) Words {
+        uint32_t w[4];
+    };
+    struct Piece {
+        Words v;
+        uint32_t next;
+    };
+    __device__ __forceinline__ Piece fetch(int k) const {
+        Piece r;
+        r.v = *reinterpret_cast<const Words*>(row + k);
+        r.next = BYTES ? *reinterpret_cast<const uint32_t*>(row + k + more) : 0;
+        return r;
+    }
+    __device__ __forceinline__ Raw16 take(const Piece& p) const {
+        Raw16 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            r.w[j] = BYTES ? __builtin_amdgcn_alignbyte(j < 3 ? p.v.w[(j + 1) & 3] : p.next, p.v.w[j], shift) : p.v.w[j];
+        return r;
+    }
+    __device__ __forceinline__ Raw16 get(int k) const { return take(fetch(k)); }
+    // 0 at or past `end`
+    __device__ __forceinline__ Raw16 get(int k, int end) const {
+        return k + 16 <= end ? get(k) : load_bytes(row + shift, k, end);
+    }
+};
+// Whether rows do not start at words.
+static bool odd_rows(const int8_t* p, int64_t ld) { return ((uintptr_t)p | (uint64_t)ld) % 4 != 0; }
+
 template <typename T>
 __device__ __forceinline__ T scaled_sum(int acc, float qs, float ws) {
     return Vec<T>::store((float)acc * qs * ws);
@@ -254,14 +299,15 @@ __device__ __forceinline__ T scaled_sum(int acc, float qs, float ws) {
 
 // 16 codes by up to 16 rows.
 constexpr int QF_W = 4;
-template <typename T>
+template <typename T, bool BYTES>
 __global__ __launch_bounds__(64 * QF_W) void k_quant_few(ProductArgs p) {
     __shared__ i32x4 sh[QF_W][64];
     const int lane = threadIdx.x & 63, h = lane >> 4, i = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c0 = blockIdx.x * 16;
-    const int8_t* w = p.w + (int64_t)(c0 + i < p.v ? c0 + i : p.v - 1) * p.ldw;
-    const int8_t* q = p.q + (i < p.n ? i : p.n - 1) * p.ldq;
+    ByteRow<BYTES> w, q;
+    w.set(p.w + (int64_t)(c0 + i < p.v ? c0 + i : p.v - 1) * p.ldw);
+    q.set(p.q + (i < p.n ? i : p.n - 1) * p.ldq);
     i32x4 acc = {0, 0, 0, 0};
     // steps of 64 integers, step s for wave s % QF_W, in groups whose loads are in flight together
     constexpr int STEP = 64 * QF_W;
@@ -269,21 +315,20 @@ __global__ __launch_bounds__(64 * QF_W) void k_quant_few(ProductArgs p) {
     auto steps = [&](auto count) {
         constexpr int U = decltype(count)::value;
         for (; k - h * 16 + (U - 1) * STEP + 64 <= p.d; k += U * STEP) {
-            Any16 a[U], b[U];
+            Raw16 a[U], b[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                a[u] = *reinterpret_cast<const Any16*>(w + k + u * STEP);
-                b[u] = *reinterpret_cast<const Any16*>(q + k + u * STEP);
+                a[u] = w.get(k + u * STEP);
+                b[u] = q.get(k + u * STEP);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                acc = mfma32(__builtin_bit_cast(i32x4, a[u]), __builtin_bit_cast(i32x4, b[u]), acc);
+            for (int u = 0; u < U; ++u) acc = mfma_i8(a[u], b[u], acc);
         }
     };
     steps(std::integral_constant<int, 8>());
     steps(std::integral_constant<int, 2>());
     steps(std::integral_constant<int, 1>());
-    if (k - h * 16 < p.d) acc = mfma_i8(load_bytes(w, k, p.d), load_bytes(q, k, p.d), acc);
+    if (k - h * 16 < p.d) acc = mfma_i8(w.get(k, p.d), q.get(k, p.d), acc);
     sh[wave][lane] = acc;
     __syncthreads();
     // lane (h, i) holds codes 4 h .. 4 h + 3 of row i: one of them for each wave
@@ -322,6 +367,46 @@ struct __attribute__((packed, aligned(sizeof(T)))) Run {
 };
 constexpr int QT_RUN = 8;  // codes that a lane has of two blocks
 
+// Writes eight sums of row r from code c on: to y, or to their part of a split product.
+template <typename T>
+__device__ __forceinline__ void run_out(const TilesArgs& p, int r, int c, const Run<float, QT_RUN>& ws, float qs,
+                                        const i32x4& lo, const i32x4& hi) {
+    constexpr int VE = Vec<T>::VE;
+    T* o = (T*)p.y + (int64_t)r * p.ldy + c;
+    float v[QT_RUN];
+#pragma unroll
+    for (int q = 0; q < QT_RUN; ++q) v[q] = (float)(q < 4 ? lo[q & 3] : hi[q & 3]) * qs * ws.v[q];
+    if (c + QT_RUN <= p.in.m) {
+#pragma unroll
+        for (int q = 0; q < QT_RUN; q += VE) *(Raw16*)(o + q) = pack16<T>(v + q);
+    } else {
+#pragma unroll
+        for (int q = 0; q < QT_RUN; ++q)
+            if (c + q < p.in.m) o[q] = Vec<T>::store(v[q]);
+    }
+}
+__device__ __forceinline__ void run_part(const TilesArgs& p, int r, int c, const i32x4& lo, const i32x4& hi) {
+    int32_t* o = p.part + ((int64_t)blockIdx.y * p.in.n + r) * p.in.m + c;
+    Run<int32_t, QT_RUN> v;
+#pragma unroll
+    for (int q = 0; q < QT_RUN; ++q) v.v[q] = q < 4 ? lo[q & 3] : hi[q & 3];
+    if (c + QT_RUN <= p.in.m) {
+        *(Run<int32_t, QT_RUN>*)o = v;
+    } else {
+#pragma unroll
+        for (int q = 0; q < QT_RUN; ++q)
+            if (c + q < p.in.m) o[q] = v.v[q];
+    }
+}
+// The scales of eight codes.
+__device__ __forceinline__ Run<float, QT_RUN> run_scales(const TilesArgs& p, int c) {
+    if (c + QT_RUN <= p.in.m) return *(const Run<float, QT_RUN>*)(p.w_scale + c);
+    Run<float, QT_RUN> ws;
+#pragma unroll
+    for (int q = 0; q < QT_RUN; ++q) ws.v[q] = c + q < p.in.m ? p.w_scale[c + q] : 0.f;
+    return ws;
+}
+
 template <typename T, int BM, int BN, int WM, int WN, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN) void k_quant_tiles(TilesArgs p) {
     using G = Gemm<BM, BN, WM, WN, true, false, i32x4>;
@@ -337,24 +422,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_quant_tiles(TilesArgs p) {
         for (int y = 0; y < G::TN; ++y) {
             const int r = n0 + G::col(y);
             if (r >= p.in.n) continue;
-            int32_t* o = p.part + ((int64_t)blockIdx.y * p.in.n + r) * p.in.m;
 #pragma unroll
-            for (int x = 0; x < G::TM; x += 2) {
-                const int c = m0 + G::row(x);
-                Run<int32_t, QT_RUN> v;
-#pragma unroll
-                for (int q = 0; q < QT_RUN; ++q) v.v[q] = g.acc[x + q / 4][y][q % 4];
-                if (c + QT_RUN <= p.in.m) {
-                    *(Run<int32_t, QT_RUN>*)(o + c) = v;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < QT_RUN; ++q)
-                        if (c + q < p.in.m) o[c + q] = v.v[q];
-                }
-            }
+            for (int x = 0; x < G::TM; x += 2) run_part(p, r, m0 + G::row(x), g.acc[x][y], g.acc[x + 1][y]);
         }
     } else {
-        constexpr int VE = Vec<T>::VE;
         gemm_walk<i32x4, G, BM, BN>(p.in, p.mt, p.nt, l0, l1, [&](G& g, int m0, int n0) {
             float qs[G::TN];
 #pragma unroll
@@ -365,33 +436,125 @@ __global__ __launch_bounds__(64 * WM * WN) void k_quant_tiles(TilesArgs p) {
 #pragma unroll
             for (int x = 0; x < G::TM; x += 2) {
                 const int c = m0 + G::row(x);
-                const bool full = c + QT_RUN <= p.in.m;
-                Run<float, QT_RUN> ws;
-                if (full) {
-                    ws = *(const Run<float, QT_RUN>*)(p.w_scale + c);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < QT_RUN; ++q) ws.v[q] = c + q < p.in.m ? p.w_scale[c + q] : 0.f;
-                }
+                const Run<float, QT_RUN> ws = run_scales(p, c);
 #pragma unroll
                 for (int y = 0; y < G::TN; ++y) {
                     const int r = n0 + G::col(y);
-                    if (r >= p.in.n) continue;
-                    T* o = (T*)p.y + (int64_t)r * p.ldy + c;
-                    float v[QT_RUN];
-#pragma unroll
-                    for (int q = 0; q < QT_RUN; ++q) v[q] = (float)g.acc[x + q / 4][y][q % 4] * qs[y] * ws.v[q];
-                    if (full) {
-#pragma unroll
-                        for (int q = 0; q < QT_RUN; q += VE) *(Raw16*)(o + q) = pack16<T>(v + q);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < QT_RUN; ++q)
-                            if (c + q < p.in.m) o[q] = Vec<T>::store(v[q]);
-                    }
+                    if (r < p.in.n) run_out<T>(p, r, c, ws, qs[y], g.acc[x][y], g.acc[x + 1][y]);
                 }
             }
         });
+    }
+}
+
+// The same product for operands of any stride and alignment, without laying them out: 64 codes by 64
+// rows, steps of 128 integers read into registers, 16 bytes a lane, QO_AHEAD ahead, and put into LDS (rows
+// turned and pieces rotated as in gmm_gemm.h) when the step before has been multiplied.
+struct OddArgs {
+    TilesArgs t;         // in.m codes, in.n rows
+    const int8_t *w, *q;
+    int64_t ldw, ldq;
+    int32_t d, steps;
+};
+constexpr int QO_TILE = 64, QO_STAGE = 2 * QO_TILE * QT_STEP;
+// Steps in flight, an even number (2: 20 x 8191 x 32767 69 us, 8000 x 5001 x 9000 950; 4: 70 and 1049).
+constexpr int QO_AHEAD = 2;
+template <typename T, bool SPLIT, bool BYTES>
+__global__ __launch_bounds__(256) void k_quant_odd(OddArgs p) {
+    __shared__ __align__(16) unsigned char lds[2][QO_STAGE];
+    int tm, tn;
+    if (!gemm_tile(blockIdx.x, p.t.mt, p.t.nt, &tm, &tn)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = lane >> 4, i = lane & 15, wm = wave >> 1, wn = wave & 1;
+    const int m0 = tm * QO_TILE, n0 = tn * QO_TILE;
+    const int first = SPLIT ? p.steps * (int)blockIdx.y / p.t.split : 0;
+    const int last = SPLIT ? p.steps * ((int)blockIdx.y + 1) / p.t.split : p.steps;
+    const int full = p.d / QT_STEP;  // steps that lie within the rows
+    const int r8 = lane >> 3, k0 = (lane & 7) * 16;
+    ByteRow<BYTES> src[4];           // this lane's pieces: two groups of 8 rows of w, two of q
+    int to[4];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int row = wave * 16 + g * 8 + r8, in32 = row & 31;
+        const int code = m0 + (row & 32) + 8 * (in32 >> 2 & 3) + 4 * (in32 >> 4) + (in32 & 3);
+        src[g].set(p.w + (int64_t)(code < p.t.in.m ? code : p.t.in.m - 1) * p.ldw);
+        src[2 + g].set(p.q + (int64_t)(n0 + row < p.t.in.n ? n0 + row : p.t.in.n - 1) * p.ldq);
+        to[g] = row * QT_STEP + (k0 ^ (r8 << 4));
+        to[2 + g] = QO_TILE * QT_STEP + to[g];
+    }
+    i32x4 acc[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
+    auto put = [&](unsigned char* l, int g, const Raw16& v) {
+        *(uint4*)(l + to[g]) = uint4{v.w[0], v.w[1], v.w[2], v.w[3]};
+    };
+    auto multiply = [&](const unsigned char* l) {
+        // A barrier for LDS alone: the loads in flight go on. The other buffer is free again (every wave
+        // has read it).
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            i32x4 a[2], b[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int piece = ((4 * c + h) ^ (i & 7)) << 4;
+                a[x] = *(const i32x4*)(l + (wm * 32 + x * 16 + i) * QT_STEP + piece);
+                b[x] = *(const i32x4*)(l + (QO_TILE + wn * 32 + x * 16 + i) * QT_STEP + piece);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) acc[x][y] = mfma32(a[x], b[y], acc[x][y]);
+        }
+    };
+    const int end = last < full ? last : full;  // whole steps; at most one that is cut follows
+    int buf = 0;
+    if (first < end) {
+        using Piece = typename ByteRow<BYTES>::Piece;
+        Piece v[QO_AHEAD][4];
+        auto fetch = [&](Piece(&to_v)[4], int s) {
+            const int k = (s < end ? s : end - 1) * QT_STEP + k0;  // (no branch around a load)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) to_v[g] = src[g].fetch(k);
+        };
+#pragma unroll
+        for (int u = 0; u < QO_AHEAD; ++u) {
+            fetch(v[u], first + u);
+            __builtin_amdgcn_sched_barrier(0);  // loads in the order in which they are waited for
+        }
+        for (int s0 = first; s0 < end; s0 += QO_AHEAD) {
+#pragma unroll
+            for (int u = 0; u < QO_AHEAD; ++u) {
+                if (s0 + u >= end) break;
+                unsigned char* l = lds[u & 1];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) put(l, g, src[g].take(v[u][g]));
+                fetch(v[u], s0 + u + QO_AHEAD);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(l);
+                buf = (u & 1) ^ 1;
+            }
+        }
+    }
+    if (last > full) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) put(lds[buf], g, src[g].get(full * QT_STEP + k0, p.d));
+        multiply(lds[buf]);
+    }
+    const int c = m0 + wm * 32 + 8 * h;
+    const Run<float, QT_RUN> ws = run_scales(p.t, c);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int r = n0 + wn * 32 + y * 16 + i;
+        if (r >= p.t.in.n) continue;
+        if constexpr (SPLIT)
+            run_part(p.t, r, c, acc[0][y], acc[1][y]);
+        else
+            run_out<T>(p.t, r, c, ws, p.t.q_scale[r], acc[0][y], acc[1][y]);
     }
 }
 
@@ -435,7 +598,9 @@ __global__ __launch_bounds__(256) void k_quant_pack(PackArgs p) {
         const int64_t r = (int64_t)group * 8 + (lane >> 3);
         if (r >= o.rows) continue;
         const int k = (int)panel * QT_STEP + (lane & 7) * 16;
-        *(Raw16*)(o.out + (panel * o.rows + r) * QT_STEP + (lane & 7) * 16) = load_bytes(o.x + r * o.ld, k, p.d);
+        ByteRow<true> x;
+        x.set(o.x + r * o.ld);
+        *(Raw16*)(o.out + (panel * o.rows + r) * QT_STEP + (lane & 7) * 16) = x.get(k, p.d);
     }
 }
 
@@ -485,18 +650,25 @@ struct QuantCost {
 constexpr QuantCost QUANT_COST[4] = {
     {256, 256, 1, 1.75f, 6.f, 1.75f}, {192, 256, 1, 1.35f, 6.f, 1.35f}, {128, 128, 2, 1.13f, 4.f, 0.7f},
     {64, 64, 4, 0.82f, 3.f, 0.4f}};
-static Choice quant_choice(int64_t m, int64_t n, int64_t steps) {
+// Operands as they lie (k_quant_odd), tile QT_ODD, against the tiles and `pack` bytes laid out before
+// (us as they lie, laid out): 64 x 1003 x 32767 16, 26; 1000 x 333 x 1111 10.5, 12; 200 x 1003 x 16384 21, 22;
+// 200 x 8191 x 32767 231, 222; 777 x 1003 x 5001 27, 20; 500 x 8191 x 16384 203, 135; 3000 x 3001 x 8000 219, 84.
+constexpr int QT_ODD = 4;
+constexpr QuantCost ODD_COST = {QO_TILE, QO_TILE, 4, 1.6f, 6.f, 0.85f};
+static Choice quant_choice(int64_t m, int64_t n, int64_t steps, size_t pack) {
     Choice best{0, 1};
     double least = 1e300;
-    for (int t = 0; t < 4; ++t) {
-        const QuantCost& c = QUANT_COST[t];
+    for (int t = 0; t < (pack > 0 ? 5 : 4); ++t) {
+        const QuantCost& c = t == QT_ODD ? ODD_COST : QUANT_COST[t];
         const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
+        if (t == QT_ODD && tiles > ((int64_t)1 << 22)) break;  // a workgroup for each: within a grid
         for (int s = 1; s <= QT_MAX_SPLIT && s <= steps; ++s) {
             if (s > 1 && (size_t)s * m * n * 4 > QT_SPLIT_BYTES) break;
             const double load = (double)((tiles * s + 255) / 256) / c.per_cu, each = (double)((steps + s - 1) / s);
             const double part = c.per_step * load > c.alone ? c.per_step * load : c.alone;
             double us = load >= 1.0 ? load * (c.fixed + c.per_step * each) : c.fixed + part * each;
             if (s > 1) us += 4.0 + (double)m * n * 8 * s / 4.0e6;
+            if (t != QT_ODD && pack > 0) us += 4.0 + (double)pack * 2 / 4.0e6;
             if (us < least) {
                 least = us;
                 best = Choice{t, s};
@@ -509,7 +681,11 @@ static Choice quant_choice(int64_t m, int64_t n, int64_t steps) {
 template <typename T>
 static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) {
     if (a.n <= QT_FEW_ROWS) {
-        hipLaunchKernelGGL((k_quant_few<T>), dim3((unsigned)((a.v + 15) / 16)), dim3(64 * QF_W), 0, st, a);
+        const dim3 grid((unsigned)((a.v + 15) / 16)), block(64 * QF_W);
+        if (odd_rows(a.w, a.ldw) || odd_rows(a.q, a.ldq))
+            hipLaunchKernelGGL((k_quant_few<T, true>), grid, block, 0, st, a);
+        else
+            hipLaunchKernelGGL((k_quant_few<T, false>), grid, block, 0, st, a);
         return hipGetLastError();
     }
     const bool pq = !quant_direct(a.q, a.d, a.ldq), pw = !quant_direct(a.w, a.d, a.ldw);
@@ -524,12 +700,44 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
     t.in.a = (const uint16_t*)(pw ? (const int8_t*)ws + q.o_w : a.w);
     t.in.lda = pw ? GK : a.ldw / 2;
     t.in.step_a = pw ? (int64_t)a.v * GK : GK;
+    bool packed = false;  // w
     for (int64_t r0 = 0; r0 < a.n; r0 += q.chunk) {
         const int64_t rows = a.n - r0 < q.chunk ? a.n - r0 : q.chunk;
+        t.in.n = (int32_t)rows;
+        t.q_scale = a.q_scale + r0;
+        t.y = (T*)a.y + r0 * a.ldy;
+        const size_t pack = (pw && !packed ? (size_t)a.v * q.dp : 0) + (pq ? (size_t)rows * q.dp : 0);
+        const Choice c = quant_choice(a.v, rows, q.dp / QT_STEP, pack);
+        t.split = c.split;
+        auto sums = [&]() {
+            if (c.split < 2) return;
+            const int64_t work = (rows * ((a.v + 3) / 4) + 255) / 256;
+            hipLaunchKernelGGL((k_quant_sum<T>), dim3((unsigned)(work < 16384 ? work : 16384)), dim3(256), 0, st, t);
+        };
+        if (c.tile == QT_ODD) {
+            t.mt = (a.v + QO_TILE - 1) / QO_TILE;
+            t.nt = (int32_t)((rows + QO_TILE - 1) / QO_TILE);
+            const OddArgs o{t, a.w, a.q + r0 * a.ldq, a.ldw, a.ldq, a.d, q.dp / QT_STEP};
+            const dim3 grid(tile_grid(t.mt, t.nt), c.split);
+            auto launch = [&](auto bytes) {
+                constexpr bool BYTES = decltype(bytes)::value;
+                if (c.split > 1)
+                    hipLaunchKernelGGL((k_quant_odd<T, true, BYTES>), grid, dim3(256), 0, st, o);
+                else
+                    hipLaunchKernelGGL((k_quant_odd<T, false, BYTES>), grid, dim3(256), 0, st, o);
+            };
+            if (odd_rows(o.w, o.ldw) || odd_rows(o.q, o.ldq))
+                launch(std::true_type());
+            else
+                launch(std::false_type());
+            sums();
+            continue;
+        }
         PackArgs p{};
         p.d = a.d;
         p.dp = q.dp;
-        if (pw && r0 == 0) p.o[0] = {a.w, a.v, a.ldw, (int8_t*)ws + q.o_w};
+        if (pw && !packed) p.o[0] = {a.w, a.v, a.ldw, (int8_t*)ws + q.o_w};
+        packed = true;
         if (pq) p.o[1] = {a.q + r0 * a.ldq, rows, a.ldq, (int8_t*)ws + q.o_q};
         const int64_t most = p.o[0].rows > p.o[1].rows ? p.o[0].rows : p.o[1].rows;
         if (most > 0) {
@@ -539,11 +747,6 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
         t.in.b = (const uint16_t*)(pq ? (const int8_t*)ws + q.o_q : a.q + r0 * a.ldq);
         t.in.ldb = pq ? GK : a.ldq / 2;
         t.in.step_b = pq ? rows * GK : GK;
-        t.in.n = (int32_t)rows;
-        t.q_scale = a.q_scale + r0;
-        t.y = (T*)a.y + r0 * a.ldy;
-        const Choice c = quant_choice(a.v, rows, q.dp / QT_STEP);
-        t.split = c.split;
         with_tile(c.tile, [&](auto id) {
             using C = Tile<decltype(id)::value>;
             t.mt = (a.v + C::BM - 1) / C::BM;
@@ -559,10 +762,7 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
                 hipLaunchKernelGGL((k_quant_tiles<T, C::BM, C::BN, C::WM, C::WN, false>), dim3(grid), block, 0, st, t);
             }
         });
-        if (c.split > 1) {
-            const int64_t work = (rows * ((a.v + 3) / 4) + 255) / 256;
-            hipLaunchKernelGGL((k_quant_sum<T>), dim3((unsigned)(work < 16384 ? work : 16384)), dim3(256), 0, st, t);
-        }
+        sums();
     }
     return hipGetLastError();
 }

@@ -115,6 +115,21 @@ def test_product(ops, n, d, v, dtype):
     assert y.dtype == dtype and torch.equal(y, _product(q, qs, w, ws, dtype))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,d,v", [(17, 1, 1), (64, 127, 63), (20, 129, 4000), (40, 4999, 200), (30, 20001, 37),
+                                   (90, 255, 1000), (64, 1003, 32767), (20, 640, 500)])
+@pytest.mark.parametrize("lead", [0, 1, 2, 4])
+def test_rows_as_they_lie(ops, n, d, v, lead, dtype):
+    # strides and starts at every remainder of 4, one cut step alone, whole steps alone, a split axis
+    print(f"# int8 odd product n={n} d={d} v={v} lead={lead} {dtype}", flush=True)
+    g = _gen(n + d + v + lead)
+    a = torch.randint(-128, 128, (n, d + lead + 4), generator=g, device=DEV, dtype=torch.int8)
+    b = torch.randint(-128, 128, (v, d + lead), generator=g, device=DEV, dtype=torch.int8)
+    q, w = a[:, lead:lead + d], b[:, lead:]
+    qs, ws = torch.rand(n, generator=g, device=DEV), torch.rand(v, generator=g, device=DEV)
+    assert torch.equal(ops.quantized_product(q, qs, w, ws, dtype), _product(q, qs, w, ws, dtype))
+
+
 @pytest.mark.parametrize("d", [130_999, 130_944])
 def test_rows_in_chunks(ops, d):
     # more rows than are taken at a time, laid out and in place
