@@ -735,6 +735,8 @@ def beam_reorder(state, parent, w: int, dim: int = 0, out=None):
     if shape[dim] != b * w:
         raise ValueError("state must have B * w rows along dim")
     _int32(w, m)
+    if w == 0:
+        raise GmmError(GMM_E_INVALID)
     shape[dim] = b * m
     new = out is None
     if new:

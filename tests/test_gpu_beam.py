@@ -323,3 +323,14 @@ def test_refusals(ops):
         ops.beam_reorder(x[:4], torch.zeros(2, 3, dtype=torch.int32, device=DEV), 2, out=x)
     with pytest.raises(ops.GmmError):  # rows of the result that overlap
         ops.beam_reorder(x, parent, 3, out=torch.zeros(10, device=DEV).expand(6, 10))
+
+
+def test_no_beams(ops):
+    none = torch.zeros(0, 10, device=DEV)
+    parent = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    with pytest.raises(ops.GmmError):
+        ops.beam_step(none, torch.zeros(2, 0, device=DEV))
+    for state in (none, none.expand(0, 10), torch.zeros(10, 0, device=DEV).t()):
+        with pytest.raises(ops.GmmError):
+            ops.beam_reorder(state, parent, 0)
+    assert ops.beam_reorder(none, parent[:0], 3).shape == (0, 10)
