@@ -28,6 +28,7 @@
 
 #include "gmm_em.h"
 #include "gmm_nn.h"
+#include "gmm_search.h"
 #include "gmm_softmax.h"
 
 namespace gmm {
@@ -366,15 +367,13 @@ __device__ __forceinline__ void embed_rows(const EmbedGradArgs& p, bool has, int
 constexpr int EZ_CODES = 16;
 __device__ __forceinline__ uint32_t absent_codes(const EmbedGradArgs& p, uint32_t c0, int lane) {
     const uint32_t c = c0 + (lane >> 2);
-    int64_t lo = 0, hi = p.n;  // the first key that is not below c lies in [lo, hi]
-    while (__builtin_amdgcn_ballot_w64(lo < hi)) {
-        const int64_t step = (hi - lo + 4) / 5, at = lo + ((lane & 3) + 1) * step - 1;
-        const bool below = at < hi && p.key[at] < c;
-        const int count = __popc((uint32_t)(__builtin_amdgcn_ballot_w64(below) >> (lane & ~3)) & 15u);
-        lo += count * step;
-        if (count < 4 && lo + step - 1 < hi) hi = lo + step - 1;  // (the place behind the fourth was not seen)
+    Search at{0, p.n};
+    while (__builtin_amdgcn_ballot_w64(at.lo < at.hi)) {
+        const int64_t probe = at.place(lane & 3);
+        const bool below = at.inside(probe) && p.key[probe] < c;
+        at.narrow(__popc((uint32_t)(__builtin_amdgcn_ballot_w64(below) >> (lane & ~3)) & 15u));
     }
-    const uint64_t none = __builtin_amdgcn_ballot_w64(lo >= p.n || p.key[lo] != c);
+    const uint64_t none = __builtin_amdgcn_ballot_w64(at.lo >= p.n || p.key[at.lo] != c);
     uint32_t absent = 0;
 #pragma unroll
     for (int j = 0; j < EZ_CODES; ++j) absent |= (uint32_t)(none >> (4 * j) & 1) << j;
