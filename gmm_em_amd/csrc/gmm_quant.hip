@@ -25,6 +25,7 @@
 
 #include "gmm_em.h"
 #include "gmm_gemm.h"
+#include "gmm_grid.h"
 #include "gmm_nn.h"
 #include "gmm_softmax.h"
 #include "gmm_tiles.h"
@@ -210,20 +211,20 @@ __global__ __launch_bounds__(NT) void k_quant_long(QuantArgs p) {
 
 template <typename T>
 static void quant_rows(const QuantArgs& a, hipStream_t st) {
-    auto grid = [&](int64_t rows) {
-        const int64_t b = (a.n + rows - 1) / rows, most = (int64_t)1 << 22;
-        return dim3((unsigned)(b < most ? b : most));
+    // workgroups of nt threads that take `rows` rows at once
+    auto launch = [&](auto kernel, int nt, int64_t rows) {
+        hipLaunchKernelGGL(kernel, dim3(grid_for((a.n + rows - 1) / rows, nt)), dim3(nt), 0, st, a);
     };
     if (a.d <= 8 * 16)
-        hipLaunchKernelGGL((k_quant_rows<T, 8, 1>), grid(32), dim3(256), 0, st, a);
+        launch(k_quant_rows<T, 8, 1>, 256, 32);
     else if (a.d <= 2 * 16 * 16)
-        hipLaunchKernelGGL((k_quant_rows<T, 16, 2>), grid(16), dim3(256), 0, st, a);
+        launch(k_quant_rows<T, 16, 2>, 256, 16);
     else if (a.d <= 4 * 64 * 16)
-        hipLaunchKernelGGL((k_quant_rows<T, 64, 4>), grid(4), dim3(256), 0, st, a);
+        launch(k_quant_rows<T, 64, 4>, 256, 4);
     else if (a.d <= 4 * 256 * 16)
-        hipLaunchKernelGGL((k_quant_long<T, 256, true>), grid(1), dim3(256), 0, st, a);
+        launch(k_quant_long<T, 256, true>, 256, 1);
     else
-        hipLaunchKernelGGL((k_quant_long<T, 1024, false>), grid(1), dim3(1024), 0, st, a);
+        launch(k_quant_long<T, 1024, false>, 1024, 1);
 }
 
 // ---- products
