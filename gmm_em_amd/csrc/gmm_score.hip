@@ -11,15 +11,14 @@
 // bound that m values of the row reach and hardly more than m do (about
 // 64 ln(64 / (64 - m))). The values of the few threads whose maximum reaches it are
 // read again by all threads (they are in the caches), those at the bound are gathered
-// in LDS, and each finds its place by counting those before it. Where ties or a mask put more values at the bound than LDS holds, the m
+// in LDS, and each finds its place by counting those before it or, where ties made them many, one wave
+// picks the m best. Where ties or a mask put more values at the bound than LDS holds, the m
 // best are found one by one over the whole row.
 // Gradient: dx = scale (g_lp ([v = t] - p) - g_H p (log p + H)) with p from the
 // stored m and log s: each logit is read once and its gradient written once.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
-
-#include <type_traits>
 
 #include "gmm_em.h"
 #include "gmm_nn.h"
@@ -29,6 +28,10 @@ namespace gmm {
 
 constexpr int SC_U = 4;       // vectors of 16 bytes in flight per thread
 constexpr int SC_CAND = 256;  // gathered values
+// Comparisons of a thread that take as long as one round of picking. Equal logits, 8192 x 256 fp32: top 1
+// counted 191 us a call, picked 14 (random logits 14); 65536 x 128, top 16 of random logits (about 25
+// candidates): counted 71, picked 121.
+constexpr int SC_COUNT = 5;
 
 // The logit of the row's target (thread 0; where there is none, unused).
 template <typename T>
@@ -85,7 +88,8 @@ struct RowPart {
 // (5.3 TB/s), 57 us with 4; the insertion of every value above a wave's own m-th best
 // into its sorted list took 73. With 16 of 333 rows of 40009 fp32 values 17.9 us; the bound's threads
 // read again value by value and a list picked by one wave took 21.5.
-// BEAM: rows of beams that are dead or have ended are left out, their results unwritten.
+// BEAM: rows of beams that are dead or have ended are not read. Their lists stay unwritten; for searches of
+// one beam (beam_parent) the list is the result, and theirs is written: the ended beam itself or nothing.
 template <typename T, int NT, bool TOP, bool BEAM = false>
 __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
     constexpr int VE = Vec<T>::VE, NW = NT / 64, G = NT / 64, CHUNK = NT * VE * SC_U;
@@ -170,26 +174,34 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
             auto in = [&](float l) { return l > -INFINITY && order_of(l) >= bound; };
             if (in(cm)) hot[atomicAdd(&hots, 1)] = tid;
             __syncthreads();
-            // the hot threads' vectors, one per thread at a time
-            const uint32_t mine = (x.len + CHUNK - 1) / CHUNK * SC_U;  // vectors of a thread
+            auto gather = [&](float l, int i) {
+                if (!in(l)) return;
+                const int to = atomicAdd(&count, 1);
+                if (to < SC_CAND) {
+                    cv[to] = l;
+                    ci[to] = (int)i0 + i;
+                }
+            };
+            // the hot threads' vectors, one per thread at a time; few of them value by value
+            const int rest = (x.len % CHUNK + NT * VE - 1) / (NT * VE);
+            const uint32_t mine = x.len / CHUNK * SC_U + rest;  // vectors of a thread
             const uint32_t total = (uint32_t)hots * mine;
-            for (uint32_t e = tid; e < total; e += NT) {
-                const int h = (int)(e / mine), j = (int)(e - h * mine);
-                const int at = j / SC_U * CHUNK + (j % SC_U * NT + hot[h]) * VE;
-                if (at >= x.len) continue;
-                Raw16 r = x.get(at);
-                x.mask(r, at);
-                const int first = (int)i0 + x.first(at);
+            if (total * VE <= NT) {
+                const int j = tid / VE, h = j / (int)mine, u = j - h * (int)mine;
+                if ((uint32_t)j < total) {
+                    const int at = u / SC_U * CHUNK + (u % SC_U * NT + hot[h]) * VE + tid % VE;
+                    if (at < x.len) gather(scaled(Vec<T>::one(x.x + at), p.scale), at);
+                }
+            } else {
+                for (uint32_t e = tid; e < total; e += NT) {
+                    const int h = (int)(e / mine), j = (int)(e - h * mine);
+                    const int at = j / SC_U * CHUNK + (j % SC_U * NT + hot[h]) * VE;
+                    if (at >= x.len) continue;
+                    Raw16 r = x.get(at);
+                    x.mask(r, at);
+                    const int first = x.first(at);
 #pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    const float l = scaled(Vec<T>::get(r, k), p.scale);
-                    if (in(l)) {
-                        const int to = atomicAdd(&count, 1);
-                        if (to < SC_CAND) {
-                            cv[to] = l;
-                            ci[to] = first + k;
-                        }
-                    }
+                    for (int k = 0; k < VE; ++k) gather(scaled(Vec<T>::get(r, k), p.scale), first + k);
                 }
             }
             __syncthreads();
@@ -237,12 +249,16 @@ __global__ __launch_bounds__(NT) void k_score(ScoreArgs p) {
                 }
                 cnt = p.m;
             }
-            // every candidate counts those before it
-            top_rank(cv, ci, cnt, p.m, ov, oi, tid, NT);
-            __syncthreads();
-            if (wave == 0 && lane < p.m) {
-                top.v = ov[lane];
-                top.i = oi[lane];
+            if (cnt * ((cnt + NT - 1) / NT) <= SC_COUNT * p.m) {
+                // every candidate counts those before it
+                top_rank(cv, ci, cnt, p.m, ov, oi, tid, NT);
+                __syncthreads();
+                if (wave == 0 && lane < p.m) {
+                    top.v = ov[lane];
+                    top.i = oi[lane];
+                }
+            } else if (wave == 0) {
+                top = top_take(cv, ci, cnt, p.m, lane);
             }
         }
         if (wave == 0) {

@@ -276,6 +276,37 @@ __device__ __forceinline__ TopList top_pick(float* cv, int* ci, int m, int lane)
     return out;
 }
 
+// The same for cnt candidates in LDS, by one wave: the lane whose best is taken looks for its next one.
+__device__ __forceinline__ TopList top_take(float* cv, const int* ci, int cnt, int m, int lane) {
+    TopList out, mine;
+    out.clear();
+    int from = 0;
+    auto next = [&]() {
+        mine.clear();
+        for (int c = lane; c < cnt; c += 64)
+            if (top_before(cv[c], ci[c], mine.v, mine.i)) {
+                mine.v = cv[c];
+                mine.i = ci[c];
+                from = c;
+            }
+    };
+    next();
+    for (int j = 0; j < m; ++j) {
+        const float best = wave_max(mine.v);
+        if (best == -INFINITY) break;
+        const int at = wave_min(mine.v == best ? mine.i : 0x7fffffff);
+        if (lane == j) {
+            out.v = best;
+            out.i = at;
+        }
+        if (mine.i == at) {
+            cv[from] = -INFINITY;
+            next();
+        }
+    }
+    return out;
+}
+
 // cnt sorted-or-not candidates (cv, ci) in LDS; the thread holding candidate c
 // writes it to rank's place in (ov, oi) when its rank is below m. Distinct
 // candidates have distinct ranks (indices differ); places that no candidate
