@@ -609,35 +609,6 @@ static bool quant_direct(const int8_t* x, int32_t d, int64_t ld) {
     return d % QT_STEP == 0 && ld % 16 == 0 && ld <= QT_MAX_LD && (uintptr_t)x % 16 == 0;
 }
 
-struct QuantPlan {
-    int32_t dp;
-    int64_t chunk;  // rows at a time
-    size_t o_w, o_q, o_part, bytes;
-};
-// pack_q, pack_w: whether the operands have to be laid out (the sizing entry point assumes both).
-static QuantPlan quant_plan(int64_t n, int32_t d, int32_t v, bool pack_q, bool pack_w) {
-    QuantPlan q{};
-    if (n <= QT_FEW_ROWS) {
-        q.bytes = 256;
-        return q;
-    }
-    q.dp = (d + QT_STEP - 1) / QT_STEP * QT_STEP;
-    q.chunk = (int64_t)(QT_PACK_BYTES / q.dp) / 256 * 256;
-    if (q.chunk > n) q.chunk = n;
-    size_t off = 0;
-    auto take = [&](size_t b) {
-        const size_t o = off;
-        off += up256(b);
-        return o;
-    };
-    q.o_w = take(pack_w ? (size_t)v * q.dp : 0);
-    q.o_q = take(pack_q ? (size_t)q.chunk * q.dp : 0);
-    const size_t most = (size_t)q.chunk * v * 4 * QT_MAX_SPLIT;
-    q.o_part = take(most < QT_SPLIT_BYTES ? most : QT_SPLIT_BYTES);
-    q.bytes = off;
-    return q;
-}
-
 // The tile and the split that take least time by a model of it: the chip's workgroups take
 // (fixed + steps * per_step) for each full load of the CUs; fewer workgroups per CU take their share of a
 // step's time, but not less than `alone`. A split adds the writing and reading of its sums.
@@ -679,8 +650,67 @@ static Choice quant_choice(int64_t m, int64_t n, int64_t steps, size_t pack) {
     return best;
 }
 
+// What a product lays out and where.
+struct QuantPlan {
+    int32_t dp;
+    int64_t chunk;  // rows at a time
+    Choice first;   // of the first chunk
+    size_t o_w, o_q, o_part, bytes;
+};
+static QuantPlan quant_rows_at_once(int64_t n, int32_t d) {
+    QuantPlan q{};
+    q.dp = (d + QT_STEP - 1) / QT_STEP * QT_STEP;
+    q.chunk = (int64_t)(QT_PACK_BYTES / q.dp) / 256 * 256;
+    if (q.chunk > n) q.chunk = n;
+    return q;
+}
+// The bytes of a chunk's operands that have to be laid out for the tiles (packed: w has been).
+static size_t pack_bytes(const QuantPlan& q, int32_t v, int64_t rows, bool pack_q, bool pack_w, bool packed) {
+    return (pack_w && !packed ? (size_t)v * q.dp : 0) + (pack_q ? (size_t)rows * q.dp : 0);
+}
+// pack_q, pack_w: whether the operands are ones that the tiles cannot read in place. A workspace that is
+// used has more than 256 bytes.
+static QuantPlan quant_plan(int64_t n, int32_t d, int32_t v, bool pack_q, bool pack_w) {
+    if (n <= QT_FEW_ROWS) {
+        QuantPlan q{};
+        q.bytes = 256;
+        return q;
+    }
+    QuantPlan q = quant_rows_at_once(n, d);
+    size_t w = 0, rows_q = 0, part = 0;
+    bool packed = false;
+    auto visit = [&](int64_t rows) {
+        const Choice c = quant_choice(v, rows, q.dp / QT_STEP, pack_bytes(q, v, rows, pack_q, pack_w, packed));
+        if (c.tile != QT_ODD) {
+            packed = true;
+            if (pack_w) w = (size_t)v * q.dp;
+            if (pack_q && (size_t)rows * q.dp > rows_q) rows_q = (size_t)rows * q.dp;
+        }
+        const size_t sums = c.split > 1 ? (size_t)c.split * rows * v * 4 : 0;
+        if (sums > part) part = sums;
+        return c;
+    };
+    // the first chunk, those between it and the last, which are alike, and the last
+    const int64_t chunks = (n + q.chunk - 1) / q.chunk;
+    q.first = visit(q.chunk);
+    if (chunks > 2) visit(q.chunk);
+    if (chunks > 1) visit(n - (chunks - 1) * q.chunk);
+    q.o_q = up256(w);
+    q.o_part = q.o_q + up256(rows_q);
+    q.bytes = q.o_part + up256(part);
+    if (q.bytes < 512) q.bytes = q.bytes == 0 ? 256 : 512;
+    return q;
+}
+// Enough for any operands.
+static size_t quant_most_bytes(int64_t n, int32_t d, int32_t v) {
+    if (n <= QT_FEW_ROWS) return 256;
+    const QuantPlan q = quant_rows_at_once(n, d);
+    const size_t sums = (size_t)q.chunk * v * 4 * QT_MAX_SPLIT;
+    return up256((size_t)v * q.dp) + up256((size_t)q.chunk * q.dp) + up256(sums < QT_SPLIT_BYTES ? sums : QT_SPLIT_BYTES);
+}
+
 template <typename T>
-static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) {
+static hipError_t quant_product(const ProductArgs& a, const QuantPlan& q, char* ws, hipStream_t st) {
     if (a.n <= QT_FEW_ROWS) {
         const dim3 grid((unsigned)((a.v + 15) / 16)), block(64 * QF_W);
         if (odd_rows(a.w, a.ldw) || odd_rows(a.q, a.ldq))
@@ -690,7 +720,6 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
         return hipGetLastError();
     }
     const bool pq = !quant_direct(a.q, a.d, a.ldq), pw = !quant_direct(a.w, a.d, a.ldw);
-    const QuantPlan q = quant_plan(a.n, a.d, a.v, pq, pw);
     TilesArgs t{};
     t.w_scale = a.w_scale;
     t.ldy = a.ldy;
@@ -707,8 +736,8 @@ static hipError_t quant_product(const ProductArgs& a, char* ws, hipStream_t st) 
         t.in.n = (int32_t)rows;
         t.q_scale = a.q_scale + r0;
         t.y = (T*)a.y + r0 * a.ldy;
-        const size_t pack = (pw && !packed ? (size_t)a.v * q.dp : 0) + (pq ? (size_t)rows * q.dp : 0);
-        const Choice c = quant_choice(a.v, rows, q.dp / QT_STEP, pack);
+        const Choice c = r0 == 0 ? q.first
+                                 : quant_choice(a.v, rows, q.dp / QT_STEP, pack_bytes(q, a.v, rows, pq, pw, packed));
         t.split = c.split;
         auto sums = [&]() {
             if (c.split < 2) return;
@@ -789,9 +818,18 @@ int gmm_quantize_rows(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t 
     return hipGetLastError() == hipSuccess ? GMM_OK : GMM_E_HIP;
 }
 
+static bool product_sizes_ok(int64_t n, int32_t d, int32_t v) {
+    return n >= 0 && n <= SC_MAX_ROWS && d >= 1 && v >= 1 && d <= QU_MAX_DIM && v <= QU_MAX_CODES;
+}
+
 size_t gmm_quantized_product_workspace_bytes(int64_t n, int32_t d, int32_t v) {
-    if (n < 0 || n > SC_MAX_ROWS || d < 1 || v < 1 || d > QU_MAX_DIM || v > QU_MAX_CODES) return 0;
-    return quant_plan(n, d, v, true, true).bytes;
+    return product_sizes_ok(n, d, v) ? quant_most_bytes(n, d, v) : 0;
+}
+
+size_t gmm_quantized_product_call_workspace_bytes(const int8_t* q, int64_t n, int32_t d, int64_t ldq,
+                                                  const int8_t* w, int32_t v, int64_t ldw) {
+    if (!product_sizes_ok(n, d, v) || ldq < d || ldw < d) return 0;
+    return quant_plan(n, d, v, !quant_direct(q, d, ldq), !quant_direct(w, d, ldw)).bytes;
 }
 
 int gmm_quantized_product(const int8_t* q, int64_t n, int32_t d, int64_t ldq, const float* q_scale,
@@ -806,8 +844,8 @@ int gmm_quantized_product(const int8_t* q, int64_t n, int32_t d, int64_t ldq, co
     if (!workspace || workspace_bytes < plan.bytes || (uintptr_t)workspace % 256 != 0) return GMM_E_WORKSPACE;
     if (n == 0) return GMM_OK;
     const ProductArgs a{q, w, q_scale, w_scale, y, n, ldq, ldw, ldy, d, v};
-    const hipError_t e = dtype == GMM_F32 ? quant_product<float>(a, (char*)workspace, (hipStream_t)stream)
-                                          : quant_product<uint16_t>(a, (char*)workspace, (hipStream_t)stream);
+    const hipError_t e = dtype == GMM_F32 ? quant_product<float>(a, plan, (char*)workspace, (hipStream_t)stream)
+                                          : quant_product<uint16_t>(a, plan, (char*)workspace, (hipStream_t)stream);
     return e == hipSuccess ? GMM_OK : GMM_E_HIP;
 }
 

@@ -60,6 +60,8 @@ lib.gmm_embed_backward.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i32, _f32,
 lib.gmm_quantize_rows.argtypes = [_vp, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _vp]
 lib.gmm_quantized_product_workspace_bytes.argtypes = [_i64, _i32, _i32]
 lib.gmm_quantized_product_workspace_bytes.restype = _sz
+lib.gmm_quantized_product_call_workspace_bytes.argtypes = [_vp, _i64, _i32, _i64, _vp, _i32, _i64]
+lib.gmm_quantized_product_call_workspace_bytes.restype = _sz
 lib.gmm_quantized_product.argtypes = [_vp, _i64, _i32, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _i32,
                                       _vp, _sz, _vp]
 lib.gmm_beam_step_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32]
@@ -626,7 +628,8 @@ def quantized_product(q, q_scale, weight, weight_scale, dtype=torch.bfloat16, ou
     dev = q.device
     qs = _row(q_scale, n, "q_scale", torch.float32, dev)
     wsc = _row(weight_scale, v, "weight_scale", torch.float32, dev)
-    ws, nb = _scratch_or_none(lib.gmm_quantized_product_workspace_bytes(n, d, v), ws, dev)
+    need = lib.gmm_quantized_product_call_workspace_bytes(q.data_ptr(), n, d, ldq, weight.data_ptr(), v, ldw)
+    ws, nb = _scratch_or_none(need, ws, dev)
     if out is None:
         out, ldy = torch.empty((n, v), dtype=dtype, device=dev), v
     elif tuple(out.shape) != (n, v) or out.dtype != dtype or out.device != dev:

@@ -388,12 +388,15 @@ int gmm_quantize_rows(const void* x, int64_t n, int32_t d, int64_t ldx, int32_t 
  * (fp32 or bf16). y must not overlap the operands. With w the codes' quantised rows this is the
  * head's logits in 8 bits, read by gmm_logits_score and gmm_beam_step. Any alignment; offsets are
  * 64-bit. n may be 0; n <= 2^40, d < 2^17, v <= 2^22 (GMM_E_UNSUPPORTED beyond). The workspace
- * (device, 256-byte aligned) has gmm_quantized_product_workspace_bytes bytes (0: invalid or
- * unsupported sizes); it is bounded in n. Operands that are 16-byte aligned with a leading dimension
- * that is a multiple of 16 and d a multiple of 128 are read in place; others too where few rows or
- * codes make that faster, and are laid out in the workspace first where it is not. Rows that are not
- * 4-byte aligned are read by the aligned words that hold their bytes. */
+ * (device, 256-byte aligned) has gmm_quantized_product_workspace_bytes bytes, enough for any operands,
+ * or gmm_quantized_product_call_workspace_bytes bytes, what these operands need (nothing for those that
+ * are read in place); 0: invalid or unsupported sizes. Both are bounded in n. Operands that are 16-byte
+ * aligned with a leading dimension that is a multiple of 16 and d a multiple of 128 are read in place;
+ * others too where few rows or codes make that faster, and are laid out in the workspace first where
+ * it is not. Rows that are not 4-byte aligned are read by the aligned words that hold their bytes. */
 size_t gmm_quantized_product_workspace_bytes(int64_t n, int32_t d, int32_t v);
+size_t gmm_quantized_product_call_workspace_bytes(const int8_t* q, int64_t n, int32_t d, int64_t ldq,
+                                                  const int8_t* w, int32_t v, int64_t ldw);
 int gmm_quantized_product(const int8_t* q, int64_t n, int32_t d, int64_t ldq, const float* q_scale,
                           const int8_t* w, int32_t v, int64_t ldw, const float* w_scale, void* y,
                           int64_t ldy, int32_t dtype, void* workspace, size_t workspace_bytes,
