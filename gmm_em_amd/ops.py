@@ -722,7 +722,8 @@ def beam_reorder(state, parent, w: int, dim: int = 0, out=None):
     """
     if not state.is_cuda:
         raise ValueError("state must be a device tensor")
-    if state.is_complex() or state.is_quantized or state.layout is not torch.strided:
+    # (a view that stands for the negated values of its memory is none: bytes are moved)
+    if state.is_complex() or state.is_quantized or state.layout is not torch.strided or state.is_neg():
         raise TypeError("state must be a plain strided tensor")
     dims = state.dim()
     if not -dims <= dim < dims:
@@ -744,7 +745,7 @@ def beam_reorder(state, parent, w: int, dim: int = 0, out=None):
     new = out is None
     if new:
         out = state.new_empty(shape)
-    elif list(out.shape) != shape or out.dtype != state.dtype or out.device != dev:
+    elif list(out.shape) != shape or out.dtype != state.dtype or out.device != dev or out.is_neg():
         raise ValueError("out must have state's shape with B * m rows, its type and device")
     if out.numel() == 0:
         return out
