@@ -16,10 +16,10 @@
 // kernel. Up to 4096 rows are sorted by one workgroup (k_embed_sort); up to 1024 take one launch
 // instead of all this (k_embed_few): the first row of a code adds the others.
 // The sum is bound by reading the rows and writing the table, everything else by the latency of
-// short kernels. 65536 x 768 bf16 against 16384 codes of uneven frequency, 52 us a call: counts 2 x
-// 3, places 2 x 6.5, sums 25 (126 MB, 5.0 TB/s), join 10. 4096 rows 27 (sorted by four launches and their
-// codes without rows found by the sum, 34), 2048 rows 27 (sort 13 beside the zeros, sums 6, join 8), 1024
-// rows 11.
+// short kernels. 65536 x 768 bf16 against 16384 codes of uneven frequency, 57 us a call (52 where the caches
+// still hold part of the rows): counts 2 x 3, places 2 x 6.5, sums 25 (126 MB, 5.0 TB/s), join 9.5. 4096 rows 27
+// (sorted by four launches and their codes without rows found by the sum, 34), 2048 rows 27 (sort 13 beside the
+// zeros, sums 6, join 8), 1024 rows 10.5.
 // Not kept: a bitmap of the codes that occur (its atomics took 65 us), segments joined by a
 // workgroup each (19 us).
 #include <hip/hip_runtime.h>
@@ -350,7 +350,8 @@ __global__ __launch_bounds__(ES_NT) void k_embed_sort(SortArgs p, EmbedGradArgs 
     }
 }
 
-// acc += EG_U rows of this lane's VE dims; rows from `cnt` on add nothing.
+// Loads rows j0 .. j0 + EG_U - 1 of a list of cnt > j0, this lane's VE dims of each. Places from cnt on hold the
+// list's last row once more (no branch around a load): the caller leaves them out.
 template <typename T, typename F>
 __device__ __forceinline__ void embed_rows(const EmbedGradArgs& p, bool has, int k, int j0, int cnt, F row_of,
                                            Raw16* r) {

@@ -6,14 +6,15 @@
 //
 // k_quant_few: up to 16 rows. The product is the reading of w: 16 weight rows by 16 rows of q
 // per matrix instruction, both straight from memory, the contracted axis split over the
-// waves and joined in LDS. 16 x 4096 x 16384 in 17.8 us (67 MB of w: 3.8 TB/s).
+// waves and joined in LDS. 16 x 4096 x 16384 in 17.8 to 19.7 us (67 MB of w: 3.4 TB/s and more).
 // k_quant_tiles: more rows, by the tiles of gmm_gemm.h (codes are the tile rows, turned so that a
 // lane has eight neighbouring codes of a row to write: 16 bytes of bf16). Operands whose rows
 // are not 16-byte aligned, or not whole steps of 128 long, are laid out in panels first.
-// 8192^3 in 470 us (2340 TOP/s) and 8192 x 4096 x 16384 in 465 (bf16 results); with operands of
-// zeros 8192^3 takes 344: on other numbers the chip's power sets the pace. Not kept: stores of four
-// codes (500 and, 8192 x 768 x 16384, 164 against 136), blocks of 32 x 32 (508 at 8192^3), four
-// waves of 128 x 128 (770), stores past the caches (607).
+// 8192^3 in 400 us (2750 TOP/s; another card 470), with operands of zeros 330: on other numbers the chip's
+// power sets part of the pace. 8192 x 4096 x 16384 in 457 (bf16 results; 427 the kernel by itself), zeros 422.
+// Not kept, on the card that took 470: stores of four codes (8192 x 4096 x 16384 500 against 465 and
+// 8192 x 768 x 16384 164 against 136), blocks of 32 x 32 (508 at 8192^3), four waves of 128 x 128 (770), stores
+// past the caches (607).
 // k_quant_odd: tiles of 64 x 64 read as the rows lie, where the layout would cost more than it saves
 // (odd rows in few tiles): 20 x 8191 x 32767 in 69 us, laid out 200; 64 x 8191 x 32767 86, 197;
 // 64 x 1003 x 32767 16, 26.
@@ -140,7 +141,8 @@ struct QuantScale {
 };
 
 // LPR lanes per row, which holds it: at most 16 LPR U values.
-// 8192 x 4096 in 28 us (bf16, 3.6 TB/s) and 30 us (fp32, 5.6 TB/s).
+// 8192 x 4096 in 31 us (bf16, 3.3 TB/s) and 34 us (fp32, 5.0 TB/s); 28 and 29 where the caches still hold part of
+// the rows, and 36 (bf16) for the kernel that follows a product of 450 us.
 template <typename T, int LPR, int U>
 __global__ __launch_bounds__(256) void k_quant_rows(QuantArgs p) {
     constexpr int RPW = 64 / LPR;
