@@ -5,7 +5,7 @@ The logits are small whole numbers and their order is given by (value, index): t
 for equality with a stable sort. Log-probabilities: l - max is exact; the sum of v exponentials, each off by 2^-22 of
 itself at most (the hardware's base 2 exponential and the factor before it, for differences below 16), in any order,
 is off by (v 2^-24 + 2^-22) of itself, its logarithm by as much and by 2^-22 of the logarithm, and the result is
-rounded twice; the sum of v = 4000 equal values is exact, so the bound is far from met.
+rounded twice.
 """
 import pytest
 
